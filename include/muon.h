@@ -49,6 +49,7 @@
 extern "C" {
 #endif
 
+/* Raised when a declaration below changes; functions added beside them keep it. */
 #define MUON_ABI_VERSION 13
 
 typedef enum muon_status {
@@ -455,6 +456,128 @@ int muon_probe_nt_out_bf16(const void* P, const void* Q, void* C, void* CT, int 
 int muon_step_noalloc(const muon_matrix_desc* desc, const muon_plan_opts* opts, void* param,
                       const void* grad, float* momentum, float lr, float beta, float wd,
                       int ns_steps, const float* coeffs, void* stream);
+
+/*
+ * Operators of a mixture-of-experts layer: the gradients that muon_step takes
+ * for the experts' matrices come out of these.  T tokens choose k of E experts
+ * each; n = T k rows, sorted by expert, hold one token each; rows
+ * [offsets[e], offsets[e + 1]) are those of expert e.
+ *
+ * For all of them: arrays are dense row-major device memory in `dtype`
+ * (MUON_F32 or MUON_BF16; weights, their gradients and scales are typed as
+ * declared), at any alignment of the element type; sums, statistics and products are
+ * fp32, rounded once to `dtype` at the end (nearest even).  A call enqueues
+ * kernels only (no allocation, copy or memory set) on `stream` and returns
+ * without waiting, so it can be captured into a graph; outputs are written in
+ * whole.  Two calls that share a workspace must be ordered.  Equal inputs give
+ * equal bits.  Sizes of zero rows or tokens are valid and need no pointers,
+ * except offsets.  Errors: EINVAL (NULL pointer, negative or inconsistent
+ * size, a workspace that is missing, too small or not 16-byte aligned), EUNSUPPORTED (dtype, kind, E
+ * over 1024, k over 64, T k >= 2^31, no gfx950 device), EHIP.
+ */
+
+/* How a checkpoint holds a value in 8 bits: in blocks of 32 columns of a row,
+ * q * 2^(scale - 127).  MUON_INT8: q in [-127, 127], the scale 2^-6 of the
+ * power of two at or below the block's largest magnitude.  MUON_E4M3: q an
+ * 8-bit float (4 exponent, 3 mantissa bits, largest 448), the smallest scale
+ * for which no value exceeds 448.  Scales are 2^-126 at least.  A block with
+ * an infinity or NaN gets scale code 255 and restores to NaN in whole. */
+typedef enum muon_kind { MUON_INT8 = 0, MUON_E4M3 = 1 } muon_kind;
+
+/*
+ * Router.  logits: T x E.  Each token takes its k largest logits, ties to the
+ * lowest expert; a NaN logit counts as -inf, +inf as the largest fp32.  A
+ * logit of -inf is never taken: where a token has fewer than k others, the
+ * rest of its choices are expert -1, slot -1, weight 0.
+ *   weights  T x k: softmax over the taken logits (normalize != 0), or the
+ *            softmax over all E at the taken ones
+ *   chosen   T x k experts, largest logit first
+ *   slots    T x k: the row of each choice; rows are sorted by expert, within
+ *            an expert by token
+ *   rows     T k: the token of each row, -1 from offsets[E] on
+ *   offsets  E + 1
+ * muon_route_workspace: bytes of device workspace a call needs (0 for small
+ * ones; workspace may then be NULL).
+ * muon_route_backward: dlogits (T x E, dtype) from dweights (T x k) and the
+ * weights and choices muon_route gave for these logits.
+ */
+int muon_route_workspace(int64_t tokens, int experts, uint64_t* bytes);
+int muon_route(const void* logits, int dtype, int64_t tokens, int experts, int k, int normalize,
+               float* weights, int32_t* chosen, int32_t* slots, int32_t* rows, int32_t* offsets,
+               void* workspace, uint64_t workspace_bytes, void* stream);
+int muon_route_backward(const float* dweights, const void* logits, const float* weights,
+                        const int32_t* chosen, int dtype, int64_t tokens, int experts, int k,
+                        int normalize, void* dlogits, void* stream);
+
+/*
+ * Products grouped by expert; w: E x outer x inner, W_e its matrices.
+ *   muon_grouped_matmul       y[r] = x[rows[r]] W_e^T for the rows r of expert
+ *                             e (n x outer); x has x_rows rows of inner.  rows
+ *                             NULL: x[r], and x_rows = n.
+ *   muon_grouped_input_grad   dx[r] = dy[r] W_e (n x inner), dy n x outer
+ *   muon_grouped_weight_grad  dw_e = sum over the rows r of expert e of
+ *                             dy[r]^T x[rows[r]] (E x outer x inner; zero for
+ *                             an expert without rows).  x dense (q, scale
+ *                             NULL), or NULL with its checkpoint q, scale, kind.
+ * Rows from offsets[E] on are zero in y and dx and count for no dw.  The
+ * device arrays are not trusted: offsets are read as their running maximum,
+ * within [0, n] and from 0 on; an entry of rows outside [0, x_rows) is a row
+ * of zeros.  Limits: inner and outer < 2^24, E <= 1024, n and x_rows < 2^31.
+ * muon_grouped_weight_grad_workspace: bytes of workspace its call needs
+ * (checkpoint: q is given).
+ */
+int muon_grouped_matmul(const void* x, const void* w, const int32_t* offsets, const int32_t* rows,
+                        int dtype, int64_t n, int64_t x_rows, int experts, int64_t outer,
+                        int64_t inner, void* y, void* stream);
+int muon_grouped_input_grad(const void* dy, const void* w, const int32_t* offsets, int dtype,
+                            int64_t n, int experts, int64_t outer, int64_t inner, void* dx,
+                            void* stream);
+int muon_grouped_weight_grad_workspace(int dtype, int64_t n, int64_t x_rows, int experts,
+                                       int64_t outer, int64_t inner, int checkpoint,
+                                       uint64_t* bytes);
+int muon_grouped_weight_grad(const void* dy, const void* x, const void* q, const uint8_t* scale,
+                             int kind, const int32_t* offsets, const int32_t* rows, int dtype,
+                             int64_t n, int64_t x_rows, int experts, int64_t outer, int64_t inner,
+                             void* dw, void* workspace, uint64_t workspace_bytes, void* stream);
+
+/*
+ * Rows back to their tokens.  y: T k x cols, the rows' outputs; slots and
+ * weights as muon_route gives them.
+ *   muon_combine           out[t] = sum_j weights[t][j] y[slots[t][j]]  (T x cols)
+ *   muon_combine_backward  dy[slots[t][j]] = weights[t][j] dout[t], rows from
+ *                          offsets[E] on zero; dweights[t][j] = <y[slots[t][j]],
+ *                          dout[t]>.  Every row below offsets[E] must have its slot
+ *                          (as muon_route's have).
+ * A slot outside [0, T k) contributes nothing and gets gradient 0.
+ */
+int muon_combine(const void* y, const int32_t* slots, const float* weights, int dtype,
+                 int64_t tokens, int k, int64_t cols, void* out, void* stream);
+int muon_combine_backward(const void* dout, const void* y, const int32_t* slots,
+                          const float* weights, const int32_t* offsets, int dtype, int64_t tokens,
+                          int k, int experts, int64_t cols, void* dy, float* dweights, void* stream);
+
+/*
+ * Activations kept in 8 bits (muon_kind).  x: rows x cols; q: rows x cols
+ * bytes; scale: rows x ceil(cols / 32) codes.
+ *   muon_checkpoint  x -> q, scale;   muon_restore  q, scale -> x
+ */
+int muon_checkpoint(const void* x, int dtype, int64_t rows, int64_t cols, int kind, void* q,
+                    uint8_t* scale, void* stream);
+int muon_restore(const void* q, const uint8_t* scale, int kind, int64_t rows, int64_t cols,
+                 int dtype, void* x, void* stream);
+
+/*
+ * Gated activation.  gu: rows x 2 cols, [g | u]; h = g sigmoid(g) u (rows x
+ * cols).  q, scale non-NULL: also the checkpoint of gu, from the same pass
+ * where cols is a multiple of 32.
+ * muon_gated_backward: dgu (rows x 2 cols) from dh, and h again, from gu (q,
+ * scale NULL) or from its checkpoint (gu NULL).
+ */
+int muon_gated(const void* gu, int dtype, int64_t rows, int64_t cols, int kind, void* h, void* q,
+               uint8_t* scale, void* stream);
+int muon_gated_backward(const void* dh, const void* gu, const void* q, const uint8_t* scale,
+                        int kind, int dtype, int64_t rows, int64_t cols, void* dgu, void* h,
+                        void* stream);
 
 /* MUON_ABI_VERSION of the library. */
 int muon_abi_version(void);

@@ -8,14 +8,30 @@ update runs in the library's HIP kernels; there is no fallback path.
 
     plan = MuonPlan([(3072, 1024), (1024, 1024)], "bf16")
     plan.step(params, grads, momenta, lr=0.02, beta=0.95, wd=0.01)
+
+The operators of a mixture-of-experts layer, whose matrices' gradients such a
+plan takes, are in experts.py and reached as attributes of this package.
 """
 import ctypes
+import importlib
 
 from . import _lib as L
 from ._lib import MuonError  # noqa: F401
 
+# the operators of experts.py, which imports torch: loaded on first use
+_EXPERTS = ["route", "route_backward", "Routing", "grouped_matmul", "grouped_input_grad", "grouped_weight_grad",
+            "combine", "combine_backward", "checkpoint", "restore", "Checkpoint", "gated", "gated_backward"]
+
 __all__ = ["MuonPlan", "AdamWPlan", "MuonError", "library_path", "assign_owners",
-           "probe_mfma_bf16", "probe_nt_bf16", "probe_nt_out_bf16", "probe_hbm_copy", "step_noalloc"]
+           "probe_mfma_bf16", "probe_nt_bf16", "probe_nt_out_bf16", "probe_hbm_copy", "step_noalloc", *_EXPERTS]
+
+
+def __getattr__(name):
+    if name not in _EXPERTS:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    experts = importlib.import_module(__name__ + ".experts")
+    globals().update({n: getattr(experts, n) for n in _EXPERTS})
+    return globals()[name]
 
 
 def library_path():

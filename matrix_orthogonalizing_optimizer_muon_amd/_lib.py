@@ -10,6 +10,7 @@ LIB_PATH = os.path.join(HERE, "libmuon_mi355x.so")
 
 MUON_OK, MUON_EINVAL, MUON_EUNSUPPORTED, MUON_ENOMEM, MUON_EHIP, MUON_ESTATE = range(6)
 MUON_F32, MUON_BF16 = 0, 1
+MUON_INT8, MUON_E4M3 = 0, 1
 PRECISION = {"auto": 0, "fp32": 1, "bf16": 2}
 FORM = {"auto": 0, "direct": 1, "gram": 2}
 TUNE = {"off": 0, "once": 1, "force": 2}
@@ -55,6 +56,8 @@ class LaunchInterval(ctypes.Structure):
 
 _PP = ctypes.POINTER(ctypes.c_void_p)
 _FP = ctypes.POINTER(ctypes.c_float)
+_U64P = ctypes.POINTER(ctypes.c_uint64)
+_P, _I, _N, _U64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint64
 
 # name -> (restype, argtypes); must list every function include/muon.h declares.
 PROTOTYPES = {
@@ -119,6 +122,19 @@ PROTOTYPES = {
                                           ctypes.c_int64, ctypes.POINTER(ctypes.c_int32),
                                           ctypes.POINTER(ctypes.c_double),
                                           ctypes.POINTER(ctypes.c_int32)]),
+    "muon_route_workspace": (_I, [_N, _I, _U64P]),
+    "muon_route": (_I, [_P, _I, _N, _I, _I, _I, _P, _P, _P, _P, _P, _P, _U64, _P]),
+    "muon_route_backward": (_I, [_P, _P, _P, _P, _I, _N, _I, _I, _I, _P, _P]),
+    "muon_grouped_matmul": (_I, [_P, _P, _P, _P, _I, _N, _N, _I, _N, _N, _P, _P]),
+    "muon_grouped_input_grad": (_I, [_P, _P, _P, _I, _N, _I, _N, _N, _P, _P]),
+    "muon_grouped_weight_grad_workspace": (_I, [_I, _N, _N, _I, _N, _N, _I, _U64P]),
+    "muon_grouped_weight_grad": (_I, [_P, _P, _P, _P, _I, _P, _P, _I, _N, _N, _I, _N, _N, _P, _P, _U64, _P]),
+    "muon_combine": (_I, [_P, _P, _P, _I, _N, _I, _N, _P, _P]),
+    "muon_combine_backward": (_I, [_P, _P, _P, _P, _P, _I, _N, _I, _I, _N, _P, _P, _P]),
+    "muon_checkpoint": (_I, [_P, _I, _N, _N, _I, _P, _P, _P]),
+    "muon_restore": (_I, [_P, _P, _I, _N, _N, _I, _P, _P]),
+    "muon_gated": (_I, [_P, _I, _N, _N, _I, _P, _P, _P, _P]),
+    "muon_gated_backward": (_I, [_P, _P, _P, _P, _I, _I, _N, _N, _P, _P, _P]),
 }
 
 _lib = None

@@ -1,0 +1,469 @@
+// Matrix products grouped by expert: rows sorted by expert times that expert's
+// matrix, and the two gradients.  Row counts live on the device (offsets), so
+// a launch has a block for every tile that could exist and each block looks
+// its expert up; nothing waits for the host.
+//
+//   matmul       y[r]  = sum_i x[rows[r]][i] W_e[o][i]    both k-contiguous
+//   input grad   dx[r] = sum_o dy[r][o] W_e[o][i]         W k-major
+//   weight grad  dW_e[o][i] = sum_r dy[r][o] x[rows[r]][i]   both k-major
+#include <hip/hip_runtime.h>
+
+#include "experts.hpp"
+#include "mfma_nt.hpp"
+
+namespace muon {
+namespace ex {
+
+int restore_rows(const void* q, const uint8_t* scale, int kind, int64_t rows, int64_t cols, int dtype, void* x,
+                 hipStream_t s);
+
+namespace {
+
+using nt::bf16x8_t;
+using nt::f32x16_t;
+using nt::s16x4_t;
+using nt::u32x2_t;
+
+enum Mode { kMatmul = 0, kInputGrad = 1, kWeightGrad = 2 };
+
+struct ProdArgs {
+  const void* p;            // x, dy, dy
+  const void* q;            // W, W, x
+  void* out;
+  const int32_t* offsets;
+  const int32_t* rows;      // gather of x's rows, or null
+  int64_t n, x_rows;
+  int32_t experts;
+  int32_t M, N, K;          // M: weight grad only; K: not in the weight grad
+  int32_t tiles_m, tiles_n; // tiles_m: weight grad only
+};
+
+// Tile t of the rows cut by expert into tiles of 2^SH: expert and rows
+// [begin, end) of the tile, end at most begin + 2^SH.  The rows past the last
+// expert's are cut the same way, as those of expert `experts`.  Offsets are
+// taken as their running maximum in [0, n], so that no input leads out of
+// bounds.  Every wave of a block calls this with the same t; false: no such
+// tile.
+struct RowTile {
+  int e;
+  int64_t begin, end;
+};
+template <int SH>
+__device__ __forceinline__ bool find_tile(const int32_t* __restrict__ offsets, int experts, int n, int64_t t, int lane,
+                                          RowTile& out) {
+  int last = 0;       // end of the experts before this round of 64
+  int64_t seen = 0;   // their tiles
+  for (int e0 = 0; e0 < experts; e0 += 64) {
+    int hi = e0 + lane < experts ? offsets[e0 + lane + 1] : 0;
+    hi = hi > n ? n : hi;
+    hi = wave_scan_max(hi > last ? hi : last, lane);
+    int lo = __shfl_up(hi, 1, 64);
+    if (lane == 0) lo = last;
+    const int tiles = (hi - lo + (1 << SH) - 1) >> SH;
+    const int upto = wave_scan_add(tiles, lane);
+    const uint64_t hit = __ballot(t < seen + upto);
+    if (hit) {
+      const int at = __ffsll((unsigned long long)hit) - 1;
+      const int b = __builtin_amdgcn_readlane(lo, at), e = __builtin_amdgcn_readlane(hi, at);
+      const int before = __builtin_amdgcn_readlane(upto - tiles, at);
+      out.e = e0 + at;
+      out.begin = b + ((t - seen - before) << SH);
+      out.end = out.begin + (1 << SH) < e ? out.begin + (1 << SH) : e;
+      return true;
+    }
+    last = __builtin_amdgcn_readlane(hi, 63);
+    seen += __builtin_amdgcn_readlane(upto, 63);
+  }
+  out.e = experts;
+  out.begin = last + ((t - seen) << SH);
+  out.end = out.begin + (1 << SH) < n ? out.begin + (1 << SH) : n;
+  return out.begin < n;
+}
+
+// Rows [begin, end) of expert e, by the same reading of offsets.
+__device__ __forceinline__ void expert_rows(const int32_t* __restrict__ offsets, int e, int n, int lane, int64_t& begin,
+                                            int64_t& end) {
+  int b = 0, m = 0;   // maxima of offsets[1..e] and of offsets[1..e+1]
+  for (int i = lane; i <= e; i += 64) {
+    const int v = offsets[i + 1];
+    m = v > m ? v : m;
+    if (i < e) b = v > b ? v : b;
+  }
+  b = (int)wave_max((uint32_t)b);
+  m = (int)wave_max((uint32_t)m);
+  begin = b < n ? b : n;
+  end = m < n ? m : n;
+}
+
+// 16 bytes from any address, of which the first cnt elements exist.
+__device__ __forceinline__ u32x4 load16(const bf16_t* p, int cnt) {
+  if (cnt >= 8) return *reinterpret_cast<const u32x4_any*>(p);
+  u32x4 v = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < cnt) v[i / 2] |= (uint32_t)p[i].bits << (16 * (i % 2));
+  return v;
+}
+__device__ __forceinline__ u32x4 load16(const float* p, int cnt) {
+  if (cnt >= 4) return *reinterpret_cast<const u32x4_any*>(p);
+  u32x4 v = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < cnt) v[i] = __float_as_uint(p[i]);
+  return v;
+}
+
+// Tile geometry of one type.  An operand's tile has `B` rows of BK elements
+// (k-contiguous) or BK rows of B elements (k-major), cut into 16-byte chunks.
+template <class T>
+struct Tile;
+template <>
+struct Tile<bf16_t> {
+  static constexpr int B = 128, SH = 7, BK = 64, PER = 8;   // PER: elements a chunk
+  // 128-byte rows of swizzled chunks, as nt::load_frags reads them
+  static __device__ __forceinline__ int at(int r, int c) { return r * 128 + ((c ^ nt::swz<128>(r)) << 4); }
+  // 256-byte rows, as nt::load_frags_qt reads them
+  static __device__ __forceinline__ int at_t(int r, int c) { return r * 256 + ((c ^ nt::swzt(r)) << 4); }
+  static constexpr int BYTES = 128 * 128, BYTES_T = 64 * 256;
+};
+template <>
+struct Tile<float> {
+  static constexpr int B = 64, SH = 6, BK = 32, PER = 4;
+  // rows padded by 16 bytes: 16-byte reads down 8 rows hit 8 bank groups
+  static __device__ __forceinline__ int at(int r, int c) { return r * 144 + (c << 4); }
+  static __device__ __forceinline__ int at_t(int r, int c) { return r * 272 + (c << 4); }
+  static constexpr int BYTES = 64 * 144, BYTES_T = 32 * 272;
+};
+
+// One operand's way from memory to its tile through registers: any alignment,
+// any length, rows that do not exist read as zero.
+template <class T, bool KM>
+struct Stager {
+  using G = Tile<T>;
+  static constexpr int CPR = KM ? G::B / G::PER : G::BK / G::PER;   // chunks a row
+  static constexpr int ROWS = KM ? G::BK : G::B;
+  static constexpr int NC = ROWS * CPR / 256;                       // chunks a thread
+  const T* base;
+  const int32_t* gather;
+  int64_t row0, rows, src_rows;   // first source row, rows from there on, rows that gather may name
+  int64_t ld;
+  int32_t col0, cols;             // k-major: first column, row length; else: row length
+  int64_t idx[NC];                // k-contiguous: source row of each chunk (-1: none)
+  u32x4 v[NC];
+
+  __device__ __forceinline__ int64_t source(int64_t r) const {
+    if (r >= rows) return -1;
+    if (!gather) return row0 + r;
+    const int32_t g = gather[row0 + r];
+    return g >= 0 && g < src_rows ? g : -1;
+  }
+  __device__ __forceinline__ void init(const void* b, const int32_t* g, int64_t r0, int64_t n_rows, int64_t sr,
+                                       int32_t c0, int32_t n_cols) {
+    base = static_cast<const T*>(b);
+    gather = g;
+    row0 = r0;
+    rows = n_rows;
+    src_rows = sr;
+    ld = n_cols;
+    col0 = c0;
+    cols = n_cols;
+    if (!KM) {
+#pragma unroll
+      for (int u = 0; u < NC; ++u) idx[u] = source((u * 256 + (int)threadIdx.x) / CPR);
+    }
+  }
+  __device__ __forceinline__ void fetch(int64_t k0) {
+#pragma unroll
+    for (int u = 0; u < NC; ++u) {
+      const int id = u * 256 + (int)threadIdx.x, r = id / CPR, c = id % CPR;
+      const int64_t src = KM ? source(k0 + r) : idx[u];
+      const int64_t col = (KM ? (int64_t)col0 : k0) + c * G::PER;
+      const int64_t left = cols - col;
+      v[u] = src < 0 || left <= 0 ? u32x4{0u, 0u, 0u, 0u}
+                                  : load16(base + src * ld + col, left < G::PER ? (int)left : G::PER);
+    }
+  }
+  __device__ __forceinline__ void commit(char* lds) const {
+#pragma unroll
+    for (int u = 0; u < NC; ++u) {
+      const int id = u * 256 + (int)threadIdx.x, r = id / CPR, c = id % CPR;
+      *reinterpret_cast<u32x4*>(lds + (KM ? G::at_t(r, c) : G::at(r, c))) = v[u];
+    }
+  }
+};
+
+// MFMA operands of one k-group (16 k of bf16, 8 of fp32) for the NT 32-wide
+// slabs from `first` on.  Both operands of a product take the k values of a
+// group in the same order, so their order does not matter.
+template <bool KM, int NT>
+__device__ __forceinline__ void fragments(u32x4 (&f)[NT], const char* lds, int first, int kg, int lane, bf16_t) {
+  if constexpr (!KM) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      f[j] = *reinterpret_cast<const u32x4*>(lds + Tile<bf16_t>::at(first + 32 * j + (lane & 31), kg * 2 + (lane >> 5)));
+  } else {
+    // nt::load_frags_qt describes the transposing read
+    const int g = lane >> 4, sl = lane & 15;
+    const int k = kg * 16 + 8 * (g >> 1) + (sl >> 2);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int byte = (first + 32 * j + (g & 1) * 16 + 4 * (sl & 3)) * 2;
+      const int a = ((byte >> 4) ^ nt::swzt(k)) * 16 + (byte & 15);
+      const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MUON_LDS s16x4_t*)(lds + k * 256 + a));
+      const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MUON_LDS s16x4_t*)(lds + (k + 4) * 256 + a));
+      const u32x2_t l2 = __builtin_bit_cast(u32x2_t, lo), h2 = __builtin_bit_cast(u32x2_t, hi);
+      f[j] = u32x4{l2[0], l2[1], h2[0], h2[1]};
+    }
+  }
+}
+template <bool KM, int NT>
+__device__ __forceinline__ void fragments(u32x4 (&f)[NT], const char* lds, int first, int kg, int lane, float) {
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int x = first + 32 * j + (lane & 31), k = kg * 8 + 4 * (lane >> 5);
+    if constexpr (!KM) {
+      f[j] = *reinterpret_cast<const u32x4*>(lds + Tile<float>::at(x, k / 4));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        f[j][i] = *reinterpret_cast<const uint32_t*>(lds + Tile<float>::at_t(k + i, x / 4) + (x & 3) * 4);
+    }
+  }
+}
+
+// (Q, P) operands: the accumulator is the transposed tile, so lane l holds
+// row l % 32 of the output and registers 4 g + 0..3 its columns 8 g + 4 (l / 32) + 0..3.
+__device__ __forceinline__ f32x16_t multiply(u32x4 q, u32x4 p, f32x16_t acc, bf16_t) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, q), __builtin_bit_cast(bf16x8_t, p), acc,
+                                                 0, 0, 0);
+}
+__device__ __forceinline__ f32x16_t multiply(u32x4 q, u32x4 p, f32x16_t acc, float) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(q[i]), __uint_as_float(p[i]), acc, 0, 0, 0);
+  return acc;
+}
+
+__device__ __forceinline__ void store4(bf16_t* p, int cnt, const float* v) {
+  if (cnt >= 4) {
+    *reinterpret_cast<u32x2_any*>(p) = u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < cnt) store1(p + i, v[i]);
+  }
+}
+__device__ __forceinline__ void store4(float* p, int cnt, const float* v) {
+  if (cnt >= 4) {
+    *reinterpret_cast<u32x4_any*>(p) =
+        u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < cnt) p[i] = v[i];
+  }
+}
+
+// One output tile per block of 4 waves (2 x 2), two LDS stages: the next
+// k-tile's loads are in flight while this one is multiplied.
+template <class T, int MODE>
+__global__ __launch_bounds__(256) void k_product(ProdArgs a) {
+  using G = Tile<T>;
+  constexpr bool PT = MODE == kWeightGrad, QT = MODE != kMatmul;
+  constexpr int PB = PT ? G::BYTES_T : G::BYTES, QB = QT ? G::BYTES_T : G::BYTES;
+  constexpr int W = G::B / 2, NT = W / 32;
+  __shared__ __attribute__((aligned(16))) char lds[2 * (PB + QB)];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, wy = w >> 1, wx = w & 1;
+  const int64_t t = blockIdx.x;
+  const int tn = (int)(t % a.tiles_n);
+  const int64_t tm = t / a.tiles_n;
+  const int n0 = tn * G::B;
+  T* out = static_cast<T*>(a.out);
+  int64_t out_row;   // first output row of the tile
+  int m_left, K;
+  Stager<T, PT> sp;
+  Stager<T, QT> sq;
+  if constexpr (MODE == kWeightGrad) {
+    const int e = (int)(tm / a.tiles_m), m0 = (int)(tm % a.tiles_m) * G::B;
+    int64_t b, end;
+    expert_rows(a.offsets, e, (int)a.n, lane, b, end);
+    K = (int)(end - b);
+    m_left = a.M - m0;
+    out_row = (int64_t)e * a.M + m0;
+    sp.init(a.p, nullptr, b, K, 0, m0, a.M);
+    sq.init(a.q, a.rows, b, K, a.x_rows, n0, a.N);
+  } else {
+    RowTile rt;
+    if (!find_tile<G::SH>(a.offsets, a.experts, (int)a.n, tm, lane, rt)) return;
+    m_left = (int)(rt.end - rt.begin);
+    out_row = rt.begin;
+    K = rt.e < a.experts ? a.K : 0;
+    sp.init(a.p, a.rows, rt.begin, K ? m_left : 0, a.x_rows, 0, a.K);
+    const int64_t w0 = (int64_t)(K ? rt.e : 0) * a.N * a.K;
+    if constexpr (QT) sq.init(static_cast<const T*>(a.q) + w0, nullptr, 0, K, 0, n0, a.N);
+    else sq.init(static_cast<const T*>(a.q) + w0, nullptr, n0, a.N - n0, 0, 0, a.K);
+  }
+  f32x16_t acc[NT][NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  const int nk = (K + G::BK - 1) / G::BK;
+  if (nk) {
+    sp.fetch(0);
+    sq.fetch(0);
+    sp.commit(lds);
+    sq.commit(lds + PB);
+  }
+  for (int kt = 0; kt < nk; ++kt) {
+    __syncthreads();
+    const char* st = lds + (kt & 1) * (PB + QB);
+    char* next = lds + (~kt & 1) * (PB + QB);
+    if (kt + 1 < nk) {
+      sp.fetch((int64_t)(kt + 1) * G::BK);
+      sq.fetch((int64_t)(kt + 1) * G::BK);
+    }
+#pragma unroll
+    for (int kg = 0; kg < 4; ++kg) {
+      u32x4 fp[NT], fq[NT];
+      fragments<PT, NT>(fp, st, wy * W, kg, lane, T());
+      fragments<QT, NT>(fq, st + PB, wx * W, kg, lane, T());
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = multiply(fq[j], fp[i], acc[i][j], T());
+    }
+    if (kt + 1 < nk) {
+      sp.commit(next);
+      sq.commit(next + PB);
+    }
+  }
+  const int64_t ldo = a.N;
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int r = wy * W + 32 * i + (lane & 31);
+    if (r < m_left) {
+      T* row = out + (out_row + r) * ldo;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int c = n0 + wx * W + 32 * j + 8 * g + 4 * (lane >> 5);
+          const float v[4] = {acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+          store4(row + c, a.N - c, v);
+        }
+    }
+  }
+}
+
+// --------------------------------------------------------------------- host
+
+constexpr int64_t kMaxSide = (int64_t(1) << 24) - 1;
+
+int check_product(int dtype, int64_t n, int64_t x_rows, int experts, int64_t outer, int64_t inner) {
+  if (!good_dtype(dtype)) return fail(MUON_EUNSUPPORTED, "unsupported dtype");
+  if (n < 0 || x_rows < 0 || experts < 1 || outer < 1 || inner < 1)
+    return fail(MUON_EINVAL, "rows must be >= 0; experts, outer and inner >= 1");
+  if (experts > kMaxExperts) return fail(MUON_EUNSUPPORTED, "more than 1024 experts");
+  if (n > kMaxCount || x_rows > kMaxCount) return fail(MUON_EUNSUPPORTED, "2^31 rows or more");
+  if (outer > kMaxSide || inner > kMaxSide) return fail(MUON_EUNSUPPORTED, "a matrix side of 2^24 or more");
+  return MUON_OK;
+}
+
+int64_t side(int dtype) { return dtype == MUON_BF16 ? Tile<bf16_t>::B : Tile<float>::B; }
+
+// Row tiles that n rows of `experts` experts (and the rows past them) can make.
+int64_t row_tiles(int64_t n, int experts, int64_t b) {
+  const int64_t cut = n < experts + 1 ? n : experts + 1;
+  return n / b + cut;
+}
+
+template <int MODE>
+int launch_product(ProdArgs a, int dtype, int64_t tiles_m, hipStream_t s) {
+  a.tiles_n = (int32_t)ceil_div(a.N, side(dtype));
+  const int64_t blocks = tiles_m * a.tiles_n;
+  if (blocks > kMaxCount) return fail(MUON_EUNSUPPORTED, "more than 2^31 output tiles");
+  if (dtype == MUON_BF16) hipLaunchKernelGGL((k_product<bf16_t, MODE>), dim3((uint32_t)blocks), dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_product<float, MODE>), dim3((uint32_t)blocks), dim3(256), 0, s, a);
+  return launch_status("grouped product launch");
+}
+
+// Workspace of the weight gradient: a checkpoint's rows as dense values.
+uint64_t weight_grad_bytes(int dtype, int64_t x_rows, int64_t inner, bool kept) {
+  return kept ? (uint64_t)x_rows * inner * (dtype == MUON_BF16 ? 2 : 4) : 0;
+}
+
+}  // namespace
+}  // namespace ex
+}  // namespace muon
+
+using namespace muon::ex;
+
+extern "C" {
+
+int muon_grouped_matmul(const void* x, const void* w, const int32_t* offsets, const int32_t* rows, int dtype,
+                        int64_t n, int64_t x_rows, int experts, int64_t outer, int64_t inner, void* y, void* stream) {
+  muon::report_error(MUON_OK, "");
+  int rc;
+  if ((rc = check_product(dtype, n, x_rows, experts, outer, inner))) return rc;
+  if (n > 0 && !rows && x_rows != n) return fail(MUON_EINVAL, "x_rows must be n where rows is NULL");
+  if (n == 0) return MUON_OK;
+  if ((!x && x_rows) || !w || !offsets || !y) return fail(MUON_EINVAL, "NULL pointer");
+  if ((rc = check_device())) return rc;
+  ProdArgs a = {x, w, y, offsets, rows, n, x_rows, experts, 0, (int32_t)outer, (int32_t)inner, 0, 0};
+  return launch_product<kMatmul>(a, dtype, row_tiles(n, experts, side(dtype)), static_cast<hipStream_t>(stream));
+}
+
+int muon_grouped_input_grad(const void* dy, const void* w, const int32_t* offsets, int dtype, int64_t n, int experts,
+                            int64_t outer, int64_t inner, void* dx, void* stream) {
+  muon::report_error(MUON_OK, "");
+  int rc;
+  if ((rc = check_product(dtype, n, n, experts, outer, inner))) return rc;
+  if (n == 0) return MUON_OK;
+  if (!dy || !w || !offsets || !dx) return fail(MUON_EINVAL, "NULL pointer");
+  if ((rc = check_device())) return rc;
+  ProdArgs a = {dy, w, dx, offsets, nullptr, n, n, experts, 0, (int32_t)inner, (int32_t)outer, 0, 0};
+  return launch_product<kInputGrad>(a, dtype, row_tiles(n, experts, side(dtype)), static_cast<hipStream_t>(stream));
+}
+
+int muon_grouped_weight_grad_workspace(int dtype, int64_t n, int64_t x_rows, int experts, int64_t outer,
+                                       int64_t inner, int checkpoint, uint64_t* bytes) {
+  muon::report_error(MUON_OK, "");
+  if (!bytes) return fail(MUON_EINVAL, "NULL bytes");
+  const int rc = check_product(dtype, n, x_rows, experts, outer, inner);
+  if (rc) return rc;
+  *bytes = weight_grad_bytes(dtype, x_rows, inner, checkpoint != 0);
+  return MUON_OK;
+}
+
+int muon_grouped_weight_grad(const void* dy, const void* x, const void* q, const uint8_t* scale, int kind,
+                             const int32_t* offsets, const int32_t* rows, int dtype, int64_t n, int64_t x_rows,
+                             int experts, int64_t outer, int64_t inner, void* dw, void* workspace,
+                             uint64_t workspace_bytes, void* stream) {
+  muon::report_error(MUON_OK, "");
+  int rc;
+  const bool kept = q || scale;
+  if ((rc = check_product(dtype, n, x_rows, experts, outer, inner))) return rc;
+  if (n > 0 && !rows && x_rows != n) return fail(MUON_EINVAL, "x_rows must be n where rows is NULL");
+  if (kept && x) return fail(MUON_EINVAL, "either x or its checkpoint, not both");
+  if (kept && kind != MUON_INT8 && kind != MUON_E4M3) return fail(MUON_EUNSUPPORTED, "kind must be MUON_INT8 or MUON_E4M3");
+  if (!offsets || !dw || (n > 0 && !dy) || (n > 0 && x_rows > 0 && (kept ? (!q || !scale) : !x)))
+    return fail(MUON_EINVAL, "NULL pointer");
+  const uint64_t need = weight_grad_bytes(dtype, x_rows, inner, kept);
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(MUON_EINVAL, "workspace of " + std::to_string(need) + " bytes needed");
+  if (need && (reinterpret_cast<uintptr_t>(workspace) & 15)) return fail(MUON_EINVAL, "workspace must be 16-byte aligned");
+  if ((rc = check_device())) return rc;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (kept) {
+    if ((rc = restore_rows(q, scale, kind, x_rows, inner, dtype, workspace, s))) return rc;
+    x = workspace;
+  }
+  ProdArgs a = {dy, x, dw, offsets, rows, n, x_rows, experts, (int32_t)outer, (int32_t)inner, 0, 0, 0};
+  a.tiles_m = (int32_t)ceil_div(outer, side(dtype));
+  return launch_product<kWeightGrad>(a, dtype, (int64_t)experts * a.tiles_m, s);
+}
+
+}  // extern "C"
