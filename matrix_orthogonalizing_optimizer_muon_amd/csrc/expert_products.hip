@@ -8,6 +8,7 @@
 //   weight grad  dW_e[o][i] = sum_r dy[r][o] x[rows[r]][i]   both k-major
 #include <hip/hip_runtime.h>
 
+#include "expert_mfma.hpp"
 #include "experts.hpp"
 #include "mfma_nt.hpp"
 
@@ -358,6 +359,177 @@ __global__ __launch_bounds__(256) void k_product(ProdArgs a) {
   }
 }
 
+// ------------------------------------------------------------- large tiles
+
+// Which tile a block of the large kernels takes: consecutive blocks go to the
+// eight XCDs in turn, so block b works on the b / 8-th tile of XCD b % 8's run
+// of total / 8 tiles, which keeps an expert's matrix and rows in one XCD's L2.
+// Within an expert eight row tiles are walked before the next column tile.
+struct Place {
+  RowTile rows;
+  int tn;
+};
+template <int SH>
+__device__ __forceinline__ bool find_place(const int32_t* __restrict__ offsets, int experts, int n, int tiles_n,
+                                           uint32_t block, int lane, Place& out) {
+  constexpr int kRowGroup = 8;
+  int last = 0, lo = 0, hi = 0, upto = 0;
+  int64_t seen = 0;
+  for (int e0 = 0; e0 < experts; e0 += 64) {
+    hi = e0 + lane < experts ? offsets[e0 + lane + 1] : 0;
+    hi = hi > n ? n : hi;
+    hi = wave_scan_max(hi > last ? hi : last, lane);
+    lo = __shfl_up(hi, 1, 64);
+    if (lane == 0) lo = last;
+    upto = wave_scan_add((hi - lo + (1 << SH) - 1) >> SH, lane);
+    last = __builtin_amdgcn_readlane(hi, 63);
+    seen += __builtin_amdgcn_readlane(upto, 63);
+  }
+  const int64_t rest = (n - last + (1 << SH) - 1) >> SH;
+  const int64_t total = (seen + rest) * tiles_n, per = (total + 7) / 8;
+  const int64_t i = block >> 3, t = (block & 7) * per + i;
+  if (i >= per || t >= total) return false;
+  const int tm = (int)(t / tiles_n);   // the expert is that of row tile tm; its tiles are reordered below
+  int64_t first;                       // row tiles before the expert
+  int count;                           // and its own
+  int b, end;
+  if (tm >= seen) {
+    out.rows.e = experts;
+    first = seen;
+    count = (int)rest;
+    b = last;
+    end = n;
+  } else {
+    int from = 0;
+    first = 0;
+    for (int e0 = 0;; e0 += 64) {
+      if (experts > 64) {   // the offsets of this round again
+        hi = e0 + lane < experts ? offsets[e0 + lane + 1] : 0;
+        hi = hi > n ? n : hi;
+        hi = wave_scan_max(hi > from ? hi : from, lane);
+        lo = __shfl_up(hi, 1, 64);
+        if (lane == 0) lo = from;
+        upto = wave_scan_add((hi - lo + (1 << SH) - 1) >> SH, lane);
+      }
+      const uint64_t hit = __ballot(tm < first + upto);
+      if (hit) {
+        const int at = __ffsll((unsigned long long)hit) - 1;
+        out.rows.e = e0 + at;
+        b = __builtin_amdgcn_readlane(lo, at);
+        end = __builtin_amdgcn_readlane(hi, at);
+        count = (end - b + (1 << SH) - 1) >> SH;
+        first += __builtin_amdgcn_readlane(upto, at) - count;
+        break;
+      }
+      from = __builtin_amdgcn_readlane(hi, 63);
+      first += __builtin_amdgcn_readlane(upto, 63);
+    }
+  }
+  const int in = (int)(t - first * tiles_n);   // tile of the expert
+  const int group = in / (kRowGroup * tiles_n), at = in - group * kRowGroup * tiles_n;
+  const int wide = count - group * kRowGroup < kRowGroup ? count - group * kRowGroup : kRowGroup;
+  out.tn = at / wide;
+  out.rows.begin = b + ((int64_t)(group * kRowGroup + at % wide) << SH);
+  out.rows.end = out.rows.begin + (1 << SH) < end ? out.rows.begin + (1 << SH) : end;
+  return true;
+}
+
+template <class S>
+__device__ __forceinline__ void store_tile(const f32x16_t (&acc)[S::MT][S::NT], bf16_t* out, int64_t row0, int m_left,
+                                           int n0, int N, int lane, int wy, int wx) {
+#pragma unroll
+  for (int i = 0; i < S::MT; ++i) {
+    const int r = wy * S::WM + 32 * i + (lane & 31);
+    if (r < m_left) {
+      bf16_t* row = out + (row0 + r) * N;
+#pragma unroll
+      for (int j = 0; j < S::NT; ++j)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int c = n0 + wx * S::WN + 32 * j + 8 * g + 4 * (lane >> 5);
+          const float v[4] = {acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+          if (c < N) store4(row + c, 4, v);   // N is a multiple of 8 here
+        }
+    }
+  }
+}
+
+template <class S>
+__device__ __forceinline__ void zero_tile(bf16_t* out, int64_t row0, int m_left, int n0, int N) {
+  const int chunks = (N - n0 < S::BN ? N - n0 : S::BN) / 8;
+  for (int i = threadIdx.x; i < m_left * chunks; i += S::THREADS)
+    *reinterpret_cast<u32x4*>(out + (row0 + i / chunks) * N + n0 + 8 * (i % chunks)) = u32x4{0u, 0u, 0u, 0u};
+}
+
+template <class S, int SH, int MODE>
+__global__ __launch_bounds__(S::THREADS, 2) void k_rows_product(ProdArgs a) {
+  __shared__ __attribute__((aligned(16))) char lds[S::LDS];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  Place p;
+  if (!find_place<SH>(a.offsets, a.experts, (int)a.n, a.tiles_n, blockIdx.x, lane, p)) return;
+  const int m_left = (int)(p.rows.end - p.rows.begin), n0 = p.tn * S::BN;
+  bf16_t* out = static_cast<bf16_t*>(a.out);
+  if (p.rows.e == a.experts) {
+    zero_tile<S>(out, p.rows.begin, m_left, n0, a.N);
+    return;
+  }
+  const char* pb = static_cast<const char*>(a.p);
+  const char* wb = static_cast<const char*>(a.q) + (int64_t)p.rows.e * a.N * a.K * 2;
+  RowCopies<S::PR> cp;
+  if (a.rows) cp.init(Operand{pb, a.rows + p.rows.begin, a.x_rows, m_left, 0, a.K}, lane, w);
+  else cp.init(Operand{pb + p.rows.begin * a.K * 2, nullptr, 0, m_left, 0, a.K}, lane, w);
+  f32x16_t acc[S::MT][S::NT];
+  const int nk = (a.K + kBK - 1) / kBK;
+  if constexpr (S::QT) {
+    KCopies<S::BN, S::QR, false> cq;
+    cq.init(Operand{wb, nullptr, 0, a.K, n0, a.N}, lane, w);
+    tile_loop<S>(acc, (MUON_LDS char*)lds, cp, cq, nk, lane, w);
+  } else {
+    RowCopies<S::QR> cq;
+    cq.init(Operand{wb + (int64_t)n0 * a.K * 2, nullptr, 0, a.N - n0, 0, a.K}, lane, w);
+    tile_loop<S>(acc, (MUON_LDS char*)lds, cp, cq, nk, lane, w);
+  }
+  store_tile<S>(acc, out, p.rows.begin, m_left, n0, a.N, lane, w / S::WGN, w % S::WGN);
+}
+
+// Weight gradient.  An expert's tiles are dealt to the XCDs in runs, so that
+// a popular expert's work is spread over all of them.
+template <class S, bool GATHER>
+__global__ __launch_bounds__(S::THREADS, 2) void k_weight_product(ProdArgs a) {
+  __shared__ __attribute__((aligned(16))) char lds[S::LDS];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tiles = a.tiles_m * a.tiles_n;
+  int e, t;
+  if (tiles >= 64) {
+    const int run = (tiles + 7) / 8, i = blockIdx.x >> 3;
+    e = i / run;
+    t = (blockIdx.x & 7) * run + i - e * run;
+    if (t >= tiles) return;
+  } else {
+    e = blockIdx.x / tiles;
+    t = blockIdx.x - e * tiles;
+  }
+  if (e >= a.experts) return;
+  const int m0 = t / a.tiles_n * S::BM, n0 = t % a.tiles_n * S::BN;
+  int64_t b, end;
+  expert_rows(a.offsets, e, (int)a.n, lane, b, end);
+  const int K = (int)(end - b), m_left = a.M - m0 < S::BM ? a.M - m0 : S::BM;
+  bf16_t* out = static_cast<bf16_t*>(a.out);
+  const int64_t row0 = (int64_t)e * a.M + m0;
+  if (K == 0) {
+    zero_tile<S>(out, row0, m_left, n0, a.N);
+    return;
+  }
+  f32x16_t acc[S::MT][S::NT];
+  KCopies<S::BM, S::PR, false> cp;
+  KCopies<S::BN, S::QR, GATHER> cq;
+  cp.init(Operand{static_cast<const char*>(a.p) + b * a.M * 2, nullptr, 0, K, m0, a.M}, lane, w);
+  if (GATHER) cq.init(Operand{static_cast<const char*>(a.q), a.rows + b, a.x_rows, K, n0, a.N}, lane, w);
+  else cq.init(Operand{static_cast<const char*>(a.q) + b * a.N * 2, nullptr, 0, K, n0, a.N}, lane, w);
+  tile_loop<S>(acc, (MUON_LDS char*)lds, cp, cq, (K + kBK - 1) / kBK, lane, w);
+  store_tile<S>(acc, out, row0, m_left, n0, a.N, lane, w / S::WGN, w % S::WGN);
+}
+
 // --------------------------------------------------------------------- host
 
 constexpr int64_t kMaxSide = (int64_t(1) << 24) - 1;
@@ -390,6 +562,36 @@ int launch_product(ProdArgs a, int dtype, int64_t tiles_m, hipStream_t s) {
   return launch_status("grouped product launch");
 }
 
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// The large kernels copy 16-byte chunks that a row holds whole and address an
+// operand (that of gathered rows whole, else one tile's rows) by 31 bits.
+bool chunked(const ProdArgs& a, int dtype, int64_t c0, int64_t c1, int64_t gathered_cols) {
+  return dtype == MUON_BF16 && c0 % 8 == 0 && c1 % 8 == 0 && aligned16(a.p) && aligned16(a.q) && aligned16(a.out) &&
+         c0 < (1 << 21) && c1 < (1 << 21) && (!a.rows || a.x_rows * gathered_cols < (int64_t(1) << 30));
+}
+
+template <class S, int SH, int MODE>
+int launch_rows(ProdArgs a, hipStream_t s) {
+  a.tiles_n = (int32_t)ceil_div(a.N, S::BN);
+  const int64_t blocks = 8 * ceil_div(row_tiles(a.n, a.experts, S::BM) * a.tiles_n, 8);
+  if (blocks > kMaxCount) return fail(MUON_EUNSUPPORTED, "more than 2^31 output tiles");
+  hipLaunchKernelGGL((k_rows_product<S, SH, MODE>), dim3((uint32_t)blocks), dim3(S::THREADS), 0, s, a);
+  return launch_status("grouped product launch");
+}
+
+template <class S>
+int launch_weight(ProdArgs a, hipStream_t s) {
+  a.tiles_m = (int32_t)ceil_div(a.M, S::BM);
+  a.tiles_n = (int32_t)ceil_div(a.N, S::BN);
+  const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
+  const int64_t blocks = a.experts * (tiles >= 64 ? 8 * ceil_div(tiles, 8) : tiles);
+  if (blocks > kMaxCount) return fail(MUON_EUNSUPPORTED, "more than 2^31 output tiles");
+  if (a.rows) hipLaunchKernelGGL((k_weight_product<S, true>), dim3((uint32_t)blocks), dim3(S::THREADS), 0, s, a);
+  else hipLaunchKernelGGL((k_weight_product<S, false>), dim3((uint32_t)blocks), dim3(S::THREADS), 0, s, a);
+  return launch_status("grouped weight gradient launch");
+}
+
 // Workspace of the weight gradient: a checkpoint's rows as dense values.
 uint64_t weight_grad_bytes(int dtype, int64_t x_rows, int64_t inner, bool kept) {
   return kept ? (uint64_t)x_rows * inner * (dtype == MUON_BF16 ? 2 : 4) : 0;
@@ -413,6 +615,8 @@ int muon_grouped_matmul(const void* x, const void* w, const int32_t* offsets, co
   if ((!x && x_rows) || !w || !offsets || !y) return fail(MUON_EINVAL, "NULL pointer");
   if ((rc = check_device())) return rc;
   ProdArgs a = {x, w, y, offsets, rows, n, x_rows, experts, 0, (int32_t)outer, (int32_t)inner, 0, 0};
+  if (chunked(a, dtype, inner, outer, inner))
+    return launch_rows<Shape<256, 256, 2, 4, false, false>, 8, kMatmul>(a, static_cast<hipStream_t>(stream));
   return launch_product<kMatmul>(a, dtype, row_tiles(n, experts, side(dtype)), static_cast<hipStream_t>(stream));
 }
 
@@ -425,6 +629,8 @@ int muon_grouped_input_grad(const void* dy, const void* w, const int32_t* offset
   if (!dy || !w || !offsets || !dx) return fail(MUON_EINVAL, "NULL pointer");
   if ((rc = check_device())) return rc;
   ProdArgs a = {dy, w, dx, offsets, nullptr, n, n, experts, 0, (int32_t)inner, (int32_t)outer, 0, 0};
+  if (chunked(a, dtype, inner, outer, inner))
+    return launch_rows<Shape<256, 256, 2, 4, false, true>, 8, kInputGrad>(a, static_cast<hipStream_t>(stream));
   return launch_product<kInputGrad>(a, dtype, row_tiles(n, experts, side(dtype)), static_cast<hipStream_t>(stream));
 }
 
@@ -462,6 +668,7 @@ int muon_grouped_weight_grad(const void* dy, const void* x, const void* q, const
     x = workspace;
   }
   ProdArgs a = {dy, x, dw, offsets, rows, n, x_rows, experts, (int32_t)outer, (int32_t)inner, 0, 0, 0};
+  if (chunked(a, dtype, inner, outer, inner)) return launch_weight<Shape<256, 256, 2, 4, true, true>>(a, s);
   a.tiles_m = (int32_t)ceil_div(outer, side(dtype));
   return launch_product<kWeightGrad>(a, dtype, (int64_t)experts * a.tiles_m, s);
 }

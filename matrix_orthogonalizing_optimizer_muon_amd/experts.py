@@ -104,17 +104,23 @@ def _rows(t):
 
 
 def _placed(*named):
-    """The GPU all tensors of (name, tensor, ...) are on; they must be contiguous."""
-    dev = named[1].device
-    for i in range(0, len(named), 2):
-        t = named[i + 1]
-        if not t.is_cuda:
-            raise ValueError(f"{named[i]} is not on the GPU")
-        if t.device != dev:
-            raise ValueError(f"{named[i]} is on {t.device}, {named[0]} on {dev}")
-        if not t.is_contiguous():
-            raise ValueError(f"{named[i]} is not contiguous")
+    """The GPU all tensors of (name, tensor, ...) are on, by index; they must be contiguous."""
+    dev = named[1].get_device()
+    for t in named[1::2]:
+        if t.get_device() != dev or dev < 0 or not t.is_contiguous():
+            _misplaced(named)
     return dev
+
+
+def _misplaced(named):
+    dev = named[1].device
+    for name, t in zip(named[::2], named[1::2]):
+        if not t.is_cuda:
+            raise ValueError(f"{name} is not on the GPU")
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, {named[0]} on {dev}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} is not contiguous")
 
 
 def _on(fn):
@@ -130,31 +136,23 @@ def _on(fn):
     return call
 
 
-class _NoSwitch:
-    def __enter__(self):
-        pass
-
-    def __exit__(self, *exc):
-        pass
-
-
-_NO_SWITCH = _NoSwitch()
-
-
-def _device(dev):
-    """Makes dev the current device (the library launches there)."""
-    return _NO_SWITCH if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+def _call(dev, fn, *args):
+    """fn(*args, stream) on dev's current stream, with dev the current device (the library launches there)."""
+    if dev == torch.cuda.current_device():
+        code = fn(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, _stream(dev))
+    if code:
+        L.check(code)
 
 
 def _stream(dev):
     return torch.cuda.current_stream(dev).cuda_stream
 
 
-def _call(dev, fn, *args):
-    with _device(dev):
-        code = fn(*args, _stream(dev))
-    if code:
-        L.check(code)
+# the stream's handle without a Stream object around it, where this torch has it: a third of a small call's time
+_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream)
 
 
 def _ptr(t):
@@ -175,14 +173,14 @@ def route(logits, k, *, normalize=True):
         raise ValueError(f"k must be in [1, {experts}], not {k}")
     dev = _placed("logits", logits)
     lib = L.lib()
-    weights = torch.empty((tokens, k), dtype=torch.float32, device=dev)
-    chosen = torch.empty((tokens, k), dtype=_I32, device=dev)
-    slots = torch.empty((tokens, k), dtype=_I32, device=dev)
-    rows = torch.empty(tokens * k, dtype=_I32, device=dev)
-    offsets = torch.empty(experts + 1, dtype=_I32, device=dev)
+    weights = logits.new_empty((tokens, k), dtype=torch.float32)
+    chosen = logits.new_empty((tokens, k), dtype=_I32)
+    slots = torch.empty_like(chosen)
+    rows = logits.new_empty(tokens * k, dtype=_I32)
+    offsets = logits.new_empty(experts + 1, dtype=_I32)
     need = ctypes.c_uint64()
     L.check(lib.muon_route_workspace(tokens, experts, ctypes.byref(need)))
-    ws = torch.empty(need.value, dtype=torch.uint8, device=dev) if need.value else None
+    ws = logits.new_empty(need.value, dtype=torch.uint8) if need.value else None
     _call(dev, lib.muon_route, _ptr(logits), code, tokens, experts, k, 1 if normalize else 0, _ptr(weights),
           _ptr(chosen), _ptr(slots), _ptr(rows), _ptr(offsets), _ptr(ws) if ws is not None else None, need.value)
     return Routing(weights, chosen, slots, rows, offsets)
@@ -225,7 +223,7 @@ def grouped_matmul(x, w, offsets, *, rows=None):
         _rows(rows)
         n = rows.shape[0]
         dev = _placed("x", x, "w", w, "offsets", offsets, "rows", rows)
-    y = torch.empty((n, outer), dtype=x.dtype, device=dev)
+    y = x.new_empty((n, outer))
     _call(dev, L.lib().muon_grouped_matmul, _ptr(x), _ptr(w), _ptr(offsets), None if rows is None else _ptr(rows),
           code, n, x.shape[0], experts, outer, inner, _ptr(y))
     return y
@@ -244,7 +242,7 @@ def grouped_input_grad(dy, w, offsets):
     _offsets(offsets, experts)
     dev = _placed("dy", dy, "w", w, "offsets", offsets)
     n = dy.shape[0]
-    dx = torch.empty((n, inner), dtype=dy.dtype, device=dev)
+    dx = dy.new_empty((n, inner))
     _call(dev, L.lib().muon_grouped_input_grad, _ptr(dy), _ptr(w), _ptr(offsets), code, n, experts, outer, inner,
           _ptr(dx))
     return dx
@@ -272,11 +270,11 @@ def grouped_weight_grad(dy, x, offsets, *, rows=None):
         raise ValueError(f"dy has {n} rows, x or rows {x_rows if rows is None else rows.shape[0]}")
     dev = _placed(*placed)
     lib = L.lib()
-    dw = torch.empty((experts, outer, inner), dtype=dy.dtype, device=dev)
+    dw = dy.new_empty((experts, outer, inner))
     need = ctypes.c_uint64()
     L.check(lib.muon_grouped_weight_grad_workspace(code, n, x_rows, experts, outer, inner, 1 if kept else 0,
                                                    ctypes.byref(need)))
-    ws = torch.empty(need.value, dtype=torch.uint8, device=dev) if need.value else None
+    ws = dy.new_empty(need.value, dtype=torch.uint8) if need.value else None
     _call(dev, lib.muon_grouped_weight_grad, _ptr(dy), None if kept else _ptr(x), _ptr(x.q) if kept else None,
           _ptr(x.scale) if kept else None, x.kind if kept else 0, _ptr(offsets), None if rows is None else _ptr(rows),
           code, n, x_rows, experts, outer, inner, _ptr(dw), _ptr(ws) if ws is not None else None, need.value)
@@ -304,7 +302,7 @@ def combine(y, slots, weights):
     code = _choices(y, slots, weights)
     dev = _placed("y", y, "slots", slots, "weights", weights)
     (tokens, k), cols = slots.shape, y.shape[1]
-    out = torch.empty((tokens, cols), dtype=y.dtype, device=dev)
+    out = y.new_empty((tokens, cols))
     _call(dev, L.lib().muon_combine, _ptr(y), _ptr(slots), _ptr(weights), code, tokens, k, cols, _ptr(out))
     return out
 
@@ -326,10 +324,12 @@ def combine_backward(dout, y, slots, weights, offsets):
 
 # ----------------------------------------------------------------- checkpoints
 
-def _kept(kind, rows, cols, dtype, dev):
-    q = torch.empty((rows, cols), dtype=_KIND[kind][1], device=dev)
-    scale = torch.empty((rows, -(-cols // BLOCK)), dtype=torch.uint8, device=dev)
-    return Checkpoint(q, scale, dtype)
+def _kept(kind, rows, cols, dtype, src):
+    q = src.new_empty((rows, cols), dtype=_KIND[kind][1])
+    scale = src.new_empty((rows, -(-cols // BLOCK)), dtype=torch.uint8)
+    c = Checkpoint.__new__(Checkpoint)
+    c.q, c.scale, c.dtype, c.kind = q, scale, dtype, _KIND[kind][0]
+    return c
 
 
 def _kind(kind):
@@ -344,7 +344,7 @@ def checkpoint(x, kind="int8"):
     code = _matrix("x", x)
     dev = _placed("x", x)
     rows, cols = x.shape
-    c = _kept(kind, rows, cols, x.dtype, dev)
+    c = _kept(kind, rows, cols, x.dtype, x)
     _call(dev, L.lib().muon_checkpoint, _ptr(x), code, rows, cols, c.kind, _ptr(c.q), _ptr(c.scale))
     return c
 
@@ -356,7 +356,7 @@ def restore(c):
         raise TypeError("restore takes a Checkpoint")
     dev = _placed("q", c.q, "scale", c.scale)
     rows, cols = c.shape
-    x = torch.empty((rows, cols), dtype=c.dtype, device=dev)
+    x = c.scale.new_empty((rows, cols), dtype=c.dtype)
     _call(dev, L.lib().muon_restore, _ptr(c.q), _ptr(c.scale), c.kind, rows, cols, _CODE[c.dtype], _ptr(x))
     return x
 
@@ -372,11 +372,11 @@ def gated(gu, checkpoint=None):
     if checkpoint is not None:
         _kind(checkpoint)
     dev = _placed("gu", gu)
-    h = torch.empty((rows, cols), dtype=gu.dtype, device=dev)
+    h = gu.new_empty((rows, cols))
     if checkpoint is None:
         _call(dev, L.lib().muon_gated, _ptr(gu), code, rows, cols, 0, _ptr(h), None, None)
         return h
-    c = _kept(checkpoint, rows, 2 * cols, gu.dtype, dev)
+    c = _kept(checkpoint, rows, 2 * cols, gu.dtype, gu)
     _call(dev, L.lib().muon_gated, _ptr(gu), code, rows, cols, c.kind, _ptr(h), _ptr(c.q), _ptr(c.scale))
     return h, c
 
@@ -393,7 +393,7 @@ def gated_backward(dh, gu):
     if gu.dtype != dh.dtype or tuple(gu.shape) != (rows, 2 * cols) or not cols:
         raise ValueError(f"gu must be {dh.dtype} of shape {(rows, 2 * cols)}, not {gu.dtype} of {tuple(gu.shape)}")
     dev = _placed("dh", dh, "q", gu.q, "scale", gu.scale) if kept else _placed("dh", dh, "gu", gu)
-    dgu = torch.empty((rows, 2 * cols), dtype=dh.dtype, device=dev)
+    dgu = dh.new_empty((rows, 2 * cols))
     h = torch.empty_like(dh)
     _call(dev, L.lib().muon_gated_backward, _ptr(dh), None if kept else _ptr(gu), _ptr(gu.q) if kept else None,
           _ptr(gu.scale) if kept else None, gu.kind if kept else 0, code, rows, cols, _ptr(dgu), _ptr(h))
