@@ -2,6 +2,9 @@
 // each operand either k-contiguous (tile rows of BK = 64 k) or k-major (64
 // tile rows of BM or BN elements), copied global -> LDS by buffer_load ... lds
 // (16 bytes a lane, no registers in between), two stages.
+// A block walks a list of output tiles: the copies of its next tile's first
+// k-tiles are issued before the stores of the last one, whose way to memory is
+// then hidden behind the next tile's products.
 //
 // It differs from the square core (mfma_nt.hpp, whose LDS layouts, swizzles
 // and transposing reads it shares) in what the copies take: rows picked by an
@@ -33,83 +36,114 @@ struct Shape {
   static_assert((!PT || BM >= 128) && (!QT || BN >= 128), "k-major tile rows of 256 bytes or more");
 };
 
+// A copy of 16 bytes a lane from memory to LDS (1 KiB at dst).  Written out, and
+// not through the builtin, because the compiler otherwise waits for every copy
+// in flight before a transposing LDS read, whose address it cannot tell from
+// the copies' targets; tile_loop makes the waits that are needed.  No register
+// is written (the compiler holds nothing in M0).  The idle cycles are those
+// that M0 (1) and a descriptor written by a vector instruction (5) take before
+// such a load reads them.
+typedef __attribute__((address_space(3))) char lds_char;
+__device__ __forceinline__ void copy_to_lds(lds_char* dst, u32x4 rsrc, uint32_t voff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :
+               : "s"((uint32_t)(uintptr_t)dst), "v"(voff), "s"(rsrc));
+}
+__device__ __forceinline__ u32x4 copy_rsrc(const char* base, uint32_t bytes) {
+  const uint64_t b = (uint64_t)(uintptr_t)base;
+  return u32x4{(uint32_t)b, (uint32_t)(b >> 32) & 0xffffu, bytes, (uint32_t)nt::kRsrcWord3};
+}
+
 // What a block's copies need to know of one operand.
 struct Operand {
   const char* base;        // row 0 (k-contiguous: of the tile; k-major: of k = 0), column 0
   const int32_t* gather;   // indices of the tile's rows, or null: rows follow each other
-  int64_t src_rows;        // rows that gather may name
-  int64_t rows;            // rows that exist (k-contiguous: of the tile; k-major: k)
+  int32_t src_rows;        // rows that gather may name
+  int32_t rows;            // rows that exist (k-contiguous: of the tile; k-major: k)
   int32_t col0, cols;      // k-major: first column; row length in elements (k-contiguous: K)
 };
 
-// k-contiguous: copy u of wave w holds tile rows (w NR + u) 8 + lane / 8.
-template <int NR>
+// k-contiguous: copy u < NR of wave w holds tile rows (w NR + u) 8 + lane / 8.
+// A block's tiles differ in height, so NR <= 4 is an argument of the calls.
 struct RowCopies {
-  static_assert(NR % 2 == 0, "the swizzle phase must follow the copy index");
   const char* base;
-  uint32_t voff[NR];
+  uint32_t voff[4];
   int32_t col[2];      // first k of the lane's chunk in tile 0, even and odd copies
   int32_t cols;
+  int32_t src[4];      // gathered source rows of the next init, -1: none
 
-  __device__ __forceinline__ void init(const Operand& o, int lane, int w) {
+  // the source rows of an operand's tile rows; these loads may be in flight until init
+  __device__ __forceinline__ void look(const Operand& o, int nr, int lane, int w) {
+    if (!o.gather) return;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int r = (w * nr + u) * 8 + lane / 8;
+      src[u] = r < o.rows && u < nr ? o.gather[r] : -1;
+    }
+  }
+  // nr: 2 or 4
+  __device__ __forceinline__ void init(const Operand& o, int nr, int lane, int w) {
     base = o.base;
     cols = o.cols;
     const uint32_t ld = (uint32_t)o.cols * 2u;
 #pragma unroll
-    for (int u = 0; u < NR; ++u) {
-      const int r = (w * NR + u) * 8 + lane / 8;
+    for (int u = 0; u < 4; ++u) {
+      const int r = (w * nr + u) * 8 + lane / 8;
       const int chunk = (lane & 7) ^ nt::swz<128>(r);
-      if (u < 2) col[u] = chunk * 8;
-      int64_t src = r;
-      bool ok = r < o.rows;
-      if (ok && o.gather) {
-        src = o.gather[r];
-        ok = src >= 0 && src < o.src_rows;
-      }
-      voff[u] = ok ? (uint32_t)src * ld + (uint32_t)chunk * 16u : kNone;
+      if (u < 2) col[u] = chunk * 8;   // nr is even: the swizzle's phase follows the copy's index
+      const int from = o.gather ? src[u] : r;
+      const bool ok = o.gather ? from >= 0 && from < o.src_rows : r < o.rows;
+      voff[u] = ok ? (uint32_t)from * ld + (uint32_t)chunk * 16u : kNone;
     }
   }
   __device__ __forceinline__ void ahead(int, int, int) {}
-  template <int U>
-  __device__ __forceinline__ void step(MUON_LDS char* dst, __amdgpu_buffer_rsrc_t rs, const bool (&in)[2], int w) const {
+  template <int NR, int U = 0>
+  __device__ __forceinline__ void step(MUON_LDS char* dst, u32x4 rs, const bool (&in)[2], int w) const {
     if constexpr (U < NR) {
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, dst + (w * NR + U) * 1024, 16, in[U & 1] ? voff[U] : kNone, 0, 0, 0);
-      step<U + 1>(dst, rs, in, w);
+      copy_to_lds(dst + (w * NR + U) * 1024, rs, in[U & 1] ? voff[U] : kNone);
+      step<NR, U + 1>(dst, rs, in, w);
     }
   }
+  template <int NR>
   __device__ __forceinline__ void issue(MUON_LDS char* dst, int kt, int, int w) {
-    const auto rs = nt::make_rsrc(base + (int64_t)kt * 128, kRange);
+    const u32x4 rs = copy_rsrc(base + (int64_t)kt * 128, kRange);
     const bool in[2] = {kt * kBK + col[0] < cols, kt * kBK + col[1] < cols};
-    step<0>(dst, rs, in, w);
+    step<NR>(dst, rs, in, w);
   }
 };
 
-// k-major, B elements a row: copy u of wave w holds tile rows w NR RPI + u RPI
-// + lane / CPR.  Rows past the last lie past the descriptor's range, which
-// ends with the operand's last row.  GATHER: the indices of a wave's rows come
-// one tile ahead, one a lane, and reach the copies through scalar registers.
-template <int B, int NR, bool GATHER>
+// k-major, 64 NR elements a row (NR = 2 or 4 copies a wave): copy u of wave w
+// holds tile rows w NR RPI + u RPI + lane / CPR.  Rows past the last lie past
+// the descriptor's range, which ends with the operand's last row.  GATHER: the
+// indices of a wave's rows come one tile ahead, one a lane, and reach the
+// copies through scalar registers.
+template <bool GATHER>
 struct KCopies {
-  static constexpr int CPR = B / 8, RPI = 64 / CPR, RPW = NR * RPI;   // chunks a row; rows a copy, a wave
-  static_assert(RPI == 2 || RPI == 4, "rows a copy");
-  static_assert(RPW <= 64, "rows a wave");
   const char* base;
   const int32_t* gather;
-  uint32_t voff[NR];       // with GATHER the column's part alone
+  uint32_t voff[4];        // with GATHER the column's part alone
   uint32_t ld;
-  int64_t rows, src_rows;
-  int32_t idx;             // GATHER: row index of row (lane % RPW) of the next tile, -1: none
+  int32_t rows, src_rows;
+  int32_t idx;             // GATHER: row index of row (lane % 8) of the next tile, -1: none
 
-  __device__ __forceinline__ void init(const Operand& o, int lane, int w) {
+  template <int NR>
+  struct Rows {
+    static constexpr int CPR = 8 * NR, RPI = 64 / CPR;   // chunks a row; rows a copy
+    static_assert(NR * RPI == 8, "a wave copies 8 of the 64 rows");
+  };
+  __device__ __forceinline__ void look(const Operand&, int, int, int) {}
+  // nr: 2 or 4 copies
+  __device__ __forceinline__ void init(const Operand& o, int nr, int lane, int w) {
     base = o.base;
     gather = o.gather;
     rows = o.rows;
     src_rows = o.src_rows;
     ld = (uint32_t)o.cols * 2u;
+    const int shift = nr == 4 ? 5 : 4;   // log2 of the chunks a row
 #pragma unroll
-    for (int u = 0; u < NR; ++u) {
-      const int r = (w * NR + u) * RPI + lane / CPR;
-      const int chunk = (lane % CPR) ^ nt::swzt(r);
+    for (int u = 0; u < 4; ++u) {
+      const int r = (((w * nr + u) << 6) >> shift) + (lane >> shift);
+      const int chunk = (lane & ((1 << shift) - 1)) ^ nt::swzt(r);
       const int c = o.col0 + chunk * 8;
       voff[u] = c < o.cols ? (uint32_t)c * 2u + (GATHER ? 0u : (uint32_t)r * ld) : kNone;
     }
@@ -117,13 +151,14 @@ struct KCopies {
   // the indices of tile kt
   __device__ __forceinline__ void ahead(int kt, int lane, int w) {
     if constexpr (GATHER) {
-      const int64_t k = (int64_t)kt * kBK + w * RPW + lane % RPW;
+      const int k = kt * kBK + w * 8 + lane % 8;   // rows + 256 stays below 2^31 where rows does
       idx = k < rows ? gather[k] : -1;
     }
   }
-  template <int U>
-  __device__ __forceinline__ void step(MUON_LDS char* dst, __amdgpu_buffer_rsrc_t rs, int lane, int w) const {
+  template <int NR, int U = 0>
+  __device__ __forceinline__ void step(MUON_LDS char* dst, u32x4 rs, int lane, int w) const {
     if constexpr (U < NR) {
+      constexpr int CPR = Rows<NR>::CPR, RPI = Rows<NR>::RPI;
       uint32_t v = voff[U];
       if constexpr (GATHER) {
         int32_t s = __builtin_amdgcn_readlane(idx, U * RPI);
@@ -134,17 +169,19 @@ struct KCopies {
         }
         v = s >= 0 && s < src_rows && v != kNone ? v + (uint32_t)s * ld : kNone;
       }
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, dst + (w * NR + U) * 1024, 16, v, 0, 0, 0);
-      step<U + 1>(dst, rs, lane, w);
+      copy_to_lds(dst + (w * NR + U) * 1024, rs, v);
+      step<NR, U + 1>(dst, rs, lane, w);
     }
   }
+  template <int NR>
   __device__ __forceinline__ void issue(MUON_LDS char* dst, int kt, int lane, int w) {
     if constexpr (GATHER) {
-      step<0>(dst, nt::make_rsrc(base, kRange), lane, w);
+      step<NR>(dst, copy_rsrc(base, kRange), lane, w);
     } else {
       const int64_t left = (rows - (int64_t)kt * kBK) * (int64_t)ld;
-      step<0>(dst, nt::make_rsrc(base + (int64_t)kt * kBK * ld, left <= 0 ? 0u : left < kRange ? (uint32_t)left : kRange),
-              lane, w);
+      step<NR>(dst,
+               copy_rsrc(base + (int64_t)kt * kBK * ld, left <= 0 ? 0u : left < kRange ? (uint32_t)left : kRange),
+               lane, w);
     }
   }
 };
@@ -183,8 +220,11 @@ struct TileFrags {
   }
 };
 
+// Accumulators of a wave: those of the widest shape; smaller ones use the first of them.
+typedef nt::f32x16_t Acc[4][2];
+
 template <class S>
-__device__ __forceinline__ void tile_mfma(nt::f32x16_t (&acc)[S::MT][S::NT], const TileFrags<S>& f) {
+__device__ __forceinline__ void tile_mfma(Acc& acc, const TileFrags<S>& f) {
 #pragma unroll
   for (int i = 0; i < S::MT; ++i)
 #pragma unroll
@@ -203,14 +243,40 @@ __device__ __forceinline__ void tile_hint() {
   }
 }
 
-// The k loop over nk >= 1 tiles of 64.  Tile kt sits in stage kt % 2; the
-// fragments of a k-group are read one group ahead.  When the reads of a tile's
-// last group are done and the copies of the next tile have landed, one
-// barrier, and the copies of tile kt + 2 go into the stage just read; past the
-// end they name no chunk and bring zeros that nothing reads.
+// Wait until at most N of the wave's memory operations and, behind them, its
+// last `stored` stores are in flight (operations of a wave complete in order).
+template <int N, bool LGKM>
+__device__ __forceinline__ void wait_behind(int stored) {
+  constexpr int kKeep = LGKM ? ~0xF00 : ~0;
+  if (stored == 16) __builtin_amdgcn_s_waitcnt(nt::waitcnt_vm(N + 16) & kKeep);
+  else if (stored == 8) __builtin_amdgcn_s_waitcnt(nt::waitcnt_vm(N + 8) & kKeep);
+  else __builtin_amdgcn_s_waitcnt(nt::waitcnt_vm(N) & kKeep);
+}
+
+// Copies of a tile's first two k-tiles; every wave is done with the stages.
 template <class S, class PC, class QC>
-__device__ __forceinline__ void tile_loop(nt::f32x16_t (&acc)[S::MT][S::NT], MUON_LDS char* lds, PC& cp, QC& cq,
-                                          int nk, int lane, int w) {
+__device__ __forceinline__ void tile_begin(MUON_LDS char* lds, PC& cp, QC& cq, int lane, int w) {
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    cp.ahead(t, lane, w);
+    cq.ahead(t, lane, w);
+    cp.template issue<S::PR>(lds + t * S::STAGE, t, lane, w);
+    cq.template issue<S::QR>(lds + t * S::STAGE + S::PB, t, lane, w);
+  }
+  cp.ahead(2, lane, w);
+  cq.ahead(2, lane, w);
+}
+
+// The k loop over nk >= 1 tiles of 64, after tile_begin and then `stored`
+// stores.  Tile kt sits in stage kt % 2; the fragments of a k-group are read
+// one group ahead.  When the reads of a tile's last group are done and the
+// copies of the next tile have landed, one barrier, and the copies of tile
+// kt + 2 go into the stage just read; past the end they name no chunk and
+// bring zeros that nothing reads.  On return every wave is done with the
+// stages.
+template <class S, class PC, class QC>
+__device__ __forceinline__ void tile_loop(Acc& acc, MUON_LDS char* lds, PC& cp, QC& cq, int nk, int stored, int lane,
+                                          int w) {
   const int wy = w / S::WGN, wx = w % S::WGN;
 #pragma unroll
   for (int i = 0; i < S::MT; ++i)
@@ -218,16 +284,7 @@ __device__ __forceinline__ void tile_loop(nt::f32x16_t (&acc)[S::MT][S::NT], MUO
     for (int j = 0; j < S::NT; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    cp.ahead(t, lane, w);
-    cq.ahead(t, lane, w);
-    cp.issue(lds + t * S::STAGE, t, lane, w);
-    cq.issue(lds + t * S::STAGE + S::PB, t, lane, w);
-  }
-  cp.ahead(2, lane, w);
-  cq.ahead(2, lane, w);
-  __builtin_amdgcn_s_waitcnt(nt::kWaitVmLgkm0);
+  wait_behind<S::PR + S::QR, false>(stored);
   nt::block_barrier();
   TileFrags<S> f0, f1;
   f0.load(lds, 0, lane, wy, wx);
@@ -245,10 +302,11 @@ __device__ __forceinline__ void tile_loop(nt::f32x16_t (&acc)[S::MT][S::NT], MUO
       }
       tile_hint<S, 0, S::NDS>();
     }
-    __builtin_amdgcn_s_waitcnt(nt::kWaitVmLgkm0);   // the next tile landed, own reads done
+    wait_behind<0, true>(stored);   // the next tile landed, own reads done
+    stored = 0;
     nt::block_barrier();
-    cp.issue(st, kt + 2, lane, w);
-    cq.issue(st + S::PB, kt + 2, lane, w);
+    cp.template issue<S::PR>(st, kt + 2, lane, w);
+    cq.template issue<S::QR>(st + S::PB, kt + 2, lane, w);
     cp.ahead(kt + 3, lane, w);
     cq.ahead(kt + 3, lane, w);
     stage ^= 1;
@@ -257,6 +315,42 @@ __device__ __forceinline__ void tile_loop(nt::f32x16_t (&acc)[S::MT][S::NT], MUO
     tile_hint<S, S::PR + S::QR, S::NDS>();
   }
   __builtin_amdgcn_s_waitcnt(nt::kWaitVmLgkm0);   // no copy outlives the loop
+  nt::block_barrier();
+}
+
+// A tile's rows out of the accumulators: 32 rows of a wave's 64 columns at a
+// time through 4 KiB of LDS of its own, so that a store instruction writes
+// whole 128-byte runs of 8 rows.  8-byte group 2 c + h of row r is kept in chunk c ^ swz(r).
+// Stores that reach past the tile name no address, so that a
+// tile always makes 4 mt of them: returned for tile_loop's waits.
+__device__ __forceinline__ int tile_store(const Acc& acc, int mt, MUON_LDS char* buf, bf16_t* out, int row0, int m_left,
+                                          int col0, int N, int lane) {
+  const auto rs = nt::make_rsrc(out, kRange);
+  const int r = lane & 31, h = lane >> 5;
+  MUON_LDS char* put = buf + r * 128 + h * 8;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i >= mt) break;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        *(MUON_LDS u32x2*)(put + (((4 * j + g) ^ nt::swz<128>(r)) << 4)) =
+            u32x2{pack2(acc[i][j][4 * g], acc[i][j][4 * g + 1]), pack2(acc[i][j][4 * g + 2], acc[i][j][4 * g + 3])};
+    u32x4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int q = u * 8 + lane / 8;
+      v[u] = *(const MUON_LDS u32x4*)(buf + q * 128 + (((lane & 7) ^ nt::swz<128>(q)) << 4));
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int q = row0 + 32 * i + u * 8 + lane / 8, c = col0 + 8 * (lane & 7);
+      const uint32_t at = q < m_left && c < N ? ((uint32_t)q * (uint32_t)N + (uint32_t)c) * 2u : kNone;
+      __builtin_amdgcn_raw_buffer_store_b128(v[u], rs, at, 0, 0);
+    }
+  }
+  return 4 * mt;
 }
 
 }  // namespace ex

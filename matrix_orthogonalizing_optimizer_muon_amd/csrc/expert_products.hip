@@ -8,6 +8,8 @@
 //   weight grad  dW_e[o][i] = sum_r dy[r][o] x[rows[r]][i]   both k-major
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "expert_mfma.hpp"
 #include "experts.hpp"
 #include "mfma_nt.hpp"
@@ -361,173 +363,318 @@ __global__ __launch_bounds__(256) void k_product(ProdArgs a) {
 
 // ------------------------------------------------------------- large tiles
 
-// Which tile a block of the large kernels takes: consecutive blocks go to the
-// eight XCDs in turn, so block b works on the b / 8-th tile of XCD b % 8's run
-// of total / 8 tiles, which keeps an expert's matrix and rows in one XCD's L2.
-// Within an expert eight row tiles are walked before the next column tile.
-struct Place {
-  RowTile rows;
-  int tn;
+// The large kernels run one block of 8 waves per CU, each walking a list of
+// output tiles: consecutive blocks go to the eight XCDs in turn, so block b has
+// every 32nd tile from b / 8 on of the list of XCD b % 8.
+constexpr int kWalkers = 256;
+constexpr int kStoreBytes = 4096;   // LDS of each wave behind the stages, for tile_store
+
+// 256 x 256 tiles, and halves of them where no more is left: 8 waves of 128 x
+// 64, or of 64 x 64.
+template <bool PT, bool QT>
+struct Shapes {
+  typedef Shape<256, 256, 2, 4, PT, QT> Full;
+  typedef Shape<128, 256, 2, 4, PT, QT> Flat;
+  typedef Shape<256, 128, 4, 2, PT, QT> Thin;
+  static constexpr int LDS = Full::LDS + 8 * kStoreBytes;
 };
-template <int SH>
-__device__ __forceinline__ bool find_place(const int32_t* __restrict__ offsets, int experts, int n, int tiles_n,
-                                           uint32_t block, int lane, Place& out) {
+enum Cut { kFull = 0, kFlat = 1, kThin = 2 };
+__device__ __forceinline__ int cut_of(int m_left, int n_left) {
+  return m_left <= 128 ? kFlat : n_left <= 128 ? kThin : kFull;
+}
+
+// The experts' rows held across a wave: lane l has those of experts l per to
+// (l + 1) per - 1, rows [lo, hi), and the row tiles of 256 up to their end.
+// Offsets are read as find_tile reads them.
+struct Spread {
+  int per, lo, hi, upto;
+};
+__device__ __forceinline__ int offset_at(const int32_t* offsets, int experts, int n, int e) {
+  if (e >= experts) return 0;
+  const int v = offsets[e + 1];
+  return v > n ? n : v;
+}
+__device__ __forceinline__ Spread spread(const int32_t* __restrict__ offsets, int experts, int n, int lane) {
+  Spread s;
+  s.per = (experts + 63) / 64;
+  int top = 0;
+  for (int i = 0; i < s.per; ++i) {
+    const int v = offset_at(offsets, experts, n, lane * s.per + i);
+    top = v > top ? v : top;
+  }
+  s.hi = wave_scan_max(top, lane);
+  s.lo = __shfl_up(s.hi, 1, 64);
+  if (lane == 0) s.lo = 0;
+  int run = s.lo, tiles = 0;
+  for (int i = 0; i < s.per; ++i) {
+    const int v = offset_at(offsets, experts, n, lane * s.per + i);
+    const int to = v > run ? v : run;
+    tiles += (to - run + 255) >> 8;
+    run = to;
+  }
+  s.upto = wave_scan_add(tiles, lane);
+  return s;
+}
+// Scalar read of an offset: the experts of a lane are told apart without the
+// vector loads' counter, behind which a tile's stores would be waited for.
+__device__ __forceinline__ int scalar_offset(const int32_t* offsets, int n, int e) {
+  typedef const int32_t __attribute__((address_space(4))) * scalar_ptr;
+  const int v = ((scalar_ptr)(uintptr_t)offsets)[__builtin_amdgcn_readfirstlane(e) + 1];
+  return v > n ? n : v;
+}
+
+// An output tile: rows (of the weight gradient: k) [begin, end) of expert e.
+struct Tile256 {
+  int e, begin, end;
+  int m0, n0;      // first output row (rows products: 0) and column
+};
+
+// Into scalar registers: divisions of scalars are done by the vector unit, which
+// would leave all that follows from them there.
+__device__ __forceinline__ void make_scalar(Tile256& t) {
+  t.e = __builtin_amdgcn_readfirstlane(t.e);
+  t.begin = __builtin_amdgcn_readfirstlane(t.begin);
+  t.end = __builtin_amdgcn_readfirstlane(t.end);
+  t.m0 = __builtin_amdgcn_readfirstlane(t.m0);
+  t.n0 = __builtin_amdgcn_readfirstlane(t.n0);
+}
+
+// Tile t of a rows product, t < tiles of all experts.  Within an expert eight
+// row tiles are walked before the next column tile, so that the blocks of an
+// XCD, which work on neighbours of its list, share rows and columns in its L2.
+__device__ __forceinline__ Tile256 rows_tile(const Spread& s, const int32_t* offsets, int experts, int n,
+                                             uint32_t tiles_n, uint32_t t) {
   constexpr int kRowGroup = 8;
-  int last = 0, lo = 0, hi = 0, upto = 0;
-  int64_t seen = 0;
-  for (int e0 = 0; e0 < experts; e0 += 64) {
-    hi = e0 + lane < experts ? offsets[e0 + lane + 1] : 0;
-    hi = hi > n ? n : hi;
-    hi = wave_scan_max(hi > last ? hi : last, lane);
-    lo = __shfl_up(hi, 1, 64);
-    if (lane == 0) lo = last;
-    upto = wave_scan_add((hi - lo + (1 << SH) - 1) >> SH, lane);
-    last = __builtin_amdgcn_readlane(hi, 63);
-    seen += __builtin_amdgcn_readlane(upto, 63);
-  }
-  const int64_t rest = (n - last + (1 << SH) - 1) >> SH;
-  const int64_t total = (seen + rest) * tiles_n, per = (total + 7) / 8;
-  const int64_t i = block >> 3, t = (block & 7) * per + i;
-  if (i >= per || t >= total) return false;
-  const int tm = (int)(t / tiles_n);   // the expert is that of row tile tm; its tiles are reordered below
-  int64_t first;                       // row tiles before the expert
-  int count;                           // and its own
-  int b, end;
-  if (tm >= seen) {
-    out.rows.e = experts;
-    first = seen;
-    count = (int)rest;
-    b = last;
-    end = n;
-  } else {
-    int from = 0;
-    first = 0;
-    for (int e0 = 0;; e0 += 64) {
-      if (experts > 64) {   // the offsets of this round again
-        hi = e0 + lane < experts ? offsets[e0 + lane + 1] : 0;
-        hi = hi > n ? n : hi;
-        hi = wave_scan_max(hi > from ? hi : from, lane);
-        lo = __shfl_up(hi, 1, 64);
-        if (lane == 0) lo = from;
-        upto = wave_scan_add((hi - lo + (1 << SH) - 1) >> SH, lane);
-      }
-      const uint64_t hit = __ballot(tm < first + upto);
-      if (hit) {
-        const int at = __ffsll((unsigned long long)hit) - 1;
-        out.rows.e = e0 + at;
-        b = __builtin_amdgcn_readlane(lo, at);
-        end = __builtin_amdgcn_readlane(hi, at);
-        count = (end - b + (1 << SH) - 1) >> SH;
-        first += __builtin_amdgcn_readlane(upto, at) - count;
-        break;
-      }
-      from = __builtin_amdgcn_readlane(hi, 63);
-      first += __builtin_amdgcn_readlane(upto, 63);
+  const int tm = (int)(t / tiles_n);
+  const uint64_t hit = __ballot(tm < s.upto);
+  const int at = __ffsll((unsigned long long)hit) - 1;
+  int run = __builtin_amdgcn_readlane(s.lo, at), to = __builtin_amdgcn_readlane(s.hi, at);
+  int first = at ? __builtin_amdgcn_readlane(s.upto, at - 1) : 0, e = at * s.per;
+  int count = (to - run + 255) >> 8;
+  if (s.per > 1) {
+    for (;; ++e) {
+      const int v = scalar_offset(offsets, n, e);
+      to = v > run ? v : run;
+      count = (to - run + 255) >> 8;
+      if (tm < first + count) break;
+      first += count;
+      run = to;
     }
   }
-  const int in = (int)(t - first * tiles_n);   // tile of the expert
-  const int group = in / (kRowGroup * tiles_n), at = in - group * kRowGroup * tiles_n;
+  const int in = (int)(t - (uint32_t)first * tiles_n);   // tile of the expert
+  const int group = in / (int)(kRowGroup * tiles_n), off = in - group * (int)(kRowGroup * tiles_n);
   const int wide = count - group * kRowGroup < kRowGroup ? count - group * kRowGroup : kRowGroup;
-  out.tn = at / wide;
-  out.rows.begin = b + ((int64_t)(group * kRowGroup + at % wide) << SH);
-  out.rows.end = out.rows.begin + (1 << SH) < end ? out.rows.begin + (1 << SH) : end;
-  return true;
+  Tile256 r;
+  r.e = e;
+  r.n0 = off / wide * 256;
+  r.m0 = 0;
+  r.begin = run + ((group * kRowGroup + off % wide) << 8);
+  r.end = r.begin + 256 < to ? r.begin + 256 : to;
+  make_scalar(r);
+  return r;
 }
 
-template <class S>
-__device__ __forceinline__ void store_tile(const f32x16_t (&acc)[S::MT][S::NT], bf16_t* out, int64_t row0, int m_left,
-                                           int n0, int N, int lane, int wy, int wx) {
-#pragma unroll
-  for (int i = 0; i < S::MT; ++i) {
-    const int r = wy * S::WM + 32 * i + (lane & 31);
-    if (r < m_left) {
-      bf16_t* row = out + (row0 + r) * N;
-#pragma unroll
-      for (int j = 0; j < S::NT; ++j)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int c = n0 + wx * S::WN + 32 * j + 8 * g + 4 * (lane >> 5);
-          const float v[4] = {acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
-          if (c < N) store4(row + c, 4, v);   // N is a multiple of 8 here
-        }
+// The lane again, as a value the compiler cannot see through: what follows from
+// it is worked out where it is used instead of being held in registers over the
+// whole walk.
+__device__ __forceinline__ int fresh(int lane) {
+  asm volatile("" : "+v"(lane));
+  return lane;
+}
+
+// A block's walk over the tiles that o.next() names, one after the other.  o
+// also gives a tile's operands (p, q), its k and, where its outputs go, its
+// first row and the rows left from there.
+template <class O>
+__device__ __forceinline__ void walk(char* lds_, int N, int lane0, int w, O& o) {
+  typedef typename O::Sh::Full Full;
+  typedef typename O::Sh::Flat Flat;
+  typedef typename O::Sh::Thin Thin;
+  MUON_LDS char* lds = (MUON_LDS char*)lds_;
+  typename O::PC cp;
+  typename O::QC cq;
+  Acc acc;
+  Tile256 cur, last, then;
+  bool some = false;
+  auto init = [&](const Tile256& t) {
+    const Operand p = o.p(t), q = o.q(t);
+    const int cut = o.cut(t), lane = fresh(lane0);
+    cp.init(p, cut == kFlat ? Flat::PR : Full::PR, lane, w);
+    cq.init(q, cut == kThin ? Thin::QR : Full::QR, lane, w);
+  };
+  auto look = [&](const Tile256& t) {
+    cp.look(o.p(t), o.cut(t) == kFlat ? Flat::PR : Full::PR, fresh(lane0), w);
+  };
+  auto store = [&](const Tile256& t) {
+    const int cut = o.cut(t);
+    const int row0 = cut == kFull ? w / Full::WGN * Full::WM : cut == kFlat ? w / Flat::WGN * Flat::WM
+                                                                           : w / Thin::WGN * Thin::WM;
+    const int col0 = cut == kThin ? w % Thin::WGN * Thin::WN : w % Full::WGN * Full::WN;
+    return tile_store(acc, cut == kFull ? 4 : 2, lds + Full::LDS + w * kStoreBytes, o.out(t), row0, o.m_left(t),
+                      t.n0 + col0, N, fresh(lane0));
+  };
+  bool more = o.next(cur);
+  if (more) {
+    look(cur);
+    init(cur);
+  }
+  while (more) {
+    const int cut = o.cut(cur), nk = (o.k(cur) + kBK - 1) / kBK, lane = fresh(lane0);
+    if (cut == kFull) tile_begin<Full>(lds, cp, cq, lane, w);
+    else if (cut == kFlat) tile_begin<Flat>(lds, cp, cq, lane, w);
+    else tile_begin<Thin>(lds, cp, cq, lane, w);
+    more = o.next(then);
+    if (more) look(then);
+    asm volatile("" ::: "memory");   // the stores stay behind the copies
+    int stored = 0;
+    if (some) stored = store(last);
+    asm volatile("" ::: "memory");
+    if (cut == kFull) tile_loop<Full>(acc, lds, cp, cq, nk, stored, lane, w);
+    else if (cut == kFlat) tile_loop<Flat>(acc, lds, cp, cq, nk, stored, lane, w);
+    else tile_loop<Thin>(acc, lds, cp, cq, nk, stored, lane, w);
+    last = cur;
+    some = true;
+    if (more) {
+      cur = then;
+      init(cur);
     }
   }
+  if (some) store(last);
 }
 
-template <class S>
-__device__ __forceinline__ void zero_tile(bf16_t* out, int64_t row0, int m_left, int n0, int N) {
-  const int chunks = (N - n0 < S::BN ? N - n0 : S::BN) / 8;
-  for (int i = threadIdx.x; i < m_left * chunks; i += S::THREADS)
-    *reinterpret_cast<u32x4*>(out + (row0 + i / chunks) * N + n0 + 8 * (i % chunks)) = u32x4{0u, 0u, 0u, 0u};
+// Zero to rows x cols elements at out (rows of N): by the threads of one block.
+__device__ __forceinline__ void zero_block(bf16_t* out, int64_t rows, int cols, int64_t N) {
+  const int chunks = cols / 8;
+  for (int64_t i = threadIdx.x; i < rows * chunks; i += 512)
+    *reinterpret_cast<u32x4*>(out + i / chunks * N + 8 * (i % chunks)) = u32x4{0u, 0u, 0u, 0u};
 }
 
-template <class S, int SH, int MODE>
-__global__ __launch_bounds__(S::THREADS, 2) void k_rows_product(ProdArgs a) {
-  __shared__ __attribute__((aligned(16))) char lds[S::LDS];
+template <int MODE>
+struct RowsWalk {
+  static constexpr bool QT = MODE == kInputGrad;
+  typedef Shapes<false, QT> Sh;
+  typedef RowCopies PC;
+  typedef typename std::conditional<QT, KCopies<false>, RowCopies>::type QC;
+  const ProdArgs& a;
+  const Spread& s;
+  uint32_t i, end;   // the next tile and the last but one
+  __device__ __forceinline__ bool next(Tile256& t) {
+    if (i >= end) return false;
+    t = rows_tile(s, a.offsets, a.experts, (int)a.n, a.tiles_n, i);
+    i += kWalkers / 8;
+    return true;
+  }
+  __device__ __forceinline__ int m_left(const Tile256& t) const { return t.end - t.begin; }
+  __device__ __forceinline__ int cut(const Tile256& t) const { return cut_of(t.end - t.begin, a.N - t.n0); }
+  __device__ __forceinline__ int k(const Tile256&) const { return a.K; }
+  __device__ __forceinline__ bf16_t* out(const Tile256& t) const {
+    return static_cast<bf16_t*>(a.out) + (int64_t)t.begin * a.N;
+  }
+  __device__ __forceinline__ Operand p(const Tile256& t) const {
+    const char* x = static_cast<const char*>(a.p);
+    if (a.rows) return Operand{x, a.rows + t.begin, (int32_t)a.x_rows, m_left(t), 0, a.K};
+    return Operand{x + (int64_t)t.begin * a.K * 2, nullptr, 0, m_left(t), 0, a.K};
+  }
+  __device__ __forceinline__ Operand q(const Tile256& t) const {
+    const char* x = static_cast<const char*>(a.q) + (int64_t)t.e * a.N * a.K * 2;
+    if (QT) return Operand{x, nullptr, 0, a.K, t.n0, a.N};
+    return Operand{x + (int64_t)t.n0 * a.K * 2, nullptr, 0, a.N - t.n0, 0, a.K};
+  }
+};
+
+template <int MODE>
+__global__ __launch_bounds__(512, 2) void k_rows_product(ProdArgs a) {
+  __shared__ __attribute__((aligned(16))) char lds[RowsWalk<MODE>::Sh::LDS];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  Place p;
-  if (!find_place<SH>(a.offsets, a.experts, (int)a.n, a.tiles_n, blockIdx.x, lane, p)) return;
-  const int m_left = (int)(p.rows.end - p.rows.begin), n0 = p.tn * S::BN;
-  bf16_t* out = static_cast<bf16_t*>(a.out);
-  if (p.rows.e == a.experts) {
-    zero_tile<S>(out, p.rows.begin, m_left, n0, a.N);
-    return;
-  }
-  const char* pb = static_cast<const char*>(a.p);
-  const char* wb = static_cast<const char*>(a.q) + (int64_t)p.rows.e * a.N * a.K * 2;
-  RowCopies<S::PR> cp;
-  if (a.rows) cp.init(Operand{pb, a.rows + p.rows.begin, a.x_rows, m_left, 0, a.K}, lane, w);
-  else cp.init(Operand{pb + p.rows.begin * a.K * 2, nullptr, 0, m_left, 0, a.K}, lane, w);
-  f32x16_t acc[S::MT][S::NT];
-  const int nk = (a.K + kBK - 1) / kBK;
-  if constexpr (S::QT) {
-    KCopies<S::BN, S::QR, false> cq;
-    cq.init(Operand{wb, nullptr, 0, a.K, n0, a.N}, lane, w);
-    tile_loop<S>(acc, (MUON_LDS char*)lds, cp, cq, nk, lane, w);
-  } else {
-    RowCopies<S::QR> cq;
-    cq.init(Operand{wb + (int64_t)n0 * a.K * 2, nullptr, 0, a.N - n0, 0, a.K}, lane, w);
-    tile_loop<S>(acc, (MUON_LDS char*)lds, cp, cq, nk, lane, w);
-  }
-  store_tile<S>(acc, out, p.rows.begin, m_left, n0, a.N, lane, w / S::WGN, w % S::WGN);
+  const Spread s = spread(a.offsets, a.experts, (int)a.n, lane);
+  const uint32_t total = (uint32_t)__builtin_amdgcn_readlane(s.upto, 63) * (uint32_t)a.tiles_n, per = (total + 7) / 8;
+  const uint32_t first = (blockIdx.x & 7) * per, end = first + per < total ? first + per : total;
+  RowsWalk<MODE> o{a, s, first + (blockIdx.x >> 3), end};
+  walk(lds, a.N, lane, w, o);
+  // the rows past the last expert's, 64 at a time
+  const int64_t last = __builtin_amdgcn_readlane(s.hi, 63);
+  for (int64_t r = last + 64 * (int64_t)blockIdx.x; r < a.n; r += 64 * kWalkers)
+    zero_block(static_cast<bf16_t*>(a.out) + r * a.N, a.n - r < 64 ? a.n - r : 64, a.N, a.N);
 }
 
-// Weight gradient.  An expert's tiles are dealt to the XCDs in runs, so that
-// a popular expert's work is spread over all of them.
-template <class S, bool GATHER>
-__global__ __launch_bounds__(S::THREADS, 2) void k_weight_product(ProdArgs a) {
-  __shared__ __attribute__((aligned(16))) char lds[S::LDS];
+// Weight gradient.  The experts' tiles in order of their rows' number, longest
+// first (where a lane has each expert), are dealt to the XCDs in sets of at
+// most 32 neighbours of one expert, which an XCD's 32 CUs take at once, sharing
+// rows in its L2.
+template <bool GATHER>
+struct WeightWalk {
+  typedef Shapes<true, true> Sh;
+  typedef KCopies<false> PC;
+  typedef KCopies<GATHER> QC;
+  const ProdArgs& a;
+  const Spread& s;
+  int rank;                      // of the lane's expert
+  uint32_t i, sets, size;        // the next place of the XCD's list; sets of an expert, tiles of a set
+  __device__ __forceinline__ bool next(Tile256& r) {
+    const uint32_t tiles = (uint32_t)a.tiles_m * (uint32_t)a.tiles_n;
+    for (;;) {
+      const uint32_t j = i / size, set = j * 8 + (blockIdx.x & 7);
+      const uint32_t q = __builtin_amdgcn_readfirstlane(set / sets), t = (set - q * sets) * size + (i - j * size);
+      if (q >= (uint32_t)a.experts) return false;
+      i += kWalkers / 8;
+      if (t >= tiles) continue;
+      if (s.per == 1) {
+        r.e = __ffsll((unsigned long long)__ballot(rank == (int)q)) - 1;
+        r.begin = __builtin_amdgcn_readlane(s.lo, r.e);
+        r.end = __builtin_amdgcn_readlane(s.hi, r.e);
+      } else {
+        const int at = (int)q / s.per;
+        r.e = at * s.per;
+        r.begin = r.end = __builtin_amdgcn_readlane(s.lo, at);
+        for (;; ++r.e) {
+          const int v = scalar_offset(a.offsets, (int)a.n, r.e);
+          r.end = v > r.begin ? v : r.begin;
+          if (r.e == (int)q) break;
+          r.begin = r.end;
+        }
+      }
+      const int tm = (int)(t / (uint32_t)a.tiles_n);
+      r.m0 = tm * 256;
+      r.n0 = (int)(t - (uint32_t)tm * a.tiles_n) * 256;
+      make_scalar(r);
+      if (r.end > r.begin) return true;
+      // no rows: zeros, whose stores come before those of the tile at hand and so are waited for with it
+      zero_block(out(r) + r.n0, m_left(r), a.N - r.n0 < 256 ? a.N - r.n0 : 256, a.N);
+    }
+  }
+  __device__ __forceinline__ int m_left(const Tile256& t) const { return a.M - t.m0 < 256 ? a.M - t.m0 : 256; }
+  __device__ __forceinline__ int cut(const Tile256& t) const { return cut_of(a.M - t.m0, a.N - t.n0); }
+  __device__ __forceinline__ int k(const Tile256& t) const { return t.end - t.begin; }
+  __device__ __forceinline__ bf16_t* out(const Tile256& t) const {
+    return static_cast<bf16_t*>(a.out) + ((int64_t)t.e * a.M + t.m0) * a.N;
+  }
+  __device__ __forceinline__ Operand p(const Tile256& t) const {
+    return Operand{static_cast<const char*>(a.p) + (int64_t)t.begin * a.M * 2, nullptr, 0, k(t), t.m0, a.M};
+  }
+  __device__ __forceinline__ Operand q(const Tile256& t) const {
+    const char* x = static_cast<const char*>(a.q);
+    if (GATHER) return Operand{x, a.rows + t.begin, (int32_t)a.x_rows, k(t), t.n0, a.N};
+    return Operand{x + (int64_t)t.begin * a.N * 2, nullptr, 0, k(t), t.n0, a.N};
+  }
+};
+
+template <bool GATHER>
+__global__ __launch_bounds__(512, 2) void k_weight_product(ProdArgs a) {
+  __shared__ __attribute__((aligned(16))) char lds[WeightWalk<GATHER>::Sh::LDS];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int tiles = a.tiles_m * a.tiles_n;
-  int e, t;
-  if (tiles >= 64) {
-    const int run = (tiles + 7) / 8, i = blockIdx.x >> 3;
-    e = i / run;
-    t = (blockIdx.x & 7) * run + i - e * run;
-    if (t >= tiles) return;
-  } else {
-    e = blockIdx.x / tiles;
-    t = blockIdx.x - e * tiles;
+  const Spread s = spread(a.offsets, a.experts, (int)a.n, lane);
+  int rank = lane;
+  if (s.per == 1) {
+    const int mine = s.hi - s.lo;
+    rank = 0;
+    for (int j = 0; j < 64; ++j) {
+      const int other = __builtin_amdgcn_readlane(mine, j);
+      rank += other > mine || (other == mine && j < lane);
+    }
   }
-  if (e >= a.experts) return;
-  const int m0 = t / a.tiles_n * S::BM, n0 = t % a.tiles_n * S::BN;
-  int64_t b, end;
-  expert_rows(a.offsets, e, (int)a.n, lane, b, end);
-  const int K = (int)(end - b), m_left = a.M - m0 < S::BM ? a.M - m0 : S::BM;
-  bf16_t* out = static_cast<bf16_t*>(a.out);
-  const int64_t row0 = (int64_t)e * a.M + m0;
-  if (K == 0) {
-    zero_tile<S>(out, row0, m_left, n0, a.N);
-    return;
-  }
-  f32x16_t acc[S::MT][S::NT];
-  KCopies<S::BM, S::PR, false> cp;
-  KCopies<S::BN, S::QR, GATHER> cq;
-  cp.init(Operand{static_cast<const char*>(a.p) + b * a.M * 2, nullptr, 0, K, m0, a.M}, lane, w);
-  if (GATHER) cq.init(Operand{static_cast<const char*>(a.q), a.rows + b, a.x_rows, K, n0, a.N}, lane, w);
-  else cq.init(Operand{static_cast<const char*>(a.q) + b * a.N * 2, nullptr, 0, K, n0, a.N}, lane, w);
-  tile_loop<S>(acc, (MUON_LDS char*)lds, cp, cq, (K + kBK - 1) / kBK, lane, w);
-  store_tile<S>(acc, out, row0, m_left, n0, a.N, lane, w / S::WGN, w % S::WGN);
+  const uint32_t tiles = (uint32_t)a.tiles_m * (uint32_t)a.tiles_n, sets = (tiles + 31) / 32;
+  WeightWalk<GATHER> o{a, s, rank, blockIdx.x >> 3, sets, (tiles + sets - 1) / sets};
+  walk(lds, a.N, lane, w, o);
 }
 
 // --------------------------------------------------------------------- host
@@ -571,24 +718,22 @@ bool chunked(const ProdArgs& a, int dtype, int64_t c0, int64_t c1, int64_t gathe
          c0 < (1 << 21) && c1 < (1 << 21) && (!a.rows || a.x_rows * gathered_cols < (int64_t(1) << 30));
 }
 
-template <class S, int SH, int MODE>
+template <int MODE>
 int launch_rows(ProdArgs a, hipStream_t s) {
-  a.tiles_n = (int32_t)ceil_div(a.N, S::BN);
-  const int64_t blocks = 8 * ceil_div(row_tiles(a.n, a.experts, S::BM) * a.tiles_n, 8);
-  if (blocks > kMaxCount) return fail(MUON_EUNSUPPORTED, "more than 2^31 output tiles");
-  hipLaunchKernelGGL((k_rows_product<S, SH, MODE>), dim3((uint32_t)blocks), dim3(S::THREADS), 0, s, a);
+  a.tiles_n = (int32_t)ceil_div(a.N, 256);
+  if (row_tiles(a.n, a.experts, 256) * a.tiles_n > kMaxCount)
+    return fail(MUON_EUNSUPPORTED, "more than 2^31 output tiles");
+  hipLaunchKernelGGL((k_rows_product<MODE>), dim3(kWalkers), dim3(512), 0, s, a);
   return launch_status("grouped product launch");
 }
 
-template <class S>
 int launch_weight(ProdArgs a, hipStream_t s) {
-  a.tiles_m = (int32_t)ceil_div(a.M, S::BM);
-  a.tiles_n = (int32_t)ceil_div(a.N, S::BN);
-  const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
-  const int64_t blocks = a.experts * (tiles >= 64 ? 8 * ceil_div(tiles, 8) : tiles);
-  if (blocks > kMaxCount) return fail(MUON_EUNSUPPORTED, "more than 2^31 output tiles");
-  if (a.rows) hipLaunchKernelGGL((k_weight_product<S, true>), dim3((uint32_t)blocks), dim3(S::THREADS), 0, s, a);
-  else hipLaunchKernelGGL((k_weight_product<S, false>), dim3((uint32_t)blocks), dim3(S::THREADS), 0, s, a);
+  a.tiles_m = (int32_t)ceil_div(a.M, 256);
+  a.tiles_n = (int32_t)ceil_div(a.N, 256);
+  if ((int64_t)a.experts * a.tiles_m * a.tiles_n > kMaxCount / 2)   // 32 sets of 17 tiles are counted as 32 x 32 at most
+    return fail(MUON_EUNSUPPORTED, "more than 2^30 output tiles");
+  if (a.rows) hipLaunchKernelGGL((k_weight_product<true>), dim3(kWalkers), dim3(512), 0, s, a);
+  else hipLaunchKernelGGL((k_weight_product<false>), dim3(kWalkers), dim3(512), 0, s, a);
   return launch_status("grouped weight gradient launch");
 }
 
@@ -616,7 +761,7 @@ int muon_grouped_matmul(const void* x, const void* w, const int32_t* offsets, co
   if ((rc = check_device())) return rc;
   ProdArgs a = {x, w, y, offsets, rows, n, x_rows, experts, 0, (int32_t)outer, (int32_t)inner, 0, 0};
   if (chunked(a, dtype, inner, outer, inner))
-    return launch_rows<Shape<256, 256, 2, 4, false, false>, 8, kMatmul>(a, static_cast<hipStream_t>(stream));
+    return launch_rows<kMatmul>(a, static_cast<hipStream_t>(stream));
   return launch_product<kMatmul>(a, dtype, row_tiles(n, experts, side(dtype)), static_cast<hipStream_t>(stream));
 }
 
@@ -630,7 +775,7 @@ int muon_grouped_input_grad(const void* dy, const void* w, const int32_t* offset
   if ((rc = check_device())) return rc;
   ProdArgs a = {dy, w, dx, offsets, nullptr, n, n, experts, 0, (int32_t)inner, (int32_t)outer, 0, 0};
   if (chunked(a, dtype, inner, outer, inner))
-    return launch_rows<Shape<256, 256, 2, 4, false, true>, 8, kInputGrad>(a, static_cast<hipStream_t>(stream));
+    return launch_rows<kInputGrad>(a, static_cast<hipStream_t>(stream));
   return launch_product<kInputGrad>(a, dtype, row_tiles(n, experts, side(dtype)), static_cast<hipStream_t>(stream));
 }
 
@@ -668,7 +813,7 @@ int muon_grouped_weight_grad(const void* dy, const void* x, const void* q, const
     x = workspace;
   }
   ProdArgs a = {dy, x, dw, offsets, rows, n, x_rows, experts, (int32_t)outer, (int32_t)inner, 0, 0, 0};
-  if (chunked(a, dtype, inner, outer, inner)) return launch_weight<Shape<256, 256, 2, 4, true, true>>(a, s);
+  if (chunked(a, dtype, inner, outer, inner)) return launch_weight(a, s);
   a.tiles_m = (int32_t)ceil_div(outer, side(dtype));
   return launch_product<kWeightGrad>(a, dtype, (int64_t)experts * a.tiles_m, s);
 }
