@@ -10,7 +10,9 @@
 
 #include <type_traits>
 
+#include "expert_few.hpp"
 #include "expert_mfma.hpp"
+#include "expert_tiles.hpp"
 #include "experts.hpp"
 #include "mfma_nt.hpp"
 
@@ -26,95 +28,6 @@ using nt::bf16x8_t;
 using nt::f32x16_t;
 using nt::s16x4_t;
 using nt::u32x2_t;
-
-enum Mode { kMatmul = 0, kInputGrad = 1, kWeightGrad = 2 };
-
-struct ProdArgs {
-  const void* p;            // x, dy, dy
-  const void* q;            // W, W, x
-  void* out;
-  const int32_t* offsets;
-  const int32_t* rows;      // gather of x's rows, or null
-  int64_t n, x_rows;
-  int32_t experts;
-  int32_t M, N, K;          // M: weight grad only; K: not in the weight grad
-  int32_t tiles_m, tiles_n; // tiles_m: weight grad only
-};
-
-// Tile t of the rows cut by expert into tiles of 2^SH: expert and rows
-// [begin, end) of the tile, end at most begin + 2^SH.  The rows past the last
-// expert's are cut the same way, as those of expert `experts`.  Offsets are
-// taken as their running maximum in [0, n], so that no input leads out of
-// bounds.  Every wave of a block calls this with the same t; false: no such
-// tile.
-struct RowTile {
-  int e;
-  int64_t begin, end;
-};
-template <int SH>
-__device__ __forceinline__ bool find_tile(const int32_t* __restrict__ offsets, int experts, int n, int64_t t, int lane,
-                                          RowTile& out) {
-  int last = 0;       // end of the experts before this round of 64
-  int64_t seen = 0;   // their tiles
-  for (int e0 = 0; e0 < experts; e0 += 64) {
-    int hi = e0 + lane < experts ? offsets[e0 + lane + 1] : 0;
-    hi = hi > n ? n : hi;
-    hi = wave_scan_max(hi > last ? hi : last, lane);
-    int lo = __shfl_up(hi, 1, 64);
-    if (lane == 0) lo = last;
-    const int tiles = (hi - lo + (1 << SH) - 1) >> SH;
-    const int upto = wave_scan_add(tiles, lane);
-    const uint64_t hit = __ballot(t < seen + upto);
-    if (hit) {
-      const int at = __ffsll((unsigned long long)hit) - 1;
-      const int b = __builtin_amdgcn_readlane(lo, at), e = __builtin_amdgcn_readlane(hi, at);
-      const int before = __builtin_amdgcn_readlane(upto - tiles, at);
-      out.e = e0 + at;
-      out.begin = b + ((t - seen - before) << SH);
-      out.end = out.begin + (1 << SH) < e ? out.begin + (1 << SH) : e;
-      return true;
-    }
-    last = __builtin_amdgcn_readlane(hi, 63);
-    seen += __builtin_amdgcn_readlane(upto, 63);
-  }
-  out.e = experts;
-  out.begin = last + ((t - seen) << SH);
-  out.end = out.begin + (1 << SH) < n ? out.begin + (1 << SH) : n;
-  return out.begin < n;
-}
-
-// Rows [begin, end) of expert e, by the same reading of offsets.
-__device__ __forceinline__ void expert_rows(const int32_t* __restrict__ offsets, int e, int n, int lane, int64_t& begin,
-                                            int64_t& end) {
-  int b = 0, m = 0;   // maxima of offsets[1..e] and of offsets[1..e+1]
-  for (int i = lane; i <= e; i += 64) {
-    const int v = offsets[i + 1];
-    m = v > m ? v : m;
-    if (i < e) b = v > b ? v : b;
-  }
-  b = (int)wave_max((uint32_t)b);
-  m = (int)wave_max((uint32_t)m);
-  begin = b < n ? b : n;
-  end = m < n ? m : n;
-}
-
-// 16 bytes from any address, of which the first cnt elements exist.
-__device__ __forceinline__ u32x4 load16(const bf16_t* p, int cnt) {
-  if (cnt >= 8) return *reinterpret_cast<const u32x4_any*>(p);
-  u32x4 v = {0u, 0u, 0u, 0u};
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < cnt) v[i / 2] |= (uint32_t)p[i].bits << (16 * (i % 2));
-  return v;
-}
-__device__ __forceinline__ u32x4 load16(const float* p, int cnt) {
-  if (cnt >= 4) return *reinterpret_cast<const u32x4_any*>(p);
-  u32x4 v = {0u, 0u, 0u, 0u};
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (i < cnt) v[i] = __float_as_uint(p[i]);
-  return v;
-}
 
 // Tile geometry of one type.  An operand's tile has `B` rows of BK elements
 // (k-contiguous) or BK rows of B elements (k-major), cut into 16-byte chunks.
@@ -245,26 +158,6 @@ __device__ __forceinline__ f32x16_t multiply(u32x4 q, u32x4 p, f32x16_t acc, flo
   for (int i = 0; i < 4; ++i)
     acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(q[i]), __uint_as_float(p[i]), acc, 0, 0, 0);
   return acc;
-}
-
-__device__ __forceinline__ void store4(bf16_t* p, int cnt, const float* v) {
-  if (cnt >= 4) {
-    *reinterpret_cast<u32x2_any*>(p) = u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])};
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < cnt) store1(p + i, v[i]);
-  }
-}
-__device__ __forceinline__ void store4(float* p, int cnt, const float* v) {
-  if (cnt >= 4) {
-    *reinterpret_cast<u32x4_any*>(p) =
-        u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < cnt) p[i] = v[i];
-  }
 }
 
 // One output tile per block of 4 waves (2 x 2), two LDS stages: the next
@@ -709,6 +602,34 @@ int launch_product(ProdArgs a, int dtype, int64_t tiles_m, hipStream_t s) {
   return launch_status("grouped product launch");
 }
 
+// Whether the kernels for few rows take a rows product (and their blocks): where
+// an expert has so few rows that its matrix's way from memory is what counts, or
+// where the tile kernels would leave most CUs idle for one tile's length.
+// Measured against the faster tile kernel, us:
+//   n / experts 4, bf16, 64 x 2816 x 2048: 142 against 154 (input gradient 125, 128); at 8: 174, 164 (149, 133)
+//   16, fp32, 64 x 1408 x 1024: 127 against 142 (93, 126); at 32: 180, 158 (142, 157)
+//   blocks 1280, 8 x 1024 x 1024, bf16 18 against 18, fp32 32 against 34; 2560: 29, 23 and 55, 50
+//   blocks 513, fp32, 8 x 257 x 513: 13 against 20
+template <int MODE>
+bool few(const ProdArgs& a, int dtype, int64_t* blocks) {
+  *blocks = row_tiles(a.n, a.experts, 16) * ceil_div(a.N, MODE == kMatmul ? 32 : 64);
+  return *blocks <= 1280 || (a.n <= (dtype == MUON_BF16 ? 4 : 16) * (int64_t)a.experts && *blocks <= kMaxCount);
+}
+
+template <int MODE>
+int launch_few(ProdArgs a, int dtype, int64_t blocks, hipStream_t s) {
+  a.tiles_n = (int32_t)ceil_div(a.N, MODE == kMatmul ? 32 : 64);
+  const dim3 grid((uint32_t)blocks);
+  if (MODE == kMatmul) {
+    if (dtype == MUON_BF16) hipLaunchKernelGGL((k_few_matmul<bf16_t, 2>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_few_matmul<float, 2>), grid, dim3(256), 0, s, a);
+  } else {
+    if (dtype == MUON_BF16) hipLaunchKernelGGL((k_few_input_grad<bf16_t>), grid, dim3(512), 0, s, a);
+    else hipLaunchKernelGGL((k_few_input_grad<float>), grid, dim3(512), 0, s, a);
+  }
+  return launch_status("grouped product launch");
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // The large kernels copy 16-byte chunks that a row holds whole and address an
@@ -760,6 +681,8 @@ int muon_grouped_matmul(const void* x, const void* w, const int32_t* offsets, co
   if ((!x && x_rows) || !w || !offsets || !y) return fail(MUON_EINVAL, "NULL pointer");
   if ((rc = check_device())) return rc;
   ProdArgs a = {x, w, y, offsets, rows, n, x_rows, experts, 0, (int32_t)outer, (int32_t)inner, 0, 0};
+  int64_t blocks;
+  if (few<kMatmul>(a, dtype, &blocks)) return launch_few<kMatmul>(a, dtype, blocks, static_cast<hipStream_t>(stream));
   if (chunked(a, dtype, inner, outer, inner))
     return launch_rows<kMatmul>(a, static_cast<hipStream_t>(stream));
   return launch_product<kMatmul>(a, dtype, row_tiles(n, experts, side(dtype)), static_cast<hipStream_t>(stream));
@@ -774,6 +697,8 @@ int muon_grouped_input_grad(const void* dy, const void* w, const int32_t* offset
   if (!dy || !w || !offsets || !dx) return fail(MUON_EINVAL, "NULL pointer");
   if ((rc = check_device())) return rc;
   ProdArgs a = {dy, w, dx, offsets, nullptr, n, n, experts, 0, (int32_t)inner, (int32_t)outer, 0, 0};
+  int64_t blocks;
+  if (few<kInputGrad>(a, dtype, &blocks)) return launch_few<kInputGrad>(a, dtype, blocks, static_cast<hipStream_t>(stream));
   if (chunked(a, dtype, inner, outer, inner))
     return launch_rows<kInputGrad>(a, static_cast<hipStream_t>(stream));
   return launch_product<kInputGrad>(a, dtype, row_tiles(n, experts, side(dtype)), static_cast<hipStream_t>(stream));
@@ -813,7 +738,10 @@ int muon_grouped_weight_grad(const void* dy, const void* x, const void* q, const
     x = workspace;
   }
   ProdArgs a = {dy, x, dw, offsets, rows, n, x_rows, experts, (int32_t)outer, (int32_t)inner, 0, 0, 0};
-  if (chunked(a, dtype, inner, outer, inner)) return launch_weight(a, s);
+  // fewer than a large tile a CU, and few rows: the small tiles' blocks are more and start faster (8 x 1024 x 1024,
+  // n 8 to 256: 9 to 11 us against 12 to 13; n 1024: 18 against 17)
+  const bool small = (int64_t)experts * ceil_div(outer, 256) * ceil_div(inner, 256) <= kWalkers && n <= 64 * (int64_t)experts;
+  if (!small && chunked(a, dtype, inner, outer, inner)) return launch_weight(a, s);
   a.tiles_m = (int32_t)ceil_div(outer, side(dtype));
   return launch_product<kWeightGrad>(a, dtype, (int64_t)experts * a.tiles_m, s);
 }
