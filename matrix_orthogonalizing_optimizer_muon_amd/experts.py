@@ -16,6 +16,7 @@ then owns the outputs; inputs made on another stream have to be waited for
 before, and kept until this one is done with them, as with any tensor.
 """
 import ctypes
+import functools
 from typing import NamedTuple
 
 import torch
@@ -161,6 +162,13 @@ def _ptr(t):
 
 # --------------------------------------------------------------------- routing
 
+@functools.lru_cache(maxsize=256)
+def _route_workspace(tokens, experts):
+    need = ctypes.c_uint64()
+    L.check(L.lib().muon_route_workspace(tokens, experts, ctypes.byref(need)))
+    return need.value
+
+
 @_on
 def route(logits, k, *, normalize=True):
     """The k largest of each token's logits (T x E), ties to the lowest expert, and the
@@ -178,11 +186,10 @@ def route(logits, k, *, normalize=True):
     slots = torch.empty_like(chosen)
     rows = logits.new_empty(tokens * k, dtype=_I32)
     offsets = logits.new_empty(experts + 1, dtype=_I32)
-    need = ctypes.c_uint64()
-    L.check(lib.muon_route_workspace(tokens, experts, ctypes.byref(need)))
-    ws = logits.new_empty(need.value, dtype=torch.uint8) if need.value else None
+    need = _route_workspace(tokens, experts)
+    ws = logits.new_empty(need, dtype=torch.uint8) if need else None
     _call(dev, lib.muon_route, _ptr(logits), code, tokens, experts, k, 1 if normalize else 0, _ptr(weights),
-          _ptr(chosen), _ptr(slots), _ptr(rows), _ptr(offsets), _ptr(ws) if ws is not None else None, need.value)
+          _ptr(chosen), _ptr(slots), _ptr(rows), _ptr(offsets), _ptr(ws) if ws is not None else None, need)
     return Routing(weights, chosen, slots, rows, offsets)
 
 
