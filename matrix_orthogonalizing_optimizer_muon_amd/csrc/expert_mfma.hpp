@@ -151,8 +151,8 @@ struct KCopies {
   // the indices of tile kt
   __device__ __forceinline__ void ahead(int kt, int lane, int w) {
     if constexpr (GATHER) {
-      const int k = kt * kBK + w * 8 + lane % 8;   // rows + 256 stays below 2^31 where rows does
-      idx = k < rows ? gather[k] : -1;
+      const uint32_t k = (uint32_t)kt * kBK + w * 8 + lane % 8;   // unsigned: up to 256 past rows < 2^31
+      idx = k < (uint32_t)rows ? gather[k] : -1;
     }
   }
   template <int NR, int U = 0>

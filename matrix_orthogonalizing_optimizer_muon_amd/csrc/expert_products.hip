@@ -279,6 +279,7 @@ __device__ __forceinline__ int cut_of(int m_left, int n_left) {
 // The experts' rows held across a wave: lane l has those of experts l per to
 // (l + 1) per - 1, rows [lo, hi), and the row tiles of 256 up to their end.
 // Offsets are read as find_tile reads them.
+__device__ __forceinline__ int row_tiles_of(int rows) { return (int)(((uint32_t)rows + 255) >> 8); }
 struct Spread {
   int per, lo, hi, upto;
 };
@@ -302,7 +303,7 @@ __device__ __forceinline__ Spread spread(const int32_t* __restrict__ offsets, in
   for (int i = 0; i < s.per; ++i) {
     const int v = offset_at(offsets, experts, n, lane * s.per + i);
     const int to = v > run ? v : run;
-    tiles += (to - run + 255) >> 8;
+    tiles += row_tiles_of(to - run);
     run = to;
   }
   s.upto = wave_scan_add(tiles, lane);
@@ -343,12 +344,12 @@ __device__ __forceinline__ Tile256 rows_tile(const Spread& s, const int32_t* off
   const int at = __ffsll((unsigned long long)hit) - 1;
   int run = __builtin_amdgcn_readlane(s.lo, at), to = __builtin_amdgcn_readlane(s.hi, at);
   int first = at ? __builtin_amdgcn_readlane(s.upto, at - 1) : 0, e = at * s.per;
-  int count = (to - run + 255) >> 8;
+  int count = row_tiles_of(to - run);
   if (s.per > 1) {
     for (;; ++e) {
       const int v = scalar_offset(offsets, n, e);
       to = v > run ? v : run;
-      count = (to - run + 255) >> 8;
+      count = row_tiles_of(to - run);
       if (tm < first + count) break;
       first += count;
       run = to;
@@ -362,7 +363,7 @@ __device__ __forceinline__ Tile256 rows_tile(const Spread& s, const int32_t* off
   r.n0 = off / wide * 256;
   r.m0 = 0;
   r.begin = run + ((group * kRowGroup + off % wide) << 8);
-  r.end = r.begin + 256 < to ? r.begin + 256 : to;
+  r.end = to - r.begin > 256 ? r.begin + 256 : to;
   make_scalar(r);
   return r;
 }
@@ -412,7 +413,7 @@ __device__ __forceinline__ void walk(char* lds_, int N, int lane0, int w, O& o) 
     init(cur);
   }
   while (more) {
-    const int cut = o.cut(cur), nk = (o.k(cur) + kBK - 1) / kBK, lane = fresh(lane0);
+    const int cut = o.cut(cur), nk = (int)(((uint32_t)o.k(cur) + kBK - 1) / kBK), lane = fresh(lane0);
     if (cut == kFull) tile_begin<Full>(lds, cp, cq, lane, w);
     else if (cut == kFlat) tile_begin<Flat>(lds, cp, cq, lane, w);
     else tile_begin<Thin>(lds, cp, cq, lane, w);
@@ -493,7 +494,9 @@ __global__ __launch_bounds__(512, 2) void k_rows_product(ProdArgs a) {
 // Weight gradient.  The experts' tiles in order of their rows' number, longest
 // first (where a lane has each expert), are dealt to the XCDs in sets of at
 // most 32 neighbours of one expert, which an XCD's 32 CUs take at once, sharing
-// rows in its L2.
+// rows in its L2.  Sets go to the XCDs, and an XCD's tiles to its CUs, in turn
+// there and back, so that none has the longer one of every round (4096 tokens,
+// 8 of 64 experts, uneven, 2048 x 1408: mean over longest 0.79 -> 0.83, 272 -> 260 us).
 template <bool GATHER>
 struct WeightWalk {
   typedef Shapes<true, true> Sh;
@@ -502,12 +505,14 @@ struct WeightWalk {
   const ProdArgs& a;
   const Spread& s;
   int rank;                      // of the lane's expert
-  uint32_t i, sets, size;        // the next place of the XCD's list; sets of an expert, tiles of a set
+  uint32_t i, sets, size;        // the XCD's places so far; sets of an expert, tiles of a set
   __device__ __forceinline__ bool next(Tile256& r) {
     const uint32_t tiles = (uint32_t)a.tiles_m * (uint32_t)a.tiles_n;
     for (;;) {
-      const uint32_t j = i / size, set = j * 8 + (blockIdx.x & 7);
-      const uint32_t q = __builtin_amdgcn_readfirstlane(set / sets), t = (set - q * sets) * size + (i - j * size);
+      const uint32_t cu = blockIdx.x >> 3, xcd = blockIdx.x & 7;
+      const uint32_t place = i + (i / 32 & 1 ? 31 - cu : cu);
+      const uint32_t j = place / size, set = j * 8 + (j & 1 ? 7 - xcd : xcd);
+      const uint32_t q = __builtin_amdgcn_readfirstlane(set / sets), t = (set - q * sets) * size + (place - j * size);
       if (q >= (uint32_t)a.experts) return false;
       i += kWalkers / 8;
       if (t >= tiles) continue;
@@ -566,7 +571,7 @@ __global__ __launch_bounds__(512, 2) void k_weight_product(ProdArgs a) {
     }
   }
   const uint32_t tiles = (uint32_t)a.tiles_m * (uint32_t)a.tiles_n, sets = (tiles + 31) / 32;
-  WeightWalk<GATHER> o{a, s, rank, blockIdx.x >> 3, sets, (tiles + sets - 1) / sets};
+  WeightWalk<GATHER> o{a, s, rank, 0, sets, (tiles + sets - 1) / sets};
   walk(lds, a.N, lane, w, o);
 }
 

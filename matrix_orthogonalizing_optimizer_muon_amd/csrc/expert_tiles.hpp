@@ -41,7 +41,7 @@ __device__ __forceinline__ bool find_tile(const int32_t* __restrict__ offsets, i
     hi = wave_scan_max(hi > last ? hi : last, lane);
     int lo = __shfl_up(hi, 1, 64);
     if (lane == 0) lo = last;
-    const int tiles = (hi - lo + (1 << SH) - 1) >> SH;
+    const int tiles = (int)(((uint32_t)(hi - lo) + (1u << SH) - 1) >> SH);
     const int upto = wave_scan_add(tiles, lane);
     const uint64_t hit = __ballot(t < seen + upto);
     if (hit) {
