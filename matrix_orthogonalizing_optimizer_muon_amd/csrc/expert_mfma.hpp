@@ -22,6 +22,8 @@ namespace ex {
 constexpr uint32_t kNone = 0x80000000u;       // lane offset of a chunk that does not exist
 constexpr uint32_t kRange = 0x7fffffffu;      // descriptor range: every real offset is below it
 constexpr int kBK = 64;
+constexpr int kStage = 65536, kQAt = 32768;   // LDS of a k-tile: that of the largest tile for all, so that stages may
+                                              // hold k-tiles of different tiles
 
 template <int BM_, int BN_, int WGM_, int WGN_, bool PT_, bool QT_>
 struct Shape {
@@ -29,10 +31,9 @@ struct Shape {
   static constexpr bool PT = PT_, QT = QT_;
   static constexpr int NW = WGM * WGN, THREADS = 64 * NW;
   static constexpr int WM = BM / WGM, WN = BN / WGN, MT = WM / 32, NT = WN / 32;
-  static constexpr int PB = BM * 128, STAGE = (BM + BN) * 128, LDS = 2 * STAGE;
   static constexpr int PR = BM / 8 / NW, QR = BN / 8 / NW;   // 1 KiB copies a wave makes of each operand
   static constexpr int NDS = (PT ? 2 : 1) * MT + (QT ? 2 : 1) * NT;
-  static_assert(BM % (16 * NW) == 0 && BN % (16 * NW) == 0 && MT >= 1 && NT >= 1 && LDS <= 160 * 1024, "tile");
+  static_assert(BM % (16 * NW) == 0 && BN % (16 * NW) == 0 && MT >= 1 && NT >= 1 && BM <= 256 && BN <= 256, "tile");
   static_assert((!PT || BM >= 128) && (!QT || BN >= 128), "k-major tile rows of 256 bytes or more");
 };
 
@@ -176,6 +177,7 @@ struct KCopies {
   template <int NR>
   __device__ __forceinline__ void issue(MUON_LDS char* dst, int kt, int lane, int w) {
     if constexpr (GATHER) {
+      asm volatile("" : "+v"(idx));   // not looked at before the wait and barrier ahead of this
       step<NR>(dst, copy_rsrc(base, kRange), lane, w);
     } else {
       const int64_t left = (rows - (int64_t)kt * kBK) * (int64_t)ld;
@@ -216,7 +218,7 @@ struct TileFrags {
   u32x4 a[S::MT], b[S::NT];
   __device__ __forceinline__ void load(const MUON_LDS char* st, int kg, int lane, int wy, int wx) {
     slab_frags<S::PT, S::BM, S::MT>(a, st, wy * S::WM, kg, lane);
-    slab_frags<S::QT, S::BN, S::NT>(b, st + S::PB, wx * S::WN, kg, lane);
+    slab_frags<S::QT, S::BN, S::NT>(b, st + kQAt, wx * S::WN, kg, lane);
   }
 };
 
@@ -253,30 +255,30 @@ __device__ __forceinline__ void wait_behind(int stored) {
   else __builtin_amdgcn_s_waitcnt(nt::waitcnt_vm(N) & kKeep);
 }
 
-// Copies of a tile's first two k-tiles; every wave is done with the stages.
-template <class S, class PC, class QC>
-__device__ __forceinline__ void tile_begin(MUON_LDS char* lds, PC& cp, QC& cq, int lane, int w) {
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    cp.ahead(t, lane, w);
-    cq.ahead(t, lane, w);
-    cp.template issue<S::PR>(lds + t * S::STAGE, t, lane, w);
-    cq.template issue<S::QR>(lds + t * S::STAGE + S::PB, t, lane, w);
-  }
-  cp.ahead(2, lane, w);
-  cq.ahead(2, lane, w);
+// Copies of k-tile kt of a tile whose copies a wave are nrp and nrq (2 or 4).
+template <class PC, class QC>
+__device__ __forceinline__ void tile_issue(MUON_LDS char* st, PC& cp, QC& cq, int nrp, int nrq, int kt, int lane,
+                                           int w) {
+  if (nrp == 4) cp.template issue<4>(st, kt, lane, w);
+  else cp.template issue<2>(st, kt, lane, w);
+  if (nrq == 4) cq.template issue<4>(st + kQAt, kt, lane, w);
+  else cq.template issue<2>(st + kQAt, kt, lane, w);
+  cp.ahead(kt + 1, lane, w);
+  cq.ahead(kt + 1, lane, w);
 }
 
-// The k loop over nk >= 1 tiles of 64, after tile_begin and then `stored`
-// stores.  Tile kt sits in stage kt % 2; the fragments of a k-group are read
-// one group ahead.  When the reads of a tile's last group are done and the
-// copies of the next tile have landed, one barrier, and the copies of tile
-// kt + 2 go into the stage just read; past the end they name no chunk and
-// bring zeros that nothing reads.  On return every wave is done with the
-// stages.
-template <class S, class PC, class QC>
-__device__ __forceinline__ void tile_loop(Acc& acc, MUON_LDS char* lds, PC& cp, QC& cq, int nk, int stored, int lane,
-                                          int w) {
+// The k loop over nk >= 2 tiles of 64 (the last ones may be zeros), the first
+// of which has landed in stage `stage` and the second is on its way to the
+// other, followed by `stored` stores.  The fragments of a k-group are read one
+// group ahead.  When the reads of a k-tile's last group are done and the copies
+// of the next one have landed, one barrier, and the copies of the one after
+// that go into the stage just read.  For the last two k-tiles these are the
+// next tile's first two: turn() makes cp and cq that tile's and tells whether
+// there is one, and then(st, t) issues its k-tile t.  On return its first
+// k-tile has landed, in stage `stage`.
+template <class S, class PC, class QC, class Turn, class Then>
+__device__ __forceinline__ void tile_loop(Acc& acc, MUON_LDS char* lds, PC& cp, QC& cq, int nk, int stored, int& stage,
+                                          int lane, int w, Turn turn, Then then) {
   const int wy = w / S::WGN, wx = w % S::WGN;
 #pragma unroll
   for (int i = 0; i < S::MT; ++i)
@@ -284,13 +286,9 @@ __device__ __forceinline__ void tile_loop(Acc& acc, MUON_LDS char* lds, PC& cp, 
     for (int j = 0; j < S::NT; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-  wait_behind<S::PR + S::QR, false>(stored);
-  nt::block_barrier();
   TileFrags<S> f0, f1;
-  f0.load(lds, 0, lane, wy, wx);
-  int stage = 0;
-  for (int kt = 0; kt < nk; ++kt) {
-    MUON_LDS char* st = lds + stage * S::STAGE;
+  f0.load(lds + stage * kStage, 0, lane, wy, wx);
+  auto first_groups = [&](const MUON_LDS char* st) {
 #pragma unroll
     for (int g = 0; g < 3; ++g) {
       if (g & 1) {
@@ -302,20 +300,32 @@ __device__ __forceinline__ void tile_loop(Acc& acc, MUON_LDS char* lds, PC& cp, 
       }
       tile_hint<S, 0, S::NDS>();
     }
-    wait_behind<0, true>(stored);   // the next tile landed, own reads done
+    wait_behind<0, true>(stored);   // the next k-tile landed, own reads done
     stored = 0;
     nt::block_barrier();
+  };
+  for (int kt = 0; kt < nk - 2; ++kt) {
+    MUON_LDS char* st = lds + stage * kStage;
+    first_groups(st);
     cp.template issue<S::PR>(st, kt + 2, lane, w);
-    cq.template issue<S::QR>(st + S::PB, kt + 2, lane, w);
+    cq.template issue<S::QR>(st + kQAt, kt + 2, lane, w);
     cp.ahead(kt + 3, lane, w);
     cq.ahead(kt + 3, lane, w);
     stage ^= 1;
-    f0.load(lds + stage * S::STAGE, 0, lane, wy, wx);
+    f0.load(lds + stage * kStage, 0, lane, wy, wx);
     tile_mfma<S>(acc, f1);
-    tile_hint<S, S::PR + S::QR, S::NDS>();
+    tile_hint<S, 0, S::NDS>();
   }
-  __builtin_amdgcn_s_waitcnt(nt::kWaitVmLgkm0);   // no copy outlives the loop
-  nt::block_barrier();
+  const bool more = turn();
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    MUON_LDS char* st = lds + stage * kStage;
+    first_groups(st);
+    if (more) then(st, t);
+    stage ^= 1;
+    if (t == 0) f0.load(lds + stage * kStage, 0, lane, wy, wx);
+    tile_mfma<S>(acc, f1);
+  }
 }
 
 // A tile's rows out of the accumulators: 32 rows of a wave's 64 columns at a

@@ -269,7 +269,7 @@ struct Shapes {
   typedef Shape<256, 256, 2, 4, PT, QT> Full;
   typedef Shape<128, 256, 2, 4, PT, QT> Flat;
   typedef Shape<256, 128, 4, 2, PT, QT> Thin;
-  static constexpr int LDS = Full::LDS + 8 * kStoreBytes;
+  static constexpr int LDS = 2 * kStage + 8 * kStoreBytes;
 };
 enum Cut { kFull = 0, kFlat = 1, kThin = 2 };
 __device__ __forceinline__ int cut_of(int m_left, int n_left) {
@@ -388,52 +388,53 @@ __device__ __forceinline__ void walk(char* lds_, int N, int lane0, int w, O& o) 
   typename O::PC cp;
   typename O::QC cq;
   Acc acc;
-  Tile256 cur, last, then;
-  bool some = false;
-  auto init = [&](const Tile256& t) {
-    const Operand p = o.p(t), q = o.q(t);
-    const int cut = o.cut(t), lane = fresh(lane0);
-    cp.init(p, cut == kFlat ? Flat::PR : Full::PR, lane, w);
-    cq.init(q, cut == kThin ? Thin::QR : Full::QR, lane, w);
-  };
-  auto look = [&](const Tile256& t) {
-    cp.look(o.p(t), o.cut(t) == kFlat ? Flat::PR : Full::PR, fresh(lane0), w);
+  Tile256 cur, next;
+  auto nrp = [&](const Tile256& t) { return o.cut(t) == kFlat ? Flat::PR : Full::PR; };
+  auto nrq = [&](const Tile256& t) { return o.cut(t) == kThin ? Thin::QR : Full::QR; };
+  auto init = [&](const Tile256& t) {   // after look(t)
+    const int lane = fresh(lane0);
+    cp.init(o.p(t), nrp(t), lane, w);
+    cq.init(o.q(t), nrq(t), lane, w);
+    cp.ahead(0, lane, w);
+    cq.ahead(0, lane, w);
   };
   auto store = [&](const Tile256& t) {
     const int cut = o.cut(t);
     const int row0 = cut == kFull ? w / Full::WGN * Full::WM : cut == kFlat ? w / Flat::WGN * Flat::WM
                                                                            : w / Thin::WGN * Thin::WM;
     const int col0 = cut == kThin ? w % Thin::WGN * Thin::WN : w % Full::WGN * Full::WN;
-    return tile_store(acc, cut == kFull ? 4 : 2, lds + Full::LDS + w * kStoreBytes, o.out(t), row0, o.m_left(t),
+    return tile_store(acc, cut == kFull ? 4 : 2, lds + 2 * kStage + w * kStoreBytes, o.out(t), row0, o.m_left(t),
                       t.n0 + col0, N, fresh(lane0));
   };
   bool more = o.next(cur);
+  int stage = 0, stored = 0;
   if (more) {
-    look(cur);
+    cp.look(o.p(cur), nrp(cur), lane0, w);
     init(cur);
+    tile_issue(lds, cp, cq, nrp(cur), nrq(cur), 0, lane0, w);
+    tile_issue(lds + kStage, cp, cq, nrp(cur), nrq(cur), 1, lane0, w);
+    __builtin_amdgcn_s_waitcnt(nt::kWaitVmLgkm0);
+    nt::block_barrier();
   }
   while (more) {
-    const int cut = o.cut(cur), nk = (int)(((uint32_t)o.k(cur) + kBK - 1) / kBK), lane = fresh(lane0);
-    if (cut == kFull) tile_begin<Full>(lds, cp, cq, lane, w);
-    else if (cut == kFlat) tile_begin<Flat>(lds, cp, cq, lane, w);
-    else tile_begin<Thin>(lds, cp, cq, lane, w);
-    more = o.next(then);
-    if (more) look(then);
+    const int cut = o.cut(cur), lane = fresh(lane0);
+    const uint32_t tiles = ((uint32_t)o.k(cur) + kBK - 1) / kBK;
+    const int nk = tiles < 2 ? 2 : (int)tiles;
+    more = o.next(next);
+    if (more) cp.look(o.p(next), nrp(next), lane, w);
+    auto turn = [&]() {
+      if (more) init(next);
+      return more;
+    };
+    auto then = [&](MUON_LDS char* st, int t) { tile_issue(st, cp, cq, nrp(next), nrq(next), t, lane, w); };
+    if (cut == kFull) tile_loop<Full>(acc, lds, cp, cq, nk, stored, stage, lane, w, turn, then);
+    else if (cut == kFlat) tile_loop<Flat>(acc, lds, cp, cq, nk, stored, stage, lane, w, turn, then);
+    else tile_loop<Thin>(acc, lds, cp, cq, nk, stored, stage, lane, w, turn, then);
     asm volatile("" ::: "memory");   // the stores stay behind the copies
-    int stored = 0;
-    if (some) stored = store(last);
+    stored = store(cur);
     asm volatile("" ::: "memory");
-    if (cut == kFull) tile_loop<Full>(acc, lds, cp, cq, nk, stored, lane, w);
-    else if (cut == kFlat) tile_loop<Flat>(acc, lds, cp, cq, nk, stored, lane, w);
-    else tile_loop<Thin>(acc, lds, cp, cq, nk, stored, lane, w);
-    last = cur;
-    some = true;
-    if (more) {
-      cur = then;
-      init(cur);
-    }
+    cur = next;
   }
-  if (some) store(last);
 }
 
 // Zero to rows x cols elements at out (rows of N): by the threads of one block.
