@@ -183,6 +183,12 @@ __global__ __launch_bounds__(256) void k_product(ProdArgs a) {
     const int e = (int)(tm / a.tiles_m), m0 = (int)(tm % a.tiles_m) * G::B;
     int64_t b, end;
     expert_rows(a.offsets, e, (int)a.n, lane, b, end);
+    if (a.parts > 1) {   // this block's part, of whole k-tiles
+      const int64_t part = ((end - b + a.parts - 1) / a.parts + G::BK - 1) / G::BK * G::BK;
+      b += part * blockIdx.y;
+      end = b + part < end ? b + part : end;
+      b = b < end ? b : end;
+    }
     K = (int)(end - b);
     m_left = a.M - m0;
     out_row = (int64_t)e * a.M + m0;
@@ -237,21 +243,39 @@ __global__ __launch_bounds__(256) void k_product(ProdArgs a) {
     }
   }
   const int64_t ldo = a.N;
+  const bool whole = MODE != kWeightGrad || a.parts == 1;
+  float* sums = whole ? nullptr : a.partial + (int64_t)blockIdx.y * a.experts * a.M * ldo;
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
     const int r = wy * W + 32 * i + (lane & 31);
     if (r < m_left) {
-      T* row = out + (out_row + r) * ldo;
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const int c = n0 + wx * W + 32 * j + 8 * g + 4 * (lane >> 5);
           const float v[4] = {acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
-          store4(row + c, a.N - c, v);
+          if (whole) store4(out + (out_row + r) * ldo + c, a.N - c, v);
+          else store4(sums + (out_row + r) * ldo + c, a.N - c, v);
         }
     }
   }
+}
+
+// The parts' sums, added in their order: a thread has four elements.
+template <class T>
+__global__ __launch_bounds__(256) void k_add_parts(const float* __restrict__ partial, T* __restrict__ out, int64_t n,
+                                                   int parts) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  const int cnt = n - i < 4 ? (int)(n - i) : 4;
+  float sum[4] = {};
+  for (int p = 0; p < parts; ++p) {
+    const u32x4 v = load16(partial + p * n + i, cnt);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) sum[u] += __uint_as_float(v[u]);
+  }
+  store4(out + i, cnt, sum);
 }
 
 // ------------------------------------------------------------- large tiles
@@ -603,8 +627,9 @@ int launch_product(ProdArgs a, int dtype, int64_t tiles_m, hipStream_t s) {
   a.tiles_n = (int32_t)ceil_div(a.N, side(dtype));
   const int64_t blocks = tiles_m * a.tiles_n;
   if (blocks > kMaxCount) return fail(MUON_EUNSUPPORTED, "more than 2^31 output tiles");
-  if (dtype == MUON_BF16) hipLaunchKernelGGL((k_product<bf16_t, MODE>), dim3((uint32_t)blocks), dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_product<float, MODE>), dim3((uint32_t)blocks), dim3(256), 0, s, a);
+  const dim3 grid((uint32_t)blocks, (uint32_t)a.parts);
+  if (dtype == MUON_BF16) hipLaunchKernelGGL((k_product<bf16_t, MODE>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_product<float, MODE>), grid, dim3(256), 0, s, a);
   return launch_status("grouped product launch");
 }
 
@@ -664,9 +689,40 @@ int launch_weight(ProdArgs a, hipStream_t s) {
   return launch_status("grouped weight gradient launch");
 }
 
-// Workspace of the weight gradient: a checkpoint's rows as dense values.
-uint64_t weight_grad_bytes(int dtype, int64_t x_rows, int64_t inner, bool kept) {
-  return kept ? (uint64_t)x_rows * inner * (dtype == MUON_BF16 ? 2 : 4) : 0;
+// Whether the weight gradient takes the small tiles although its rows would let
+// it take the large ones, and the parts into which these cut an expert's rows.
+// Small: at most one large tile a CU and few rows (8 x 1024 x 1024, 8 to 256
+// rows: 9 to 11 us against 12 to 13; 1024 rows: 18 against 17), or so few large
+// tiles that most CUs would idle over long sums.  Parts: until there are two
+// blocks a CU, two k-tiles in a part on average.  Without and with them, us (bf16):
+//   9 x 192 x 208, 26960 rows:  99, 29    5 x 64 x 1280, 28945 rows: 89, 40
+//   2 x 512 x 512, 16384 rows: 185, 40    6 x 2752 x 64, 8016 rows:  28, 29
+// With 128 large tiles (8 x 1024 x 1024, 16384 rows) the small ones take 141 us, the large ones 95.
+struct WeightCut {
+  bool small;
+  int parts;
+};
+WeightCut weight_cut(int dtype, int64_t n, int experts, int64_t outer, int64_t inner) {
+  const int64_t large = experts * ceil_div(outer, 256) * ceil_div(inner, 256);
+  const int64_t tiles = experts * ceil_div(outer, side(dtype)) * ceil_div(inner, side(dtype));
+  const int64_t k_tile = dtype == MUON_BF16 ? Tile<bf16_t>::BK : Tile<float>::BK;
+  const int64_t most = n / (experts * 2 * k_tile);
+  int64_t parts = 2 * kWalkers / tiles;
+  if (parts > most) parts = most;
+  if (parts > 64) parts = 64;
+  const bool few = large <= kWalkers && n <= 64 * (int64_t)experts;
+  if (few || parts < 1) parts = 1;
+  return WeightCut{few || (large <= 96 && parts > 1), (int)parts};
+}
+
+uint64_t dense_bytes(int dtype, int64_t x_rows, int64_t inner) {
+  return ((uint64_t)x_rows * inner * (dtype == MUON_BF16 ? 2 : 4) + 15) / 16 * 16;
+}
+// Workspace of the weight gradient: a checkpoint's rows as dense values, and the parts' sums.
+uint64_t weight_grad_bytes(int dtype, int64_t n, int64_t x_rows, int experts, int64_t outer, int64_t inner, bool kept) {
+  const int parts = weight_cut(dtype, n, experts, outer, inner).parts;
+  return (kept ? dense_bytes(dtype, x_rows, inner) : 0) +
+         (parts > 1 ? (uint64_t)parts * experts * outer * inner * 4 : 0);
 }
 
 }  // namespace
@@ -686,7 +742,7 @@ int muon_grouped_matmul(const void* x, const void* w, const int32_t* offsets, co
   if (n == 0) return MUON_OK;
   if ((!x && x_rows) || !w || !offsets || !y) return fail(MUON_EINVAL, "NULL pointer");
   if ((rc = check_device())) return rc;
-  ProdArgs a = {x, w, y, offsets, rows, n, x_rows, experts, 0, (int32_t)outer, (int32_t)inner, 0, 0};
+  ProdArgs a = {x, w, y, offsets, rows, n, x_rows, experts, 0, (int32_t)outer, (int32_t)inner, 0, 0, 1, nullptr};
   int64_t blocks;
   if (few<kMatmul>(a, dtype, &blocks)) return launch_few<kMatmul>(a, dtype, blocks, static_cast<hipStream_t>(stream));
   if (chunked(a, dtype, inner, outer, inner))
@@ -702,7 +758,7 @@ int muon_grouped_input_grad(const void* dy, const void* w, const int32_t* offset
   if (n == 0) return MUON_OK;
   if (!dy || !w || !offsets || !dx) return fail(MUON_EINVAL, "NULL pointer");
   if ((rc = check_device())) return rc;
-  ProdArgs a = {dy, w, dx, offsets, nullptr, n, n, experts, 0, (int32_t)inner, (int32_t)outer, 0, 0};
+  ProdArgs a = {dy, w, dx, offsets, nullptr, n, n, experts, 0, (int32_t)inner, (int32_t)outer, 0, 0, 1, nullptr};
   int64_t blocks;
   if (few<kInputGrad>(a, dtype, &blocks)) return launch_few<kInputGrad>(a, dtype, blocks, static_cast<hipStream_t>(stream));
   if (chunked(a, dtype, inner, outer, inner))
@@ -716,7 +772,7 @@ int muon_grouped_weight_grad_workspace(int dtype, int64_t n, int64_t x_rows, int
   if (!bytes) return fail(MUON_EINVAL, "NULL bytes");
   const int rc = check_product(dtype, n, x_rows, experts, outer, inner);
   if (rc) return rc;
-  *bytes = weight_grad_bytes(dtype, x_rows, inner, checkpoint != 0);
+  *bytes = weight_grad_bytes(dtype, n, x_rows, experts, outer, inner, checkpoint != 0);
   return MUON_OK;
 }
 
@@ -733,7 +789,7 @@ int muon_grouped_weight_grad(const void* dy, const void* x, const void* q, const
   if (kept && kind != MUON_INT8 && kind != MUON_E4M3) return fail(MUON_EUNSUPPORTED, "kind must be MUON_INT8 or MUON_E4M3");
   if (!offsets || !dw || (n > 0 && !dy) || (n > 0 && x_rows > 0 && (kept ? (!q || !scale) : !x)))
     return fail(MUON_EINVAL, "NULL pointer");
-  const uint64_t need = weight_grad_bytes(dtype, x_rows, inner, kept);
+  const uint64_t need = weight_grad_bytes(dtype, n, x_rows, experts, outer, inner, kept);
   if (need && (!workspace || workspace_bytes < need))
     return fail(MUON_EINVAL, "workspace of " + std::to_string(need) + " bytes needed");
   if (need && (reinterpret_cast<uintptr_t>(workspace) & 15)) return fail(MUON_EINVAL, "workspace must be 16-byte aligned");
@@ -743,13 +799,20 @@ int muon_grouped_weight_grad(const void* dy, const void* x, const void* q, const
     if ((rc = restore_rows(q, scale, kind, x_rows, inner, dtype, workspace, s))) return rc;
     x = workspace;
   }
-  ProdArgs a = {dy, x, dw, offsets, rows, n, x_rows, experts, (int32_t)outer, (int32_t)inner, 0, 0, 0};
-  // fewer than a large tile a CU, and few rows: the small tiles' blocks are more and start faster (8 x 1024 x 1024,
-  // n 8 to 256: 9 to 11 us against 12 to 13; n 1024: 18 against 17)
-  const bool small = (int64_t)experts * ceil_div(outer, 256) * ceil_div(inner, 256) <= kWalkers && n <= 64 * (int64_t)experts;
-  if (!small && chunked(a, dtype, inner, outer, inner)) return launch_weight(a, s);
+  ProdArgs a = {dy, x, dw, offsets, rows, n, x_rows, experts, (int32_t)outer, (int32_t)inner, 0, 0, 0, 1, nullptr};
+  const WeightCut cut = weight_cut(dtype, n, experts, outer, inner);
+  if (!cut.small && chunked(a, dtype, inner, outer, inner)) return launch_weight(a, s);
   a.tiles_m = (int32_t)ceil_div(outer, side(dtype));
-  return launch_product<kWeightGrad>(a, dtype, (int64_t)experts * a.tiles_m, s);
+  a.parts = cut.parts;
+  a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + (kept ? dense_bytes(dtype, x_rows, inner) : 0));
+  if ((rc = launch_product<kWeightGrad>(a, dtype, (int64_t)experts * a.tiles_m, s)) || cut.parts == 1) return rc;
+  const int64_t count = experts * outer * inner;
+  const dim3 grid((uint32_t)ceil_div(count, 1024));
+  if (dtype == MUON_BF16)
+    hipLaunchKernelGGL((k_add_parts<bf16_t>), grid, dim3(256), 0, s, a.partial, static_cast<bf16_t*>(dw), count, cut.parts);
+  else
+    hipLaunchKernelGGL((k_add_parts<float>), grid, dim3(256), 0, s, a.partial, static_cast<float*>(dw), count, cut.parts);
+  return launch_status("weight gradient parts launch");
 }
 
 }  // extern "C"

@@ -18,6 +18,8 @@ struct ProdArgs {
   int32_t experts;
   int32_t M, N, K;          // M: weight grad only; K: not in the weight grad
   int32_t tiles_m, tiles_n; // tiles_m: weight grad only
+  int32_t parts;            // weight grad by small tiles: parts of an expert's rows, 1 or more
+  float* partial;           // with more than one: their sums, [parts][experts][M][N]
 };
 
 // Tile t of the rows cut by expert into tiles of 2^SH: expert and rows

@@ -69,6 +69,28 @@ def test_few_rows_of_many_experts():
     base.check_products(*base.product_inputs([e % 2 for e in range(1024)], 40, 24, F, False, 0, 94))
 
 
+@pytest.mark.parametrize("dtype", [B, F])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("sides", [(40, 72), (129, 33)])
+def test_weight_grad_in_parts(dtype, gather, sides):
+    """Few tiles and long sums: experts' rows in parts, some of them empty."""
+    base.check_products(*base.product_inputs([5000, 0, 2500, 3], *sides, dtype, gather, 9 if gather else 0, 99))
+    base.check_products(*base.product_inputs([1, 129, 6000], *sides, dtype, gather, 0, 100))
+
+
+@pytest.mark.parametrize("dtype", [B, F])
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+def test_weight_grad_in_parts_from_a_checkpoint(dtype, kind):
+    x, _, dy, rows, off = base.product_inputs([3000, 0, 1700], 72, 70, dtype, True, 4, 101)
+    c = M.checkpoint(x.cuda(), kind)
+    back = M.restore(c).cpu()
+    base.poison((3, 72, 70), dtype)
+    dw = M.grouped_weight_grad(dy.cuda(), c, torch.tensor(off, dtype=I, device="cuda"), rows=rows.cuda())
+    want = O.weight_grad(dy, back, off, rows)
+    size = O.weight_grad(dy.abs(), back.abs(), off, rows)
+    base.close(dw, want, base.HALF[dtype] * want.abs() + 3000 * base.ULP * size + base.TINY[dtype], "in parts")
+
+
 @pytest.mark.parametrize("off", [[0, 1900, 600, 2500], [-7, -3, 1200, 1100], [50, 900, 1500, 2 ** 31 - 1],
                                  [9, 0, 0, 0], [0, 2 ** 31 - 1, 3, 150]])
 def test_large_tiles_of_broken_offsets(off):
