@@ -75,6 +75,8 @@ __device__ __forceinline__ bool few_sum(Acc16 (&acc)[NQ], Acc16* lds, Acc16& sum
 }
 
 // y[r] = x[r] W_e^T: strips of 16 CT columns, k in steps of 64 bytes a row.
+// Bound by the matrices' way from memory: 8 rows of 8 experts, 2816 x 2048 bf16,
+// 92 MB: 20 us, 4.5 TB/s; 222 rows of 59 experts, 2048 x 1408, 341 MB: 65 us, 5.2 TB/s.
 // A row or column that does not exist reads another's values instead, which
 // reach only results that are not stored or are zeroed.
 template <class T, int CT>
@@ -167,6 +169,7 @@ struct Cols<float> {
 // dx[r] = dy[r] W_e: strips of 64 columns.  A lane has 4 of them of PER rows of
 // the matrix, so the operand for column 4 (l % 16) + c is put together from
 // registers, and the product of c is rows 4 (l / 16) + i: columns 16 (l / 16) + 4 i + c.
+// 8 rows of 8 experts, 2816 x 2048 bf16: 19 us.
 template <class T>
 __global__ __launch_bounds__(512) void k_few_input_grad(ProdArgs a) {
   constexpr int PER = Few<T>::PER, STEP = 4 * PER, NW = 8, U = 2;
