@@ -33,7 +33,7 @@ struct Shape {
   static constexpr int WM = BM / WGM, WN = BN / WGN, MT = WM / 32, NT = WN / 32;
   static constexpr int PR = BM / 8 / NW, QR = BN / 8 / NW;   // 1 KiB copies a wave makes of each operand
   static constexpr int NDS = (PT ? 2 : 1) * MT + (QT ? 2 : 1) * NT;
-  static_assert(BM % (16 * NW) == 0 && BN % (16 * NW) == 0 && MT >= 1 && NT >= 1 && BM <= 256 && BN <= 256, "tile");
+  static_assert(BM % (16 * NW) == 0 && BN % (16 * NW) == 0 && MT % 2 == 0 && NT >= 1 && BM <= 256 && BN <= 256, "tile");
   static_assert((!PT || BM >= 128) && (!QT || BN >= 128), "k-major tile rows of 256 bytes or more");
 };
 
@@ -225,22 +225,23 @@ struct TileFrags {
 // Accumulators of a wave: those of the widest shape; smaller ones use the first of them.
 typedef nt::f32x16_t Acc[4][2];
 
-template <class S>
+// Rows [I0, I1) of the wave's MFMA tiles.
+template <class S, int I0 = 0, int I1 = S::MT>
 __device__ __forceinline__ void tile_mfma(Acc& acc, const TileFrags<S>& f) {
 #pragma unroll
-  for (int i = 0; i < S::MT; ++i)
+  for (int i = I0; i < I1; ++i)
 #pragma unroll
     for (int j = 0; j < S::NT; ++j)
       acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(nt::bf16x8_t, f.b[j]),
                                                          __builtin_bit_cast(nt::bf16x8_t, f.a[i]), acc[i][j], 0, 0, 0);
 }
 
-template <class S, int NVM, int NDS>
+// An LDS read behind each of the first NDS products.
+template <class S, int NDS>
 __device__ __forceinline__ void tile_hint() {
 #pragma unroll
   for (int i = 0; i < S::MT * S::NT; ++i) {
     MUON_SCHED(0x008, 1);
-    if (i < NVM) MUON_SCHED(0x020, 1);
     if (i < NDS) MUON_SCHED(0x100, 1);
   }
 }
@@ -298,7 +299,7 @@ __device__ __forceinline__ void tile_loop(Acc& acc, MUON_LDS char* lds, PC& cp, 
         f1.load(st, g + 1, lane, wy, wx);
         tile_mfma<S>(acc, f0);
       }
-      tile_hint<S, 0, S::NDS>();
+      tile_hint<S, S::NDS>();
     }
     wait_behind<0, true>(stored);   // the next k-tile landed, own reads done
     stored = 0;
@@ -307,14 +308,20 @@ __device__ __forceinline__ void tile_loop(Acc& acc, MUON_LDS char* lds, PC& cp, 
   for (int kt = 0; kt < nk - 2; ++kt) {
     MUON_LDS char* st = lds + stage * kStage;
     first_groups(st);
-    cp.template issue<S::PR>(st, kt + 2, lane, w);
+    // the copies in two runs with products between them, the fragment reads with the second: 728 -> 703 us for the
+    // training batch against both runs first and the products after (input gradient 419 -> 414, weight gradient
+    // 252 -> 248, from 8 bits 818 -> 783); the reads ahead of all, or the products' first half, are slower
+    stage ^= 1;
     cq.template issue<S::QR>(st + kQAt, kt + 2, lane, w);
+    __builtin_amdgcn_sched_barrier(0);
+    tile_mfma<S, 0, S::MT / 2>(acc, f1);
+    __builtin_amdgcn_sched_barrier(0);
+    f0.load(lds + stage * kStage, 0, lane, wy, wx);
+    cp.template issue<S::PR>(st, kt + 2, lane, w);
     cp.ahead(kt + 3, lane, w);
     cq.ahead(kt + 3, lane, w);
-    stage ^= 1;
-    f0.load(lds + stage * kStage, 0, lane, wy, wx);
-    tile_mfma<S>(acc, f1);
-    tile_hint<S, 0, S::NDS>();
+    __builtin_amdgcn_sched_barrier(0);
+    tile_mfma<S, S::MT / 2>(acc, f1);
   }
   const bool more = turn();
 #pragma unroll

@@ -283,10 +283,10 @@ __global__ __launch_bounds__(256) void k_add_parts(const float* __restrict__ par
 // ------------------------------------------------------------- large tiles
 
 // Products of many rows.  65536 rows (8192 tokens to 8 of 64 experts) through
-// 2816 x 2048: 730 to 750 us, 1010 to 1035 TFLOP/s; the input gradient of half
-// of them 410 to 425 us, the weight gradient 820 us.  A k-tile of 64 takes a block
-// 1.75 us in the first: 1.25 without the copies (the MFMAs at the clock that
-// power leaves), 0.25 for copies that hit L2, 0.25 for those that do not.
+// 2816 x 2048: 695 to 703 us, 1075 to 1088 TFLOP/s; the input gradient of half
+// of them 402 to 414 us, the weight gradient 775 us.  A k-tile of 64 takes a block
+// about 1.7 us in the first: 1.25 without the copies (the MFMAs at the clock that
+// power leaves), the rest for the copies, half of that for those that miss L2.
 //
 // The large kernels run one block of 8 waves per CU, each walking a list of
 // output tiles: consecutive blocks go to the eight XCDs in turn, so block b has
