@@ -214,7 +214,7 @@ __global__ __launch_bounds__(256) void k_product(ProdArgs a) {
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-  const int nk = (K + G::BK - 1) / G::BK;
+  const int nk = (int)(((uint32_t)K + G::BK - 1) / G::BK);
   if (nk) {
     sp.fetch(0);
     sq.fetch(0);
