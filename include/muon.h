@@ -518,7 +518,8 @@ int muon_route_backward(const float* dweights, const void* logits, const float* 
  *   muon_grouped_weight_grad  dw_e = sum over the rows r of expert e of
  *                             dy[r]^T x[rows[r]] (E x outer x inner; zero for
  *                             an expert without rows).  x dense (q, scale
- *                             NULL), or NULL with its checkpoint q, scale, kind.
+ *                             NULL), or NULL with its checkpoint q, scale, kind
+ *                             (not read where n is 0).
  * Rows from offsets[E] on are zero in y and dx and count for no dw.  The
  * device arrays are not trusted: offsets are read as their running maximum,
  * within [0, n] and from 0 on; an entry of rows outside [0, x_rows) is a row

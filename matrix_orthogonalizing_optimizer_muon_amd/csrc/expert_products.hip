@@ -726,10 +726,11 @@ WeightCut weight_cut(int dtype, int64_t n, int experts, int64_t outer, int64_t i
 uint64_t dense_bytes(int dtype, int64_t x_rows, int64_t inner) {
   return ((uint64_t)x_rows * inner * (dtype == MUON_BF16 ? 2 : 4) + 15) / 16 * 16;
 }
-// Workspace of the weight gradient: a checkpoint's rows as dense values, and the parts' sums.
+// Workspace of the weight gradient: a checkpoint's rows as dense values (`kept`; where there are rows to sum), and
+// the parts' sums.
 uint64_t weight_grad_bytes(int dtype, int64_t n, int64_t x_rows, int experts, int64_t outer, int64_t inner, bool kept) {
   const int parts = weight_cut(dtype, n, experts, outer, inner).parts;
-  return (kept ? dense_bytes(dtype, x_rows, inner) : 0) +
+  return (kept && n > 0 ? dense_bytes(dtype, x_rows, inner) : 0) +
          (parts > 1 ? (uint64_t)parts * experts * outer * inner * 4 : 0);
 }
 
@@ -795,15 +796,16 @@ int muon_grouped_weight_grad(const void* dy, const void* x, const void* q, const
   if (n > 0 && !rows && x_rows != n) return fail(MUON_EINVAL, "x_rows must be n where rows is NULL");
   if (kept && x) return fail(MUON_EINVAL, "either x or its checkpoint, not both");
   if (kept && kind != MUON_INT8 && kind != MUON_E4M3) return fail(MUON_EUNSUPPORTED, "kind must be MUON_INT8 or MUON_E4M3");
-  if (!offsets || !dw || (n > 0 && !dy) || (n > 0 && x_rows > 0 && (kept ? (!q || !scale) : !x)))
-    return fail(MUON_EINVAL, "NULL pointer");
+  if (kept && x_rows > 0 && (!q || !scale)) return fail(MUON_EINVAL, "q and scale come together");
+  if (!offsets || !dw || (n > 0 && !dy) || (n > 0 && x_rows > 0 && !kept && !x)) return fail(MUON_EINVAL, "NULL pointer");
   const uint64_t need = weight_grad_bytes(dtype, n, x_rows, experts, outer, inner, kept);
   if (need && (!workspace || workspace_bytes < need))
     return fail(MUON_EINVAL, "workspace of " + std::to_string(need) + " bytes needed");
   if (need && (reinterpret_cast<uintptr_t>(workspace) & 15)) return fail(MUON_EINVAL, "workspace must be 16-byte aligned");
   if ((rc = check_device())) return rc;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (kept) {
+  const bool restored = kept && n > 0;
+  if (restored) {
     if ((rc = restore_rows(q, scale, kind, x_rows, inner, dtype, workspace, s))) return rc;
     x = workspace;
   }
@@ -812,7 +814,7 @@ int muon_grouped_weight_grad(const void* dy, const void* x, const void* q, const
   if (!cut.small && chunked(a, dtype, inner, outer, inner)) return launch_weight(a, s);
   a.tiles_m = (int32_t)ceil_div(outer, side(dtype));
   a.parts = cut.parts;
-  a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + (kept ? dense_bytes(dtype, x_rows, inner) : 0));
+  a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + (restored ? dense_bytes(dtype, x_rows, inner) : 0));
   if ((rc = launch_product<kWeightGrad>(a, dtype, (int64_t)experts * a.tiles_m, s)) || cut.parts == 1) return rc;
   const int64_t count = experts * outer * inner;
   const dim3 grid((uint32_t)ceil_div(count, 1024));
