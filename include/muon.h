@@ -473,7 +473,8 @@ int muon_step_noalloc(const muon_matrix_desc* desc, const muon_plan_opts* opts, 
  * equal bits.  Sizes of zero rows or tokens are valid and need no pointers,
  * except offsets.  Errors: EINVAL (NULL pointer, negative or inconsistent
  * size, a workspace that is missing, too small or not 16-byte aligned), EUNSUPPORTED (dtype, kind, E
- * over 1024, k over 64, T k >= 2^31, no gfx950 device), EHIP.
+ * over 1024, k over 64, T k >= 2^31, 2^31 groups of 8 columns or more in the row-wise ones, no gfx950
+ * device), EHIP.
  */
 
 /* How a checkpoint holds a value in 8 bits: in blocks of 32 columns of a row,

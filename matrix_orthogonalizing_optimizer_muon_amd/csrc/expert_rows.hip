@@ -846,9 +846,9 @@ __global__ __launch_bounds__(256) void k_gated_backward(const T* __restrict__ dh
 
 // --------------------------------------------------------------------- host
 
-// Work items of eight columns each over `rows` rows of `groups` groups.
+// Work items of eight columns each over `rows` >= 1 rows of `groups` groups.
 int items_of(int64_t rows, int64_t groups, uint32_t* items, FastDiv* div) {
-  if (rows > 0 && groups > kMaxCount / rows) return fail(MUON_EUNSUPPORTED, "more than 2^31 groups of 8 columns");
+  if (groups > kMaxCount / rows) return fail(MUON_EUNSUPPORTED, "more than 2^31 groups of 8 columns");
   *items = (uint32_t)(rows * groups);
   *div = fast_div((uint32_t)groups);
   return MUON_OK;
@@ -917,6 +917,7 @@ void by_width(int experts, F f) {
 int check_rows(int dtype, int64_t rows, int64_t cols) {
   if (!good_dtype(dtype)) return fail(MUON_EUNSUPPORTED, "unsupported dtype");
   if (rows < 0 || cols < 1) return fail(MUON_EINVAL, "rows must be >= 0 and columns >= 1");
+  if (rows > 0 && cols > 8 * kMaxCount) return fail(MUON_EUNSUPPORTED, "2^34 columns or more");
   return MUON_OK;
 }
 
@@ -974,11 +975,11 @@ void launch_gated_backward(const void* dh, const void* gu, const void* q, const 
 // Rows of a checkpoint as dense values (used by the products' weight gradient).
 int restore_rows(const void* q, const uint8_t* scale, int kind, int64_t rows, int64_t cols, int dtype, void* x,
                  hipStream_t s) {
+  if (rows == 0) return MUON_OK;
   uint32_t items;
   FastDiv div;
   int rc;
   if ((rc = items_of(rows, ceil_div(cols, 8), &items, &div))) return rc;
-  if (!items) return MUON_OK;
   if (dtype == MUON_BF16) launch_restore<bf16_t>(q, scale, cols, kind, x, items, div, s);
   else launch_restore<float>(q, scale, cols, kind, x, items, div, s);
   return launch_status("restore launch");
@@ -1104,10 +1105,10 @@ int muon_combine(const void* y, const int32_t* slots, const float* weights, int 
   if ((rc = check_rows(dtype, tokens, cols))) return rc;
   if (k < 1) return fail(MUON_EINVAL, "k must be positive");
   if (tokens > kMaxCount / k) return fail(MUON_EUNSUPPORTED, "tokens * k must stay below 2^31");
+  if (tokens == 0) return MUON_OK;
   uint32_t items;
   FastDiv div;
   if ((rc = items_of(tokens, ceil_div(cols, 8), &items, &div))) return rc;
-  if (!items) return MUON_OK;
   if (!y || !slots || !weights || !out) return fail(MUON_EINVAL, "NULL pointer");
   if ((rc = check_device())) return rc;
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -1149,10 +1150,10 @@ int muon_checkpoint(const void* x, int dtype, int64_t rows, int64_t cols, int ki
   muon::report_error(MUON_OK, "");
   int rc;
   if ((rc = check_rows(dtype, rows, cols)) || (rc = check_kind(kind))) return rc;
+  if (rows == 0) return MUON_OK;
   uint32_t items;
   FastDiv div;
   if ((rc = items_of(rows, 4 * ceil_div(cols, kBlock), &items, &div))) return rc;
-  if (!items) return MUON_OK;
   if (!x || !q || !scale) return fail(MUON_EINVAL, "NULL pointer");
   if ((rc = check_device())) return rc;
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -1178,12 +1179,12 @@ int muon_gated(const void* gu, int dtype, int64_t rows, int64_t cols, int kind, 
   int rc;
   const bool keep = q || scale;
   if ((rc = check_rows(dtype, rows, cols)) || (keep && (rc = check_kind(kind)))) return rc;
+  if (rows == 0) return MUON_OK;
   uint32_t items, kitems;
   FastDiv div, kdiv;
   if ((rc = items_of(rows, ceil_div(cols, 8), &items, &div)) ||
       (rc = items_of(rows, 4 * ceil_div(2 * cols, kBlock), &kitems, &kdiv)))
     return rc;
-  if (!items) return MUON_OK;
   if (!gu || !h || (keep && (!q || !scale))) return fail(MUON_EINVAL, "NULL pointer");
   if ((rc = check_device())) return rc;
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -1215,10 +1216,10 @@ int muon_gated_backward(const void* dh, const void* gu, const void* q, const uin
   const bool kept = q || scale;
   if ((rc = check_rows(dtype, rows, cols)) || (kept && (rc = check_kind(kind)))) return rc;
   if (kept && gu) return fail(MUON_EINVAL, "either gu or its checkpoint, not both");
+  if (rows == 0) return MUON_OK;
   uint32_t items;
   FastDiv div;
   if ((rc = items_of(rows, ceil_div(cols, 8), &items, &div))) return rc;
-  if (!items) return MUON_OK;
   if (!dh || !dgu || !h || (kept ? (!q || !scale) : !gu)) return fail(MUON_EINVAL, "NULL pointer");
   if ((rc = check_device())) return rc;
   hipStream_t s = static_cast<hipStream_t>(stream);

@@ -1,6 +1,9 @@
 """The borders of the expert-layer entry points on the CPU: sizes of zero, sizes past
 a limit, pointers that come in pairs.  Nothing here reaches a kernel."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 
@@ -24,3 +27,38 @@ def test_weight_grad_of_no_rows_needs_no_workspace():
         need = ctypes.c_uint64(99)
         assert L.lib().muon_grouped_weight_grad_workspace(L.MUON_BF16, 0, 4096, 2, 8, 8, kept, ctypes.byref(need)) == L.MUON_OK
         assert need.value == 0
+
+
+NOTHING_OF_MANY_COLUMNS = """
+import sys
+sys.path.insert(0, {root!r})
+from matrix_orthogonalizing_optimizer_muon_amd import _lib as L
+lib, N = L.lib(), None
+for cols in (1 << 33, 1 << 35, (1 << 35) + 1, (1 << 62) + 8, (1 << 63) - 1):
+    assert lib.muon_checkpoint(N, 1, 0, cols, 0, N, N, N) == L.MUON_OK, cols
+    assert lib.muon_restore(N, N, 0, 0, cols, 1, N, N) == L.MUON_OK, cols
+    assert lib.muon_gated(N, 1, 0, cols, 0, N, N, N, N) == L.MUON_OK, cols
+    assert lib.muon_gated_backward(N, N, N, N, 0, 1, 0, cols, N, N, N) == L.MUON_OK, cols
+    assert lib.muon_combine(N, N, N, 1, 0, 2, cols, N, N) == L.MUON_OK, cols
+    assert lib.muon_combine_backward(N, N, N, N, N, 1, 0, 2, 2, cols, N, N, N) == L.MUON_OK, cols
+"""
+
+
+def test_nothing_to_do_at_any_width():
+    """Zero rows of so many columns that a count of column groups wraps to zero; in a process of its own, which a
+    division by that count would end."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", NOTHING_OF_MANY_COLUMNS.format(root=root)], capture_output=True, text=True)
+    assert r.returncode == 0, (r.returncode, r.stderr)
+
+
+@pytest.mark.parametrize("cols", [(1 << 34) + 1, 1 << 35, (1 << 62) + 8, (1 << 63) - 1])
+def test_more_columns_than_a_launch_has(cols):
+    lib = L.lib()
+    for rows in (1, 3):
+        assert lib.muon_checkpoint(P, 1, rows, cols, 0, P, P, N) == L.MUON_EUNSUPPORTED
+        assert lib.muon_restore(P, P, 0, rows, cols, 1, P, N) == L.MUON_EUNSUPPORTED
+        assert lib.muon_gated(P, 1, rows, cols, 0, P, N, N, N) == L.MUON_EUNSUPPORTED
+        assert lib.muon_gated(P, 1, rows, cols, 0, P, P, P, N) == L.MUON_EUNSUPPORTED
+        assert lib.muon_gated_backward(P, P, N, N, 0, 1, rows, cols, P, P, N) == L.MUON_EUNSUPPORTED
+        assert lib.muon_combine(P, P, P, 1, rows, 2, cols, P, N) == L.MUON_EUNSUPPORTED
