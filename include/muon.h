@@ -550,7 +550,8 @@ int muon_grouped_weight_grad(const void* dy, const void* x, const void* q, const
  *                          offsets[E] on zero; dweights[t][j] = <y[slots[t][j]],
  *                          dout[t]>.  Every row below offsets[E] must have its slot
  *                          (as muon_route's have).
- * A slot outside [0, T k) contributes nothing and gets gradient 0.
+ * A slot outside [0, T k) contributes nothing and gets gradient 0; one from
+ * offsets[E] on leaves its row of dy zero.  No two choices have one slot.
  */
 int muon_combine(const void* y, const int32_t* slots, const float* weights, int dtype,
                  int64_t tokens, int k, int64_t cols, void* out, void* stream);

@@ -586,8 +586,9 @@ __global__ __launch_bounds__(256) void k_combine(const T* __restrict__ y, const 
 
 // dy[slot_j] = w_j dout[t], dw_j = <y[slot_j], dout[t]>: a wave per choice;
 // the waves of one token sit side by side, so dout comes from cache but once.
-// The wave of place p also clears row p of dy where no expert has it.  The
-// sizes above: 106 us, 570 MB, 5.4 TB/s.
+// The wave of place p also clears row p of dy where no expert has it; such a
+// row is written by no other wave, whatever slot names it.  The sizes above: 106
+// us, 570 MB, 5.4 TB/s.
 template <class T>
 __global__ __launch_bounds__(256) void k_combine_backward(
     const T* __restrict__ dout, const T* __restrict__ y, const int32_t* __restrict__ slots,
@@ -597,7 +598,7 @@ __global__ __launch_bounds__(256) void k_combine_backward(
   const uint32_t p = blockIdx.x * 4 + (threadIdx.x >> 6);
   if (p >= n) return;
   const uint32_t t = div_by(p, k);
-  const int32_t s = slots[p];
+  const int32_t s = slots[p], live = offsets[experts];
   float dot = 0.f;
   if (s >= 0 && s < n) {
     const float w = weights[p];
@@ -611,12 +612,12 @@ __global__ __launch_bounds__(256) void k_combine_backward(
         dot += a[i] * b[i];
         b[i] *= w;
       }
-      store8(dy + s * cols + c, cnt, b);
+      if (s < live) store8(dy + s * cols + c, cnt, b);
     }
   }
   dot = wave_sum(dot);
   if (lane == 0) dw[p] = dot;
-  if (p >= offsets[experts]) {
+  if ((int64_t)p >= live) {
     const float z[8] = {};
     for (int64_t c = 8 * lane; c < cols; c += 512) store8(dy + p * cols + c, (int)(cols - c < 8 ? cols - c : 8), z);
   }

@@ -21,3 +21,25 @@ def test_weight_grad_of_no_rows_from_a_checkpoint(dtype, kind):
     base.poison((3, 24, 72), dtype)
     dw = M.grouped_weight_grad(dy, c, torch.zeros(4, dtype=I, device="cuda"), rows=rows)
     assert dw.shape == (3, 24, 72) and (dw == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [B, F])
+@pytest.mark.parametrize("live", [0, 100000, -5])
+def test_combine_backward_clears_rows_that_slots_name(dtype, live):
+    """Rows from offsets[E] on are zero although slots name them, in whatever order their waves run: the last choices
+    have the first rows here."""
+    tokens, k, cols = 100000, 2, 24
+    n = tokens * k
+    y, dout = (torch.randn(r, cols, generator=gen(2)).to(dtype).cuda() for r in (n, tokens))
+    slots = torch.arange(n, dtype=I, device="cuda").flip(0).view(tokens, k).contiguous()
+    w = torch.rand(tokens, k, generator=gen(3)).cuda() + 0.5
+    off = torch.tensor([0, 7, live], dtype=I, device="cuda")
+    base.poison((n, cols), dtype)
+    dy, dw = M.combine_backward(dout, y, slots, w, off)
+    want = (w[..., None] * dout.float()[:, None]).view(n, cols).flip(0)
+    want[max(live, 0):] = 0
+    assert (dy[max(live, 0):] == 0).all()
+    # one product rounded to fp32 and to the type
+    base.close(dy, want.cpu().double(), (base.HALF[dtype] + base.ULP) * want.abs().cpu().double(), "dy")
+    dots = (y.flip(0).view(tokens, k, cols).double() * dout[:, None].double())
+    base.close(dw, dots.sum(2).cpu(), cols * base.ULP * dots.abs().sum(2).cpu(), "dweights")
