@@ -1,10 +1,13 @@
 """The expert-layer operators at the borders of their sizes, where a launch, a
 workspace or an index changes its form, and on inputs that are valid but seldom."""
+import math
+
 import pytest
 import torch
 
 import matrix_orthogonalizing_optimizer_muon_amd as M
 import test_experts_gpu as base
+from oracle import experts_oracle as O
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +46,26 @@ def test_combine_backward_clears_rows_that_slots_name(dtype, live):
     base.close(dy, want.cpu().double(), (base.HALF[dtype] + base.ULP) * want.abs().cpu().double(), "dy")
     dots = (y.flip(0).view(tokens, k, cols).double() * dout[:, None].double())
     base.close(dw, dots.sum(2).cpu(), cols * base.ULP * dots.abs().sum(2).cpu(), "dweights")
+
+
+# rows of the experts, outer, inner: few rows, tiles through registers, large bf16 tiles, odd k
+@pytest.mark.parametrize("dtype", [B, F])
+@pytest.mark.parametrize("sizes", [([3, 2], 40, 256), ([3, 2], 33, 37), ([1], 8, 1600), ([700, 900], 259, 515),
+                                   ([600, 900], 776, 512)])
+def test_a_row_that_names_no_token_is_a_row_of_zeros(dtype, sizes):
+    """Whichever kernel takes the product: zero, and NaN where the matrix has an infinity."""
+    counts, outer, inner = sizes
+    x, w, _, rows, off = base.product_inputs(counts, outer, inner, dtype, True, 2, 4)
+    rows[0], rows[counts[0] - 1] = x.shape[0], -9
+    w[0, 3, 1], w[0, 7, inner - 1], w[-1, 5, inner // 2] = math.inf, -math.inf, math.nan
+    o = torch.tensor(off, dtype=I, device="cuda")
+    base.poison((rows.shape[0], outer), dtype)
+    y = M.grouped_matmul(x.cuda(), w.cuda(), o, rows=rows.cuda()).cpu().double()
+    want = O.matmul(x, w, off, rows)
+    fine = torch.isfinite(want)
+    assert not fine[0, 3] and not fine[0, 7] and (want[0][fine[0]] == 0).all()
+    assert torch.equal(torch.isnan(y), torch.isnan(want))
+    assert torch.equal(y[torch.isinf(want)], want[torch.isinf(want)])
+    z = torch.where(torch.isfinite(w), w, torch.zeros((), dtype=dtype))
+    bound = base.HALF[dtype] * want.abs() + inner * base.ULP * O.matmul(x.abs(), z.abs(), off, rows) + base.TINY[dtype]
+    assert ((y - want).abs()[fine] <= bound[fine]).all()
