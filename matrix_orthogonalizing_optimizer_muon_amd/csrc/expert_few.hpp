@@ -88,7 +88,7 @@ __global__ __launch_bounds__(256) void k_few_matmul(ProdArgs a) {
   constexpr bool BRANCH = sizeof(T) == 2;
   __shared__ Acc16 lds[NW * CT * 64];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t t = blockIdx.x, tm = t / a.tiles_n;
+  const int64_t t = block_index(), tm = t / a.tiles_n;
   const int n0 = (int)(t - tm * a.tiles_n) * 16 * CT;
   RowTile rt;
   if (!find_tile<4>(a.offsets, a.experts, (int)a.n, tm, lane, rt)) return;
@@ -188,7 +188,7 @@ __global__ __launch_bounds__(512) void k_few_input_grad(ProdArgs a) {
   typedef typename Cols<T>::type cols_t;
   __shared__ Acc16 lds[NW * 4 * 64];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t t = blockIdx.x, tm = t / a.tiles_n;
+  const int64_t t = block_index(), tm = t / a.tiles_n;
   const int n0 = (int)(t - tm * a.tiles_n) * 64;
   RowTile rt;
   if (!find_tile<4>(a.offsets, a.experts, (int)a.n, tm, lane, rt)) return;

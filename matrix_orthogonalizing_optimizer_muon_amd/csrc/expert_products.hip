@@ -172,7 +172,7 @@ __global__ __launch_bounds__(256) void k_product(ProdArgs a) {
   constexpr int W = G::B / 2, NT = W / 32;
   __shared__ __attribute__((aligned(16))) char lds[2 * (PB + QB)];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, wy = w >> 1, wx = w & 1;
-  const int64_t t = blockIdx.x;
+  const int64_t t = block_index();
   const int tn = (int)(t % a.tiles_n);
   const int64_t tm = t / a.tiles_n;
   const int n0 = tn * G::B;
@@ -182,12 +182,13 @@ __global__ __launch_bounds__(256) void k_product(ProdArgs a) {
   Stager<T, PT> sp;
   Stager<T, QT> sq;
   if constexpr (MODE == kWeightGrad) {
+    if (tm >= (int64_t)a.experts * a.tiles_m) return;
     const int e = (int)(tm / a.tiles_m), m0 = (int)(tm % a.tiles_m) * G::B;
     int64_t b, end;
     expert_rows(a.offsets, e, (int)a.n, lane, b, end);
     if (a.parts > 1) {   // this block's part, of whole k-tiles
       const int64_t part = ((end - b + a.parts - 1) / a.parts + G::BK - 1) / G::BK * G::BK;
-      b += part * blockIdx.y;
+      b += part * blockIdx.z;
       end = b + part < end ? b + part : end;
       b = b < end ? b : end;
     }
@@ -246,7 +247,7 @@ __global__ __launch_bounds__(256) void k_product(ProdArgs a) {
   }
   const int64_t ldo = a.N;
   const bool whole = MODE != kWeightGrad || a.parts == 1;
-  float* sums = whole ? nullptr : a.partial + (int64_t)blockIdx.y * a.experts * a.M * ldo;
+  float* sums = whole ? nullptr : a.partial + (int64_t)blockIdx.z * a.experts * a.M * ldo;
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
     const int r = wy * W + 32 * i + (lane & 31);
@@ -635,7 +636,7 @@ int launch_product(ProdArgs a, int dtype, int64_t tiles_m, hipStream_t s) {
   a.tiles_n = (int32_t)ceil_div(a.N, side(dtype));
   const int64_t blocks = tiles_m * a.tiles_n;
   if (blocks > kMaxCount) return fail(MUON_EUNSUPPORTED, "more than 2^31 output tiles");
-  const dim3 grid((uint32_t)blocks, (uint32_t)a.parts);
+  const dim3 grid = grid_of_blocks(blocks, 256, (uint32_t)a.parts);
   if (dtype == MUON_BF16) hipLaunchKernelGGL((k_product<bf16_t, MODE>), grid, dim3(256), 0, s, a);
   else hipLaunchKernelGGL((k_product<float, MODE>), grid, dim3(256), 0, s, a);
   return launch_status("grouped product launch");
@@ -658,7 +659,7 @@ bool few(const ProdArgs& a, int dtype, int64_t* blocks) {
 template <int MODE>
 int launch_few(ProdArgs a, int dtype, int64_t blocks, hipStream_t s) {
   a.tiles_n = (int32_t)ceil_div(a.N, MODE == kMatmul ? 32 : 64);
-  const dim3 grid((uint32_t)blocks);
+  const dim3 grid = grid_of_blocks(blocks, MODE == kMatmul ? 256 : 512);
   if (MODE == kMatmul) {
     if (dtype == MUON_BF16) hipLaunchKernelGGL((k_few_matmul<bf16_t, 2>), grid, dim3(256), 0, s, a);
     else hipLaunchKernelGGL((k_few_matmul<float, 2>), grid, dim3(256), 0, s, a);

@@ -214,7 +214,7 @@ __device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t* sums, uin
 // in all) the block finishes the sort, else it leaves its masks and counts.
 template <bool ONE>
 __device__ __forceinline__ void after_choice(const RouteArgs& a, const uint64_t* mask, uint32_t* before,
-                                             uint32_t* sums, int tokens) {
+                                             uint32_t* sums, int64_t block, int tokens) {
   const int tid = threadIdx.x;
   __syncthreads();
   if (ONE) {
@@ -229,8 +229,8 @@ __device__ __forceinline__ void after_choice(const RouteArgs& a, const uint64_t*
     __syncthreads();
     place(a, mask, before, live, 0, tokens);
   } else if (tid < a.experts) {
-    a.mask[(int64_t)blockIdx.x * a.experts + tid] = mask[tid];
-    a.count[(int64_t)tid * a.stride + blockIdx.x] = (uint8_t)__popcll(mask[tid]);
+    a.mask[block * a.experts + tid] = mask[tid];
+    a.count[(int64_t)tid * a.stride + block] = (uint8_t)__popcll(mask[tid]);
   }
 }
 
@@ -241,7 +241,8 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_choose(RouteArgs a) {
   __shared__ uint32_t before[64 * V];
   __shared__ uint32_t sums[kRouteThreads / 64];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  const int64_t t0 = (int64_t)blockIdx.x * kTokensPerBlock;
+  const int64_t block = ONE ? 0 : block_index(), t0 = block * kTokensPerBlock;
+  if (!ONE && block >= a.blocks) return;
   const int tokens = (int)(a.tokens - t0 < kTokensPerBlock ? a.tokens - t0 : kTokensPerBlock);
   if (tid < 64 * V) mask[tid] = 0;
   __syncthreads();
@@ -269,7 +270,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_choose(RouteArgs a) {
       if (id >= 0) atomicOr((unsigned long long*)&mask[id], 1ull << tl);
     }
   }
-  after_choice<ONE>(a, mask, before, sums, tokens);
+  after_choice<ONE>(a, mask, before, sums, block, tokens);
 }
 
 // The block's 64 tokens at once, 16 lanes each: up to 16 V experts and 16
@@ -281,7 +282,8 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_choose_rows(RouteArgs a
   __shared__ uint32_t before[16 * V];
   __shared__ uint32_t sums[kRouteThreads / 64];
   const int tid = threadIdx.x, li = tid & 15, tl = tid >> 4;
-  const int64_t t0 = (int64_t)blockIdx.x * kTokensPerBlock, t = t0 + tl;
+  const int64_t block = ONE ? 0 : block_index(), t0 = block * kTokensPerBlock, t = t0 + tl;
+  if (!ONE && block >= a.blocks) return;
   const int tokens = (int)(a.tokens - t0 < kTokensPerBlock ? a.tokens - t0 : kTokensPerBlock);
   if (tid < 16 * V) mask[tid] = 0;
   __syncthreads();
@@ -308,7 +310,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_choose_rows(RouteArgs a
       if (id >= 0) atomicOr((unsigned long long*)&mask[id], 1ull << tl);
     }
   }
-  after_choice<ONE>(a, mask, before, sums, tokens);
+  after_choice<ONE>(a, mask, before, sums, block, tokens);
 }
 
 // One block per expert: how many of its rows are in earlier blocks, for more blocks than a placing
@@ -352,10 +354,11 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_place(RouteArgs a) {
   __shared__ uint32_t total[SCANNED ? 1 : kMaxExperts];
   __shared__ uint32_t sums[kRouteThreads / 64];
   const int tid = threadIdx.x;
-  const int64_t t0 = (int64_t)blockIdx.x * kTokensPerBlock;
+  const int64_t block = block_index(), t0 = block * kTokensPerBlock;
+  if (block >= a.blocks) return;
   const int tokens = (int)(a.tokens - t0 < kTokensPerBlock ? a.tokens - t0 : kTokensPerBlock);
   if (!SCANNED) {   // 16 threads add up an expert's counts
-    const int li = tid & 15, me = (int)blockIdx.x;
+    const int li = tid & 15, me = (int)block;
     for (int e0 = 0; e0 < a.experts; e0 += kRouteThreads / 16) {
       const int e = e0 + tid / 16;
       uint32_t earlier = 0, all = 0;
@@ -383,11 +386,11 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_place(RouteArgs a) {
   uint32_t live;
   const uint32_t b = block_prefix(c, sums, &live);
   if (tid < a.experts) {
-    mask[tid] = a.mask[(int64_t)blockIdx.x * a.experts + tid];
-    before[tid] = b + (SCANNED ? a.ahead[(int64_t)tid * a.blocks + blockIdx.x] : before[tid]);
-    if (blockIdx.x == 0) a.offsets[tid] = (int32_t)b;
+    mask[tid] = a.mask[block * a.experts + tid];
+    before[tid] = b + (SCANNED ? a.ahead[(int64_t)tid * a.blocks + block] : before[tid]);
+    if (block == 0) a.offsets[tid] = (int32_t)b;
   }
-  if (blockIdx.x == 0 && tid == 0) a.offsets[a.experts] = (int32_t)live;
+  if (block == 0 && tid == 0) a.offsets[a.experts] = (int32_t)live;
   __syncthreads();
   place(a, mask, before, live, t0, tokens);
 }
@@ -401,7 +404,7 @@ __global__ __launch_bounds__(256) void k_route_backward(const float* __restrict_
                                                         const int32_t* __restrict__ chosen, T* __restrict__ out,
                                                         int64_t tokens, int experts, int k, int normalize) {
   const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t t = block_index() * 4 + (threadIdx.x >> 6);
   if (t >= tokens) return;
   int id = -1;
   float wd = 0.f, w = 0.f;
@@ -462,7 +465,7 @@ __global__ __launch_bounds__(256) void k_route_backward_rows(const float* __rest
                                                              int64_t tokens, int experts, int k, int normalize) {
   __shared__ float part[16][16 * V + 1];
   const int li = threadIdx.x & 15, row = threadIdx.x >> 4;
-  const int64_t t = (int64_t)blockIdx.x * 16 + row;
+  const int64_t t = block_index() * 16 + row;
 #pragma unroll
   for (int v = 0; v < V; ++v) part[row][li * V + v] = 0.f;
   if (t >= tokens) return;   // a row's lanes are of one wave and share nothing with others
@@ -595,7 +598,7 @@ __global__ __launch_bounds__(256) void k_combine_backward(
     const float* __restrict__ weights, const int32_t* __restrict__ offsets, T* __restrict__ dy,
     float* __restrict__ dw, int experts, FastDiv k, int64_t n, int64_t cols) {
   const int lane = threadIdx.x & 63;
-  const uint32_t p = blockIdx.x * 4 + (threadIdx.x >> 6);
+  const uint32_t p = (uint32_t)block_index() * 4 + (threadIdx.x >> 6);
   if (p >= n) return;
   const uint32_t t = div_by(p, k);
   const int32_t s = slots[p], live = offsets[experts];
@@ -885,14 +888,14 @@ void launch_choose(const RouteArgs& a, hipStream_t s) {
   if (a.tokens <= kTokensPerBlock)
     hipLaunchKernelGGL((k_route_choose<T, V, true>), dim3(1), dim3(kRouteThreads), 0, s, a);
   else
-    hipLaunchKernelGGL((k_route_choose<T, V, false>), dim3(a.blocks), dim3(kRouteThreads), 0, s, a);
+    hipLaunchKernelGGL((k_route_choose<T, V, false>), grid_of_blocks(a.blocks, kRouteThreads), dim3(kRouteThreads), 0, s, a);
 }
 template <class T, int V>
 void launch_choose_rows(const RouteArgs& a, hipStream_t s) {
   if (a.tokens <= kTokensPerBlock)
     hipLaunchKernelGGL((k_route_choose_rows<T, V, true>), dim3(1), dim3(kRouteThreads), 0, s, a);
   else
-    hipLaunchKernelGGL((k_route_choose_rows<T, V, false>), dim3(a.blocks), dim3(kRouteThreads), 0, s, a);
+    hipLaunchKernelGGL((k_route_choose_rows<T, V, false>), grid_of_blocks(a.blocks, kRouteThreads), dim3(kRouteThreads), 0, s, a);
 }
 
 // Whether 16 lanes take a token, and the logits each of them has to hold then.
@@ -1057,9 +1060,9 @@ int muon_route(const void* logits, int dtype, int64_t tokens, int experts, int k
   if (a.blocks > kCountedBlocks) {
     hipLaunchKernelGGL(k_route_scan, dim3(experts), dim3(kRouteThreads), 0, s, a);
     if ((rc = launch_status("route scan launch"))) return rc;
-    hipLaunchKernelGGL((k_route_place<true>), dim3(a.blocks), dim3(kRouteThreads), 0, s, a);
+    hipLaunchKernelGGL((k_route_place<true>), grid_of_blocks(a.blocks, kRouteThreads), dim3(kRouteThreads), 0, s, a);
   } else {
-    hipLaunchKernelGGL((k_route_place<false>), dim3(a.blocks), dim3(kRouteThreads), 0, s, a);
+    hipLaunchKernelGGL((k_route_place<false>), grid_of_blocks(a.blocks, kRouteThreads), dim3(kRouteThreads), 0, s, a);
   }
   return launch_status("route place launch");
 }
@@ -1074,7 +1077,7 @@ int muon_route_backward(const float* dweights, const void* logits, const float* 
   if ((rc = check_device())) return rc;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (by_rows(experts, k)) {
-    const dim3 grid((uint32_t)ceil_div(tokens, 16));
+    const dim3 grid = grid_of_blocks(ceil_div(tokens, 16), 256);
     by_row_width(experts, [&](auto v) {
       constexpr int V = decltype(v)::value;
       if (dtype == MUON_BF16)
@@ -1086,7 +1089,7 @@ int muon_route_backward(const float* dweights, const void* logits, const float* 
     });
     return launch_status("route backward launch");
   }
-  const dim3 grid((uint32_t)ceil_div(tokens, 4));
+  const dim3 grid = grid_of_blocks(ceil_div(tokens, 4), 256);
   by_width(experts, [&](auto v) {
     constexpr int V = decltype(v)::value;
     if (dtype == MUON_BF16)
@@ -1135,7 +1138,7 @@ int muon_combine_backward(const void* dout, const void* y, const int32_t* slots,
   if ((rc = check_device())) return rc;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int64_t n = tokens * k;
-  const dim3 grid((uint32_t)ceil_div(n, 4));
+  const dim3 grid = grid_of_blocks(ceil_div(n, 4), 256);
   const FastDiv div = fast_div((uint32_t)k);
   if (dtype == MUON_BF16)
     hipLaunchKernelGGL((k_combine_backward<bf16_t>), grid, dim3(256), 0, s, (const bf16_t*)dout, (const bf16_t*)y,

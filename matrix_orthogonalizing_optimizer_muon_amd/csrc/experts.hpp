@@ -33,6 +33,14 @@ inline int launch_status(const char* what) {
 inline bool good_dtype(int d) { return d == MUON_F32 || d == MUON_BF16; }
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// A grid of `blocks` >= 1 blocks.  A launch takes less than 2^32 threads along x:
+// more blocks are laid out in rows along y, the last of which can go past
+// `blocks`.  block_index() is a block's number in it.
+inline dim3 grid_of_blocks(int64_t blocks, uint32_t threads, uint32_t z = 1) {
+  const int64_t y = ceil_div(blocks, ((int64_t(1) << 32) - 1) / threads);
+  return dim3((uint32_t)ceil_div(blocks, y), (uint32_t)y, z);
+}
+
 // ------------------------------------------------------------------ device
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -43,6 +51,8 @@ typedef u32x4 u32x4_any __attribute__((aligned(1)));
 typedef u32x2 u32x2_any __attribute__((aligned(1)));
 typedef uint32_t u32_any __attribute__((aligned(1)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ int64_t block_index() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
 
 struct bf16_t { uint16_t bits; };
 

@@ -69,3 +69,111 @@ def test_a_row_that_names_no_token_is_a_row_of_zeros(dtype, sizes):
     z = torch.where(torch.isfinite(w), w, torch.zeros((), dtype=dtype))
     bound = base.HALF[dtype] * want.abs() + inner * base.ULP * O.matmul(x.abs(), z.abs(), off, rows) + base.TINY[dtype]
     assert ((y - want).abs()[fine] <= bound[fine]).all()
+
+
+# ------------------------------------- more threads than a launch takes along one axis (2^32)
+
+def rand(*shape, seed, dtype=F):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(*shape, generator=g, device="cuda").to(dtype)
+
+
+def spots(n, at):
+    """Rows at both ends and around `at`."""
+    return torch.cat([torch.arange(max(0, m - 2000), min(n, m + 2000), device="cuda") for m in (0, n // 2, at, n)]).unique()
+
+
+def test_combine_backward_of_2_to_26_choices():
+    n = (1 << 26) + 5
+    y, dout = rand(n, 1, seed=5, dtype=B), rand(n, 1, seed=6, dtype=B)
+    w = rand(n, 1, seed=7)
+    slots = torch.arange(n, dtype=I, device="cuda").flip(0).view(n, 1).contiguous()
+    off = torch.tensor([0, n - 3], dtype=I, device="cuda")
+    base.poison((n, 1), B)
+    dy, dw = M.combine_backward(dout, y, slots, w, off)
+    want = (w * dout.float()).to(B).flip(0)       # one product each, rounded alike
+    want[n - 3:] = 0
+    assert torch.equal(dy, want)
+    assert torch.equal(dw, y.flip(0).float() * dout.float())
+
+
+def test_route_of_2_to_28_tokens():
+    n = (1 << 28) + 70
+    l = rand(n, 2, seed=8, dtype=B)
+    r = M.route(l, 1)
+    second = l[:, 1] > l[:, 0]
+    assert torch.equal(r.experts[:, 0], second.to(I))
+    assert (r.weights == 1).all()
+    first = n - int(second.sum())
+    assert r.offsets.tolist() == [0, first, n]
+    assert torch.equal(r.rows[:first], (~second).nonzero()[:, 0].to(I))
+    assert torch.equal(r.rows[first:], second.nonzero()[:, 0].to(I))
+    assert torch.equal(r.slots[r.rows.long(), 0], torch.arange(n, dtype=I, device="cuda"))
+    # and the gradient, 16 lanes a token
+    r = M.route(l, 1, normalize=False)
+    dw = rand(n, 1, seed=9)
+    base.poison((n, 2), B)
+    d = M.route_backward(dw, l, r, normalize=False)
+    assert torch.isfinite(d).all()
+    at = spots(n, (1 << 28) // 64 * 64)
+    ids, lc = r.experts[at, 0].tolist(), l[at].cpu()
+    p = torch.softmax(lc.double(), 1)
+    hot = torch.nn.functional.one_hot(torch.tensor(ids), 2).double()
+    up = (p * hot * dw[at].cpu().double()).sum(1, keepdim=True)
+    # exp of a difference below 2^4 rounded to fp32, a sum of two, a quotient; then products of two such
+    tol = (2 ** 4 + 2 + 8) * base.ULP
+    want = hot * up - p * up
+    base.close(d[at], want, base.HALF[B] * want.abs() + 2 * tol * (hot + p) * up.abs() + 2.0 ** -120, "logits' gradient")
+
+
+def test_route_backward_of_2_to_26_tokens_a_wave_each():
+    n, k = (1 << 26) + 9, 17
+    chosen = torch.arange(k, dtype=I, device="cuda").repeat(n, 1)
+    w = torch.full((n, k), 1 / 32, device="cuda")
+    dw = rand(n, k, seed=10)
+    l = torch.zeros(n, k, dtype=B, device="cuda")
+    r = M.Routing(w, chosen, chosen, chosen.view(-1), chosen[0])
+    base.poison((n, k), B)
+    d = M.route_backward(dw, l, r)
+    assert torch.isfinite(d).all()
+    at = spots(n, 1 << 26)
+    x = dw[at].cpu().double() / 32                  # exact
+    # 17 terms, and a product and a difference
+    want = x - x.sum(1, keepdim=True) / 32
+    size = x.abs() + x.abs().sum(1, keepdim=True) / 32
+    base.close(d[at], want, base.HALF[B] * want.abs() + 20 * base.ULP * size, "logits' gradient")
+
+
+@pytest.mark.parametrize("grad", [False, True])
+def test_rows_products_of_2_to_30_rows(grad):
+    n = (1 << 30) + 70
+    x = rand(n, 1, seed=11)
+    w = torch.tensor([[[1.7]]], device="cuda")
+    o = torch.tensor([0, n - 3], dtype=I, device="cuda")
+    y = M.grouped_input_grad(x, w, o) if grad else M.grouped_matmul(x, w, o)
+    assert (y[-3:] == 0).all()
+    assert torch.equal(y[:-3], x[:-3] * w[0])       # one product each
+
+
+def test_weight_grad_of_2_to_24_tiles():
+    experts, cols = 1024, (1 << 20) + 1
+    dy, x = rand(3, 1, seed=12), rand(3, cols, seed=13)
+    o = torch.tensor([0] * 513 + [3] * 512, dtype=I, device="cuda")
+    dw = M.grouped_weight_grad(dy, x, o)
+    assert (dw[:512] == 0).all() and (dw[513:] == 0).all()
+    want = (dy.double() * x.double()).sum(0).cpu()
+    size = (dy.double() * x.double()).abs().sum(0).cpu()
+    base.close(dw[512, 0], want, base.HALF[F] * want.abs() + 3 * base.ULP * size, "dw")
+
+
+@pytest.mark.parametrize("grad", [False, True])
+def test_few_rows_of_2_to_24_columns(grad):
+    experts, cols = 64, (1 << 24) - 1
+    w = rand(experts, cols, seed=14, dtype=B)
+    x = rand(experts, 1, seed=15, dtype=B)
+    o = torch.arange(experts + 1, dtype=I, device="cuda")
+    if grad:
+        y = M.grouped_input_grad(x, w.view(experts, 1, cols), o)
+    else:
+        y = M.grouped_matmul(x, w.view(experts, cols, 1), o)
+    assert torch.equal(y, (x.float() * w.float()).to(B))   # one product each
