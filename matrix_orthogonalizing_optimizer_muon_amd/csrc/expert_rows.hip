@@ -1184,17 +1184,17 @@ int muon_gated(const void* gu, int dtype, int64_t rows, int64_t cols, int kind, 
   const bool keep = q || scale;
   if ((rc = check_rows(dtype, rows, cols)) || (keep && (rc = check_kind(kind)))) return rc;
   if (rows == 0) return MUON_OK;
-  uint32_t items, kitems;
-  FastDiv div, kdiv;
+  // blocks that hold both g and u cannot be encoded by the fused kernel
+  const bool fused = keep && cols % kBlock == 0;
+  uint32_t items, kitems = 0;
+  FastDiv div, kdiv = {};
   if ((rc = items_of(rows, ceil_div(cols, 8), &items, &div)) ||
-      (rc = items_of(rows, 4 * ceil_div(2 * cols, kBlock), &kitems, &kdiv)))
+      (keep && !fused && (rc = items_of(rows, 4 * ceil_div(2 * cols, kBlock), &kitems, &kdiv))))
     return rc;
   if (!gu || !h || (keep && (!q || !scale))) return fail(MUON_EINVAL, "NULL pointer");
   if ((rc = check_device())) return rc;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const bool bf = dtype == MUON_BF16;
-  // blocks that hold both g and u cannot be encoded by the fused kernel
-  const bool fused = keep && cols % kBlock == 0;
   if (!fused) {
     if (bf) launch_gated<bf16_t, -1>(gu, cols, h, nullptr, nullptr, items, div, s);
     else launch_gated<float, -1>(gu, cols, h, nullptr, nullptr, items, div, s);

@@ -177,3 +177,17 @@ def test_few_rows_of_2_to_24_columns(grad):
     else:
         y = M.grouped_matmul(x, w.view(experts, cols, 1), o)
     assert torch.equal(y, (x.float() * w.float()).to(B))   # one product each
+
+
+def test_gated_of_2_to_29_rows_without_a_checkpoint():
+    """More rows than a checkpoint of them could have (its blocks of one column pair): none is asked for."""
+    n = (1 << 29) + 8
+    gu = rand(n, 2, seed=16, dtype=B)
+    base.poison((n, 1), B)
+    h = M.gated(gu)
+    assert torch.isfinite(h).all()
+    at = spots(n, 1 << 29)
+    want = O.gated(gu[at].cpu())
+    base.close(h[at], want, base.HALF[B] * want.abs() + 24 * base.ULP * want.abs() + 2.0 ** -120, "h")
+    with pytest.raises(M.MuonError, match="groups of 8 columns"):
+        M.gated(gu, checkpoint="int8")
