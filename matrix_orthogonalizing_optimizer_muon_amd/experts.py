@@ -10,6 +10,11 @@ the gradients these give.
     y = grouped_matmul(h, w_down, r.offsets)
     out = combine(y, r.slots, r.weights)
 
+Autograd does not see these calls: the backward functions here are called by
+the program (or by its own torch.autograd.Function).  So that no gradient is
+lost unnoticed, a tensor that requires grad is refused while grad mode is on;
+pass it detached, or call under torch.no_grad().
+
 Tensors are contiguous, on one GPU, float32 or bfloat16; outputs are new
 tensors.  Calls are asynchronous on the current stream, or on ``stream``, which
 then owns the outputs; inputs made on another stream have to be waited for
@@ -105,16 +110,23 @@ def _rows(t):
 
 
 def _placed(*named):
-    """The GPU all tensors of (name, tensor, ...) are on, by index; they must be contiguous."""
+    """The GPU all tensors of (name, tensor, ...) are on, by index; they must be contiguous, and
+    not require grad while grad mode is on."""
     dev = named[1].get_device()
     for t in named[1::2]:
-        if t.get_device() != dev or dev < 0 or not t.is_contiguous():
+        if t.get_device() != dev or dev < 0 or not t.is_contiguous() or t.requires_grad:
             _misplaced(named)
     return dev
 
 
 def _misplaced(named):
+    """Raises for what _placed found, if it is wrong (a tensor that requires grad is not under no_grad)."""
     dev = named[1].device
+    if torch.is_grad_enabled():
+        for name, t in zip(named[::2], named[1::2]):
+            if t.requires_grad:
+                raise ValueError(f"{name} requires grad, which autograd would lose here: call under torch.no_grad(), "
+                                 "or pass it detached, and call the backward functions")
     for name, t in zip(named[::2], named[1::2]):
         if not t.is_cuda:
             raise ValueError(f"{name} is not on the GPU")

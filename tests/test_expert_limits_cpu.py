@@ -6,7 +6,9 @@ import subprocess
 import sys
 
 import pytest
+import torch
 
+import matrix_orthogonalizing_optimizer_muon_amd as M
 from matrix_orthogonalizing_optimizer_muon_amd import _lib as L
 
 # a non-NULL address that no refused call may touch
@@ -32,6 +34,7 @@ def test_weight_grad_of_no_rows_needs_no_workspace():
 NOTHING_OF_MANY_COLUMNS = """
 import sys
 sys.path.insert(0, {root!r})
+import matrix_orthogonalizing_optimizer_muon_amd as M
 from matrix_orthogonalizing_optimizer_muon_amd import _lib as L
 lib, N = L.lib(), None
 for cols in (1 << 33, 1 << 35, (1 << 35) + 1, (1 << 62) + 8, (1 << 63) - 1):
@@ -62,3 +65,40 @@ def test_more_columns_than_a_launch_has(cols):
         assert lib.muon_gated(P, 1, rows, cols, 0, P, P, P, N) == L.MUON_EUNSUPPORTED
         assert lib.muon_gated_backward(P, P, N, N, 0, 1, rows, cols, P, P, N) == L.MUON_EUNSUPPORTED
         assert lib.muon_combine(P, P, P, 1, rows, 2, cols, P, N) == L.MUON_EUNSUPPORTED
+
+
+# ----------------------------------------------------------- tensors that require grad
+
+def g(*shape, dtype=torch.float32):
+    return torch.zeros(shape, dtype=dtype, requires_grad=True)
+
+
+def z(*shape, dtype=torch.float32):
+    return torch.zeros(shape, dtype=dtype)
+
+
+OFF = torch.tensor([0, 2, 4], dtype=torch.int32)
+SLOTS = torch.zeros(4, 2, dtype=torch.int32)
+GRADS = {
+    "route": ("logits", lambda: M.route(g(4, 8), 2)),
+    "route_backward": ("logits", lambda: M.route_backward(z(4, 2), g(4, 8), M.Routing(z(4, 2), SLOTS, SLOTS, SLOTS, OFF))),
+    "matmul, x": ("x", lambda: M.grouped_matmul(g(4, 8), z(2, 3, 8), OFF)),
+    "matmul, w": ("w", lambda: M.grouped_matmul(z(4, 8), g(2, 3, 8), OFF, rows=OFF)),
+    "input grad": ("w", lambda: M.grouped_input_grad(z(4, 3), g(2, 3, 8), OFF)),
+    "weight grad": ("x", lambda: M.grouped_weight_grad(z(4, 3), g(4, 8), OFF)),
+    "combine": ("weights", lambda: M.combine(z(8, 8), SLOTS, g(4, 2))),
+    "combine_backward": ("y", lambda: M.combine_backward(z(4, 8), g(8, 8), SLOTS, z(4, 2), OFF)),
+    "checkpoint": ("x", lambda: M.checkpoint(g(4, 8))),
+    "gated": ("gu", lambda: M.gated(g(4, 8))),
+    "gated_backward": ("gu", lambda: M.gated_backward(z(4, 4), g(4, 8))),
+}
+
+
+@pytest.mark.parametrize("name", list(GRADS))
+def test_a_tensor_that_requires_grad_is_refused(name):
+    """Its gradient would be lost: no call is recorded by autograd."""
+    arg, call = GRADS[name]
+    with pytest.raises(ValueError, match=f"{arg} requires grad"):
+        call()
+    with torch.no_grad(), pytest.raises(ValueError, match="is not on the GPU"):
+        call()                                    # taken as far as where it lies

@@ -191,3 +191,14 @@ def test_gated_of_2_to_29_rows_without_a_checkpoint():
     base.close(h[at], want, base.HALF[B] * want.abs() + 24 * base.ULP * want.abs() + 2.0 ** -120, "h")
     with pytest.raises(M.MuonError, match="groups of 8 columns"):
         M.gated(gu, checkpoint="int8")
+
+
+def test_parameters_under_no_grad():
+    x, w, _, rows, off = base.product_inputs([3, 0, 9], 24, 40, B, True, 0, 17)
+    o, wd = torch.tensor(off, dtype=I, device="cuda"), w.cuda()
+    p = torch.nn.Parameter(wd)
+    with pytest.raises(ValueError, match="w requires grad"):
+        M.grouped_matmul(x.cuda(), p, o, rows=rows.cuda())
+    with torch.no_grad():
+        y = M.grouped_matmul(x.cuda(), p, o, rows=rows.cuda())
+    assert torch.equal(y, M.grouped_matmul(x.cuda(), wd, o, rows=rows.cuda()))
