@@ -16,8 +16,8 @@ lost unnoticed, a tensor that requires grad is refused while grad mode is on;
 pass it detached, or call under torch.no_grad().
 
 Tensors are contiguous, on one GPU, float32 or bfloat16; outputs are new
-tensors.  Calls are asynchronous on the current stream, or on ``stream``, which
-then owns the outputs; inputs made on another stream have to be waited for
+tensors.  Calls are asynchronous on the current stream, or on ``stream`` (of the
+tensors' GPU; a Stream or a handle), which then owns the outputs; inputs made on another stream have to be waited for
 before, and kept until this one is done with them, as with any tensor.
 """
 import ctypes
@@ -136,13 +136,28 @@ def _misplaced(named):
             raise ValueError(f"{name} is not contiguous")
 
 
+def _device(values):
+    """Where the first tensor or Checkpoint of an operator's arguments is, None without one."""
+    for t in values:
+        if isinstance(t, Checkpoint):
+            t = t.q
+        if isinstance(t, torch.Tensor):
+            return t.device
+    return None
+
+
 def _on(fn):
     """Adds ``stream`` to an operator: it runs, and allocates, on that stream."""
     def call(*args, stream=None, **kw):
         if stream is None:
             return fn(*args, **kw)
+        dev = _device((*args, *kw.values()))
+        if dev is None or dev.type != "cuda":
+            return fn(*args, **kw)            # which refuses it
         if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream))
+            stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        elif stream.device != dev:
+            raise ValueError(f"stream is of {stream.device}, the tensors are on {dev}")
         with torch.cuda.stream(stream):
             return fn(*args, **kw)
     call.__name__, call.__qualname__, call.__doc__ = fn.__name__, fn.__name__, fn.__doc__

@@ -1,5 +1,6 @@
 """The borders of the expert-layer entry points on the CPU: sizes of zero, sizes past
 a limit, pointers that come in pairs.  Nothing here reaches a kernel."""
+import contextlib
 import ctypes
 import os
 import subprocess
@@ -102,3 +103,35 @@ def test_a_tensor_that_requires_grad_is_refused(name):
         call()
     with torch.no_grad(), pytest.raises(ValueError, match="is not on the GPU"):
         call()                                    # taken as far as where it lies
+
+
+# ------------------------------------------------------------------------- streams
+
+class OnGpu1(torch.Tensor):
+    device = property(lambda self: torch.device("cuda:1"))
+
+
+class OtherStream:
+    device = torch.device("cuda:0")
+
+
+def test_a_stream_is_of_the_tensors_gpu(monkeypatch):
+    """A handle is taken as one of the tensors' GPU, whichever is current; a Stream of another GPU is refused."""
+    from matrix_orthogonalizing_optimizer_muon_amd import experts as E
+    seen = []
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda *a, **kw: seen.append((a, kw)) or "stream")
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: seen.append(s) or contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "Stream", OtherStream)
+    x = z(4).as_subclass(OnGpu1)
+    op = E._on(lambda x: "ran")
+    assert op(x, stream=5) == op(x=x, stream=5) == "ran"
+    assert seen == [((5,), {"device": torch.device("cuda:1")}), "stream"] * 2
+    with pytest.raises(ValueError, match="stream is of cuda:0, the tensors are on cuda:1"):
+        op(x, stream=OtherStream())
+
+
+def test_tensors_off_the_gpu_are_refused_with_a_stream_too():
+    with pytest.raises(ValueError, match="not on the GPU"):
+        M.route(z(4, 8), 2, stream=0)
+    with pytest.raises(TypeError, match="takes a Checkpoint"):
+        M.restore([1], stream=0)
