@@ -167,8 +167,8 @@ struct RouteArgs {
   int32_t* offsets;
   uint64_t* mask;      // [blocks][experts]: which of the block's tokens chose the expert
   uint8_t* count;      // [experts][stride]: how many of them; a row is a multiple of 16 bytes
-  uint32_t* ahead;     // with a scan, [experts][blocks]: how many in earlier blocks
-  uint32_t* total;     // with a scan, [experts]
+  uint32_t* ahead;     // with the scan, [experts][blocks]: how many in earlier blocks
+  uint32_t* total;     // with the scan, [experts]
   int64_t tokens;
   int32_t experts, k, normalize, blocks, stride;
 };
@@ -344,9 +344,9 @@ __device__ __forceinline__ uint32_t sum_counts(u32x4 v, int n) {
   return s;
 }
 
-// Places of a block's choices.  Below 65537 tokens every block adds up all
-// counts (bytes: 16 KiB of L2 reads a block for 16384 tokens of 64 experts), which saves
-// the scan's launch: 4.8 us against 3.9 + 3.9.
+// Places of a block's choices.  Where the counts are few (counted_by_blocks) every
+// block adds up all of them (bytes: 16 KiB of L2 reads a block for 16384 tokens
+// of 64 experts), which saves the scan's launch: 4.8 us against 3.9 + 3.9.
 template <bool SCANNED>
 __global__ __launch_bounds__(kRouteThreads) void k_route_place(RouteArgs a) {
   __shared__ uint64_t mask[kMaxExperts];
@@ -862,15 +862,25 @@ dim3 grid_of(uint32_t items) { return dim3((items + 255) / 256); }
 
 int route_blocks(int64_t tokens) { return (int)ceil_div(tokens, kTokensPerBlock); }
 
-// More blocks than this take the scan: with 1024 a placing block reads 1 KiB of counts an expert.
-constexpr int kCountedBlocks = 1024;
+// Whether the placing blocks add up the counts by themselves; the others take the
+// scan.  Each reads experts x blocks bytes, 64 experts a round.  A whole route
+// call, us, without / with the scan, by tokens:
+//            1024         16384        32768         65536
+//     8:   7.8 / 9.7    8.3 / 10.1   11.3 / 12.8    20.1 / 19.1
+//    64:   9.5 / 11.1  10.7 / 12.2   16.3 / 16.2    31.3 / 26.2
+//   128:  13.8 / 14.9  15.5 / 16.5   26.7 / 24.7    53.5 / 40.9
+//   256:  21.2 / 21.9  24.5 / 24.5   45.0 / 39.1   115 / 85
+//  1024:  52.5 / 45.1  67.9 / 61.1   106 / 78      277 / 155
+bool counted_by_blocks(int64_t blocks, int experts) {
+  return experts <= 128 && blocks <= 512 && experts * blocks <= 32768;
+}
 int route_stride(int64_t tokens) { return (int)(ceil_div(route_blocks(tokens), 16) * 16); }
 
 uint64_t route_bytes(int64_t tokens, int experts) {
   if (tokens <= kTokensPerBlock) return 0;
   const uint64_t blocks = (uint64_t)route_blocks(tokens);
   const uint64_t fixed = (blocks * 8 + (uint64_t)route_stride(tokens)) * experts;
-  return (fixed + 15) / 16 * 16 + (blocks > kCountedBlocks ? (blocks + 1) * experts * 4 : 0);
+  return (fixed + 15) / 16 * 16 + (counted_by_blocks((int64_t)blocks, experts) ? 0 : (blocks + 1) * experts * 4);
 }
 
 int check_route(int dtype, int64_t tokens, int experts, int k) {
@@ -1057,7 +1067,7 @@ int muon_route(const void* logits, int dtype, int64_t tokens, int experts, int k
   }
   if ((rc = launch_status("route launch"))) return rc;
   if (!need) return MUON_OK;
-  if (a.blocks > kCountedBlocks) {
+  if (!counted_by_blocks(a.blocks, experts)) {
     hipLaunchKernelGGL(k_route_scan, dim3(experts), dim3(kRouteThreads), 0, s, a);
     if ((rc = launch_status("route scan launch"))) return rc;
     hipLaunchKernelGGL((k_route_place<true>), grid_of_blocks(a.blocks, kRouteThreads), dim3(kRouteThreads), 0, s, a);

@@ -135,3 +135,20 @@ def test_tensors_off_the_gpu_are_refused_with_a_stream_too():
         M.route(z(4, 8), 2, stream=0)
     with pytest.raises(TypeError, match="takes a Checkpoint"):
         M.restore([1], stream=0)
+
+
+# ------------------------------------------------------------------------- router
+
+@pytest.mark.parametrize("tokens,experts,scan", [
+    (16384, 64, False), (32768, 64, False), (32769, 64, True), (65536, 64, True), (16384, 128, False),
+    (16385, 128, True), (65, 129, True), (4096, 256, True), (65536, 256, True), (65536, 1024, True),
+    (32768, 8, False), (32769, 8, True), (64, 1024, None)])
+def test_route_scans_where_the_counts_are_many(tokens, experts, scan):
+    """A placing block reads every block's counts of all experts where the scan does not: 32 KiB at most, of at most 128
+    experts.  The workspace shows which (None: one block does it all and needs none)."""
+    need = ctypes.c_uint64()
+    assert L.lib().muon_route_workspace(tokens, experts, ctypes.byref(need)) == L.MUON_OK
+    blocks = -(-tokens // 64)
+    stride = -(-blocks // 16) * 16
+    counts = -(-(blocks * 8 + stride) * experts // 16) * 16        # masks and counts
+    assert need.value == (0 if scan is None else counts + (4 * (blocks + 1) * experts if scan else 0))

@@ -202,3 +202,22 @@ def test_parameters_under_no_grad():
     with torch.no_grad():
         y = M.grouped_matmul(x.cuda(), p, o, rows=rows.cuda())
     assert torch.equal(y, M.grouped_matmul(x.cuda(), wd, o, rows=rows.cuda()))
+
+
+@pytest.mark.parametrize("tokens,experts,k", [(32768, 64, 8), (32769, 64, 8), (16384, 128, 3), (16385, 128, 3),
+                                              (20000, 129, 2), (65536, 256, 8), (65537, 300, 4), (65536, 1024, 2),
+                                              (32768, 3, 2), (32769, 3, 2), (65, 129, 17)])
+def test_route_on_both_sides_of_its_scan(tokens, experts, k):
+    l = rand(tokens, experts, seed=18)
+    l[::7, experts // 2] = -math.inf
+    r = M.route(l, k)
+    _, ids = torch.sort(l, dim=1, descending=True, stable=True)
+    ids = ids[:, :k].contiguous()
+    order = torch.argsort(ids.reshape(-1), stable=True)
+    slots = torch.empty_like(order)
+    slots[order] = torch.arange(tokens * k, device="cuda")
+    assert torch.equal(r.experts.long(), ids)
+    assert torch.equal(r.rows.long(), order // k)
+    assert torch.equal(r.slots.long().reshape(-1), slots)
+    counts = torch.bincount(ids.reshape(-1), minlength=experts).cumsum(0)
+    assert r.offsets.tolist() == [0] + counts.tolist()
