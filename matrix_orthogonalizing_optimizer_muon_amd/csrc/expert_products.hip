@@ -674,9 +674,13 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 
 // The large kernels copy 16-byte chunks that a row holds whole and address an
 // operand (that of gathered rows whole, else one tile's rows) by 31 bits.
+bool chunked_sides(int dtype, int64_t c0, int64_t c1) {
+  return dtype == MUON_BF16 && c0 % 8 == 0 && c1 % 8 == 0 && c0 < (1 << 21) && c1 < (1 << 21);
+}
+bool gathered_whole(int64_t x_rows, int64_t cols) { return x_rows * cols < (int64_t(1) << 30); }
 bool chunked(const ProdArgs& a, int dtype, int64_t c0, int64_t c1, int64_t gathered_cols) {
-  return dtype == MUON_BF16 && c0 % 8 == 0 && c1 % 8 == 0 && aligned16(a.p) && aligned16(a.q) && aligned16(a.out) &&
-         c0 < (1 << 21) && c1 < (1 << 21) && (!a.rows || a.x_rows * gathered_cols < (int64_t(1) << 30));
+  return chunked_sides(dtype, c0, c1) && aligned16(a.p) && aligned16(a.q) && aligned16(a.out) &&
+         (!a.rows || gathered_whole(a.x_rows, gathered_cols));
 }
 
 template <int MODE>
@@ -706,12 +710,14 @@ int launch_weight(ProdArgs a, hipStream_t s) {
 // blocks a CU, two k-tiles in a part on average.  Without and with them, us (bf16):
 //   9 x 192 x 208, 26960 rows:  99, 29    5 x 64 x 1280, 28945 rows: 89, 40
 //   2 x 512 x 512, 16384 rows: 185, 40    6 x 2752 x 64, 8016 rows:  28, 29
-// With 128 large tiles (8 x 1024 x 1024, 16384 rows) the small ones take 141 us, the large ones 95.
+// With 128 large tiles (8 x 1024 x 1024, 16384 rows) the small ones take 141 us, the large ones 95; 128 x 128 x 128,
+// 100000 rows, 24 in parts, 16.  No parts, and so no workspace, where the large ones take the sizes; the few calls of
+// these whose arrays are off 16 bytes: 128 x 128 x 128, 100000 rows 21 without parts, 24 with; 64 x 64 20, 16.
 struct WeightCut {
   bool small;
   int parts;
 };
-WeightCut weight_cut(int dtype, int64_t n, int experts, int64_t outer, int64_t inner) {
+WeightCut weight_cut(int dtype, int64_t n, int64_t x_rows, int experts, int64_t outer, int64_t inner) {
   const int64_t large = experts * ceil_div(outer, 256) * ceil_div(inner, 256);
   const int64_t tiles = experts * ceil_div(outer, side(dtype)) * ceil_div(inner, side(dtype));
   const int64_t k_tile = dtype == MUON_BF16 ? Tile<bf16_t>::BK : Tile<float>::BK;
@@ -720,7 +726,8 @@ WeightCut weight_cut(int dtype, int64_t n, int experts, int64_t outer, int64_t i
   if (parts > most) parts = most;
   if (parts > 64) parts = 64;
   const bool few = large <= kWalkers && n <= 64 * (int64_t)experts;
-  if (few || parts < 1) parts = 1;
+  const bool by_large = large > 96 && chunked_sides(dtype, outer, inner) && gathered_whole(x_rows, inner);
+  if (few || by_large || parts < 1) parts = 1;
   return WeightCut{few || (large <= 96 && parts > 1), (int)parts};
 }
 
@@ -730,7 +737,7 @@ uint64_t dense_bytes(int dtype, int64_t x_rows, int64_t inner) {
 // Workspace of the weight gradient: a checkpoint's rows as dense values (`kept`; where there are rows to sum), and
 // the parts' sums.
 uint64_t weight_grad_bytes(int dtype, int64_t n, int64_t x_rows, int experts, int64_t outer, int64_t inner, bool kept) {
-  const int parts = weight_cut(dtype, n, experts, outer, inner).parts;
+  const int parts = weight_cut(dtype, n, x_rows, experts, outer, inner).parts;
   return (kept && n > 0 ? dense_bytes(dtype, x_rows, inner) : 0) +
          (parts > 1 ? (uint64_t)parts * experts * outer * inner * 4 : 0);
 }
@@ -811,7 +818,7 @@ int muon_grouped_weight_grad(const void* dy, const void* x, const void* q, const
     x = workspace;
   }
   ProdArgs a = {dy, x, dw, offsets, rows, n, x_rows, experts, (int32_t)outer, (int32_t)inner, 0, 0, 0, 1, nullptr};
-  const WeightCut cut = weight_cut(dtype, n, experts, outer, inner);
+  const WeightCut cut = weight_cut(dtype, n, x_rows, experts, outer, inner);
   if (!cut.small && chunked(a, dtype, inner, outer, inner)) return launch_weight(a, s);
   a.tiles_m = (int32_t)ceil_div(outer, side(dtype));
   a.parts = cut.parts;

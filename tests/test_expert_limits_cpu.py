@@ -152,3 +152,16 @@ def test_route_scans_where_the_counts_are_many(tokens, experts, scan):
     stride = -(-blocks // 16) * 16
     counts = -(-(blocks * 8 + stride) * experts // 16) * 16        # masks and counts
     assert need.value == (0 if scan is None else counts + (4 * (blocks + 1) * experts if scan else 0))
+
+
+# ---------------------------------------------------------------- weight gradient
+
+@pytest.mark.parametrize("dtype,n,experts,outer,inner,some", [
+    (L.MUON_BF16, 100000, 128, 128, 128, False), (L.MUON_BF16, 100000, 128, 256, 128, False),
+    (L.MUON_BF16, 100000, 128, 129, 128, True), (L.MUON_F32, 100000, 128, 64, 64, True),
+    (L.MUON_BF16, 100000, 64, 128, 128, True), (L.MUON_BF16, 28945, 5, 64, 1280, True)])
+def test_weight_grad_asks_for_no_workspace_that_it_leaves(dtype, n, experts, outer, inner, some):
+    """The parts' sums, where the tiles that make them take the sizes."""
+    need = ctypes.c_uint64(99)
+    assert L.lib().muon_grouped_weight_grad_workspace(dtype, n, n, experts, outer, inner, 0, ctypes.byref(need)) == L.MUON_OK
+    assert (need.value > 0) == some

@@ -221,3 +221,17 @@ def test_route_on_both_sides_of_its_scan(tokens, experts, k):
     assert torch.equal(r.slots.long().reshape(-1), slots)
     counts = torch.bincount(ids.reshape(-1), minlength=experts).cumsum(0)
     assert r.offsets.tolist() == [0] + counts.tolist()
+
+
+@pytest.mark.parametrize("off", [1, 8])
+@pytest.mark.parametrize("gather", [False, True])
+def test_weight_grad_of_many_small_matrices(off, gather):
+    """Few tiles of long sums and more than 96 large ones, on 16 bytes (8 elements past) and off them."""
+    counts = [130 + 3 * (e % 40) for e in range(128)]
+    x, _, dy, rows, offsets = base.product_inputs(counts, 128, 120, B, gather, 0, 19)
+    base.poison((128, 128, 120), B)
+    dw = M.grouped_weight_grad(base.guarded(dy, off), base.guarded(x, off), torch.tensor(offsets, dtype=I, device="cuda"),
+                               rows=rows.cuda() if gather else None)
+    want = O.weight_grad(dy, x, offsets, rows)
+    size = O.weight_grad(dy.abs(), x.abs(), offsets, rows)
+    base.close(dw, want, base.HALF[B] * want.abs() + max(counts) * base.ULP * size, "dw")
