@@ -235,3 +235,52 @@ def test_weight_grad_of_many_small_matrices(off, gather):
     want = O.weight_grad(dy, x, offsets, rows)
     size = O.weight_grad(dy.abs(), x.abs(), offsets, rows)
     base.close(dw, want, base.HALF[B] * want.abs() + max(counts) * base.ULP * size, "dw")
+
+
+# ------------------------------------------------------------- operands past 2^31 bytes and elements
+
+def test_products_that_gather_from_2_to_30_elements():
+    """More than the large tiles' 31-bit lane offsets hold: the tiles staged through registers take them."""
+    inner, outer, experts, x_rows = 1024, 512, 64, (1 << 20) + 8
+    x = torch.zeros(x_rows, inner, dtype=B, device="cuda")
+    tail = rand(300, inner, seed=20, dtype=B)
+    x[-300:] = tail
+    x[:300] = tail.flip(0)
+    n = 3000
+    g = gen(21)
+    pick = torch.randint(0, 600, (n,), generator=g)
+    rows = torch.where(pick < 300, pick, pick - 600 + x_rows).to(I)
+    far = torch.where(pick < 300, 299 - pick, pick - 300)           # the row of `tail` that a row names
+    off = [n * e // experts for e in range(experts + 1)]
+    o = torch.tensor(off, dtype=I, device="cuda")
+    w = rand(experts, outer, inner, seed=22, dtype=B)
+    dy = rand(n, outer, seed=23, dtype=B)
+    near = tail.cpu()[far]
+    base.poison((n, outer), B)
+    y = M.grouped_matmul(x, w, o, rows=rows.cuda())
+    want = O.matmul(near, w.cpu(), off)
+    base.close(y, want, base.HALF[B] * want.abs() + inner * base.ULP * O.matmul(near.abs(), w.cpu().abs(), off), "matmul")
+    base.poison((experts, outer, inner), B)
+    dw = M.grouped_weight_grad(dy, x, o, rows=rows.cuda())
+    want = O.weight_grad(dy.cpu(), near, off)
+    size = O.weight_grad(dy.cpu().abs(), near.abs(), off)
+    base.close(dw, want, base.HALF[B] * want.abs() + 47 * base.ULP * size, "dw")
+
+
+def test_weight_grad_by_large_tiles_of_2_to_31_elements():
+    inner, outer, experts, n = 2048, 16, 16, (1 << 20) + 40         # 128 large tiles
+    x = torch.zeros(n, inner, dtype=B, device="cuda")
+    dy = torch.zeros(n, outer, dtype=B, device="cuda")
+    for t, seed in ((x, 24), (dy, 25)):
+        t[-300:] = rand(300, t.shape[1], seed=seed, dtype=B)
+        t[:100] = rand(100, t.shape[1], seed=seed + 2, dtype=B)
+    off = [e * (n // experts) for e in range(experts)] + [n]
+    off[-2] = n - 200
+    o = torch.tensor(off, dtype=I, device="cuda")
+    base.poison((experts, outer, inner), B)
+    dw = M.grouped_weight_grad(dy, x, o)
+    assert (dw[1:-2] == 0).all()
+    for e, part in ((0, slice(0, 100)), (-2, slice(n - 300, n - 200)), (-1, slice(n - 200, n))):
+        a, b = dy[part].cpu().double(), x[part].cpu().double()
+        want, size = a.t() @ b, a.abs().t() @ b.abs()
+        base.close(dw[e], want, base.HALF[B] * want.abs() + 200 * base.ULP * size, f"dw of {e}")
