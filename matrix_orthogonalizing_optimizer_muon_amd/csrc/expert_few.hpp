@@ -76,7 +76,7 @@ __device__ __forceinline__ bool few_sum(Acc16 (&acc)[NQ], Acc16* lds, Acc16& sum
 
 // y[r] = x[r] W_e^T: strips of 16 CT columns, k in steps of 64 bytes a row.
 // Bound by the matrices' way from memory: 8 rows of 8 experts, 2816 x 2048 bf16,
-// 92 MB: 20 us, 4.5 TB/s; 222 rows of 59 experts, 2048 x 1408, 341 MB: 65 us, 5.2 TB/s.
+// 92 MB: 20 us, 4.6 TB/s; 222 rows of 59 experts, 2048 x 1408, 341 MB: 65 us, 5.2 TB/s.
 // A column that does not exist reads another's values instead, which reach only
 // results that are not stored.  A row that x does not have is zeros (its product
 // with an infinity is NaN, as in the tiles): in bf16 its lanes load nothing, in

@@ -284,8 +284,8 @@ __global__ __launch_bounds__(256) void k_add_parts(const float* __restrict__ par
 // ------------------------------------------------------------- large tiles
 
 // Products of many rows.  65536 rows (8192 tokens to 8 of 64 experts) through
-// 2816 x 2048: 695 to 703 us, 1075 to 1088 TFLOP/s; the input gradient of half
-// of them 402 to 414 us, the weight gradient 775 us.  A k-tile of 64 takes a block
+// 2816 x 2048: 695 to 724 us, 1044 to 1088 TFLOP/s; the input gradient of half
+// of them 402 to 422 us, the weight gradient 770 us.  A k-tile of 64 takes a block
 // about 1.7 us in the first: 1.25 without the copies (the MFMAs at the clock that
 // power leaves), the rest for the copies, half of that for those that miss L2.
 //
@@ -645,11 +645,11 @@ int launch_product(ProdArgs a, int dtype, int64_t tiles_m, hipStream_t s) {
 // Whether the kernels for few rows take a rows product (and their blocks): where
 // an expert has so few rows that its matrix's way from memory is what counts, or
 // where the tile kernels would leave most CUs idle for one tile's length.
-// Measured against the faster tile kernel, us:
-//   n / experts 4, bf16, 64 x 2816 x 2048: 142 against 154 (input gradient 125, 128); at 8: 174, 164 (149, 133)
-//   16, fp32, 64 x 1408 x 1024: 127 against 142 (93, 126); at 32: 180, 158 (142, 157)
-//   blocks 1280, 8 x 1024 x 1024, bf16 18 against 18, fp32 32 against 34; 2560: 29, 23 and 55, 50
-//   blocks 513, fp32, 8 x 257 x 513: 13 against 20
+// Measured against the faster tile kernel, us (even experts):
+//   n / experts 4, bf16, 64 x 2816 x 2048: 145 against 159 (input gradient 135, 128); at 8: 152, 160 (140, 128)
+//   16, fp32, 64 x 1408 x 1024: 93 against 122 (75, 113); at 32: 159, 124 (108, 116)
+//   blocks 1280, 8 x 1024 x 1024, bf16 16 against 16, fp32 30 against 32; 2560: 27, 23 and 51, 48
+//   blocks 513, fp32, 8 x 257 x 513: 11 against 19
 template <int MODE>
 bool few(const ProdArgs& a, int dtype, int64_t* blocks) {
   *blocks = row_tiles(a.n, a.experts, 16) * ceil_div(a.N, MODE == kMatmul ? 32 : 64);

@@ -534,7 +534,7 @@ __device__ __forceinline__ void values8(const u32x4 (&r)[2], float (&v)[8]) {
 // out[t] = sum_j w_j y[slot_j]: a thread holds eight columns of one token.  The
 // rows of eight choices (four in fp32) are on their way at once.  Bound by the
 // rows' way from memory: 8192 tokens of 2048 bf16 columns and 8 choices take 76
-// us (302 MB, 4.0 TB/s; 80 us one row after the other, 77 with a wave a token
+// us (302 MB, 4.0 TB/s of the copy probe's 6.2; 80 us one row after the other, 77 with a wave a token
 // and scalar loads of slots and weights).
 template <class T>
 __global__ __launch_bounds__(256) void k_combine(const T* __restrict__ y, const int32_t* __restrict__ slots,
@@ -590,8 +590,8 @@ __global__ __launch_bounds__(256) void k_combine(const T* __restrict__ y, const 
 // dy[slot_j] = w_j dout[t], dw_j = <y[slot_j], dout[t]>: a wave per choice;
 // the waves of one token sit side by side, so dout comes from cache but once.
 // The wave of place p also clears row p of dy where no expert has it; such a
-// row is written by no other wave, whatever slot names it.  The sizes above: 106
-// us, 570 MB, 5.4 TB/s.
+// row is written by no other wave, whatever slot names it.  The sizes above: 108
+// us, 570 MB, 5.3 TB/s.
 template <class T>
 __global__ __launch_bounds__(256) void k_combine_backward(
     const T* __restrict__ dout, const T* __restrict__ y, const int32_t* __restrict__ slots,
@@ -731,7 +731,7 @@ __device__ __forceinline__ void load_kept(const uint8_t* q, const uint8_t* scale
 }
 
 // A thread encodes eight columns; four threads hold a block.  4099 x 2056 bf16:
-// 7.2 us for 25 MB, most of it the launch and the way to memory; restoring 6.4.
+// 7.4 us for 25 MB, most of it the launch and the way to memory; restoring 5.9.
 template <class T, int KIND>
 __global__ __launch_bounds__(256) void k_checkpoint(const T* __restrict__ x, uint8_t* __restrict__ q,
                                                     uint8_t* __restrict__ scale, uint32_t items, FastDiv groups,
@@ -784,7 +784,7 @@ __device__ __forceinline__ float sigmoid<bf16_t>(float g) {
 
 // h = g sigma(g) u of [g | u], and with KIND its 8-bit checkpoint in the same
 // pass (f a multiple of 32, so that no block holds both g and u).  Bound by
-// memory: 32768 x 1408 bf16 with its int8 checkpoint, 372 MB, 70 us, 5.3 TB/s.
+// memory: 32768 x 1408 bf16 with its int8 checkpoint, 372 MB, 69 us, 5.4 TB/s.
 template <class T, int KIND>
 __global__ __launch_bounds__(256) void k_gated(const T* __restrict__ gu, T* __restrict__ h, uint8_t* __restrict__ q,
                                                uint8_t* __restrict__ scale, uint32_t items, FastDiv groups,
@@ -814,7 +814,7 @@ __global__ __launch_bounds__(256) void k_gated(const T* __restrict__ gu, T* __re
 
 // dg = dh u sigma(g) (1 + g (1 - sigma(g))), du = dh g sigma(g), and h again
 // (what the down projection's weight gradient reads), from [g | u] or from
-// its checkpoint.  The sizes above, from the checkpoint: 464 MB, 77 us, 6.0 TB/s.
+// its checkpoint.  The sizes above, from the checkpoint: 464 MB, 76 us, 6.1 TB/s.
 template <class T, int KIND>
 __global__ __launch_bounds__(256) void k_gated_backward(const T* __restrict__ dh, const T* __restrict__ gu,
                                                         const uint8_t* __restrict__ q,
