@@ -582,6 +582,90 @@ int muon_gated_backward(const void* dh, const void* gu, const void* q, const uin
                         int kind, int dtype, int64_t rows, int64_t cols, void* dgu, void* h,
                         void* stream);
 
+/*
+ * Operators over a vocabulary: the embedding of tokens and the losses of the
+ * classifier, the two ends of a model, whose parameters' gradients
+ * muon_adamw_step takes.  table, w: vocab x dim; x: tokens x dim.
+ *
+ * For all of them what is said above of the expert layer's operators holds
+ * (arrays, types, sums, streams, graphs, workspaces, errors).  Indices (tokens,
+ * targets, a teacher's ids) are signed whole numbers of index_bytes, 4 or 8; one
+ * outside [0, vocab) names nothing and is never followed.  Two calls that share a
+ * workspace must be ordered.  Limits (EUNSUPPORTED): tokens, vocab and
+ * tokens k < 2^31, dim < 2^24, k <= 256.
+ */
+
+/*
+ * Embedding.
+ *   muon_embed           out[t] = scale table[tokens[t]] (n x dim); zeros where
+ *                        tokens[t] names nothing
+ *   muon_embed_backward  dtable[v] = scale times the sum of dout[t] over the t with
+ *                        tokens[t] = v, added up in an order that n and the tokens
+ *                        alone determine; every row is written
+ */
+int muon_embed(const void* tokens, int index_bytes, const void* table, int dtype, int64_t n,
+               int64_t vocab, int64_t dim, float scale, void* out, void* stream);
+int muon_embed_backward_workspace(int64_t n, int64_t vocab, int64_t dim, uint64_t* bytes);
+int muon_embed_backward(const void* dout, const void* tokens, int index_bytes, int dtype, int64_t n,
+                        int64_t vocab, int64_t dim, float scale, void* dtable, void* workspace,
+                        uint64_t workspace_bytes, void* stream);
+
+/*
+ * Cross entropy of the logits l = x w^T, which are never in memory whole:
+ *   lse[t] = log sum_v exp(l_tv),  loss[t] = lse[t] - l_t,targets[t]
+ * A target that names nothing takes its row out: loss and lse 0, its gradient
+ * zeros, its x not read.  Work goes with the rows that are left.
+ *   muon_classifier_loss           loss and lse (fp32, tokens)
+ *   muon_classifier_loss_grads     these and, for the loss's gradient dloss (fp32,
+ *                                  tokens), dx (tokens x dim) and dw (vocab x dim):
+ *                                  dl_tv = dloss[t] (exp(l_tv - lse[t]) - [v = targets[t]]),
+ *                                  dx = dl w, dw = dl^T x, with dl rounded to dtype
+ *   muon_classifier_loss_backward  dx and dw from the lse that a loss call gave
+ *                                  (computes the logits again)
+ * muon_classifier_loss_workspace: bytes that a call needs; gradients 0: the loss
+ * alone, 1: with gradients, 2: gradients from lse.
+ */
+int muon_classifier_loss_workspace(int dtype, int64_t tokens, int64_t vocab, int64_t dim,
+                                   int gradients, uint64_t* bytes);
+int muon_classifier_loss(const void* x, const void* w, const void* targets, int index_bytes,
+                         int dtype, int64_t tokens, int64_t vocab, int64_t dim, float* loss,
+                         float* lse, void* workspace, uint64_t workspace_bytes, void* stream);
+int muon_classifier_loss_grads(const float* dloss, const void* x, const void* w,
+                               const void* targets, int index_bytes, int dtype, int64_t tokens,
+                               int64_t vocab, int64_t dim, float* loss, float* lse, void* dx,
+                               void* dw, void* workspace, uint64_t workspace_bytes, void* stream);
+int muon_classifier_loss_backward(const float* dloss, const void* x, const void* w,
+                                  const void* targets, const float* lse, int index_bytes, int dtype,
+                                  int64_t tokens, int64_t vocab, int64_t dim, void* dx, void* dw,
+                                  void* workspace, uint64_t workspace_bytes, void* stream);
+
+/*
+ * Distillation from a teacher's k largest logits: teacher (teacher_dtype,
+ * tokens x k) at ids (tokens x k), q = softmax(teacher / temperature) over a
+ * row's entries, lse[t] = log sum_v exp(l_tv / temperature),
+ *   loss[t] = temperature^2 sum_j q_tj (log q_tj - l_t,id_tj / temperature + lse[t])
+ *   dl_tv = dloss[t] temperature (exp(l_tv / temperature - lse[t]) - sum of q_tj over id_tj = v)
+ * An entry whose id names nothing or whose logit is -inf or NaN is not there
+ * (+inf counts as the largest fp32); a row without entries is taken out, as above.
+ * The calls are those of the cross entropy.
+ */
+int muon_distill_loss_workspace(int dtype, int64_t tokens, int64_t vocab, int64_t dim, int k,
+                                int gradients, uint64_t* bytes);
+int muon_distill_loss(const void* x, const void* w, const void* teacher, int teacher_dtype,
+                      const void* ids, int index_bytes, int dtype, int64_t tokens, int64_t vocab,
+                      int64_t dim, int k, float temperature, float* loss, float* lse,
+                      void* workspace, uint64_t workspace_bytes, void* stream);
+int muon_distill_loss_grads(const float* dloss, const void* x, const void* w, const void* teacher,
+                            int teacher_dtype, const void* ids, int index_bytes, int dtype,
+                            int64_t tokens, int64_t vocab, int64_t dim, int k, float temperature,
+                            float* loss, float* lse, void* dx, void* dw, void* workspace,
+                            uint64_t workspace_bytes, void* stream);
+int muon_distill_loss_backward(const float* dloss, const void* x, const void* w,
+                               const void* teacher, int teacher_dtype, const void* ids,
+                               const float* lse, int index_bytes, int dtype, int64_t tokens,
+                               int64_t vocab, int64_t dim, int k, float temperature, void* dx,
+                               void* dw, void* workspace, uint64_t workspace_bytes, void* stream);
+
 /* MUON_ABI_VERSION of the library. */
 int muon_abi_version(void);
 

@@ -10,7 +10,9 @@ update runs in the library's HIP kernels; there is no fallback path.
     plan.step(params, grads, momenta, lr=0.02, beta=0.95, wd=0.01)
 
 The operators of a mixture-of-experts layer, whose matrices' gradients such a
-plan takes, are in experts.py and reached as attributes of this package.
+plan takes, are in experts.py, those over a vocabulary (embedding, the
+classifier's losses), whose gradients AdamWPlan takes, in vocabulary.py; both
+are reached as attributes of this package.
 """
 import ctypes
 import importlib
@@ -18,20 +20,24 @@ import importlib
 from . import _lib as L
 from ._lib import MuonError  # noqa: F401
 
-# the operators of experts.py, which imports torch: loaded on first use
+# the operators of experts.py and vocabulary.py, which import torch: loaded on first use
 _EXPERTS = ["route", "route_backward", "Routing", "grouped_matmul", "grouped_input_grad", "grouped_weight_grad",
             "combine", "combine_backward", "checkpoint", "restore", "Checkpoint", "gated", "gated_backward"]
+_VOCABULARY = ["embed", "embed_backward", "classifier_loss", "classifier_loss_grads", "classifier_loss_backward",
+               "distill_loss", "distill_loss_grads", "distill_loss_backward"]
 
 __all__ = ["MuonPlan", "AdamWPlan", "MuonError", "library_path", "assign_owners",
-           "probe_mfma_bf16", "probe_nt_bf16", "probe_nt_out_bf16", "probe_hbm_copy", "step_noalloc", *_EXPERTS]
+           "probe_mfma_bf16", "probe_nt_bf16", "probe_nt_out_bf16", "probe_hbm_copy", "step_noalloc", *_EXPERTS,
+           *_VOCABULARY]
 
 
 def __getattr__(name):
-    if name not in _EXPERTS:
-        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    experts = importlib.import_module(__name__ + ".experts")
-    globals().update({n: getattr(experts, n) for n in _EXPERTS})
-    return globals()[name]
+    for module, names in ((".experts", _EXPERTS), (".vocabulary", _VOCABULARY)):
+        if name in names:
+            found = importlib.import_module(__name__ + module)
+            globals().update({n: getattr(found, n) for n in names})
+            return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def library_path():

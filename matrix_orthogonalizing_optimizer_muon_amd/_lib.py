@@ -57,7 +57,7 @@ class LaunchInterval(ctypes.Structure):
 _PP = ctypes.POINTER(ctypes.c_void_p)
 _FP = ctypes.POINTER(ctypes.c_float)
 _U64P = ctypes.POINTER(ctypes.c_uint64)
-_P, _I, _N, _U64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint64
+_P, _I, _N, _U64, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float
 
 # name -> (restype, argtypes); must list every function include/muon.h declares.
 PROTOTYPES = {
@@ -135,6 +135,19 @@ PROTOTYPES = {
     "muon_restore": (_I, [_P, _P, _I, _N, _N, _I, _P, _P]),
     "muon_gated": (_I, [_P, _I, _N, _N, _I, _P, _P, _P, _P]),
     "muon_gated_backward": (_I, [_P, _P, _P, _P, _I, _I, _N, _N, _P, _P, _P]),
+    "muon_embed": (_I, [_P, _I, _P, _I, _N, _N, _N, _F, _P, _P]),
+    "muon_embed_backward_workspace": (_I, [_N, _N, _N, _U64P]),
+    "muon_embed_backward": (_I, [_P, _P, _I, _I, _N, _N, _N, _F, _P, _P, _U64, _P]),
+    "muon_classifier_loss_workspace": (_I, [_I, _N, _N, _N, _I, _U64P]),
+    "muon_classifier_loss": (_I, [_P, _P, _P, _I, _I, _N, _N, _N, _P, _P, _P, _U64, _P]),
+    "muon_classifier_loss_grads": (_I, [_P, _P, _P, _P, _I, _I, _N, _N, _N, _P, _P, _P, _P, _P, _U64, _P]),
+    "muon_classifier_loss_backward": (_I, [_P, _P, _P, _P, _P, _I, _I, _N, _N, _N, _P, _P, _P, _U64, _P]),
+    "muon_distill_loss_workspace": (_I, [_I, _N, _N, _N, _I, _I, _U64P]),
+    "muon_distill_loss": (_I, [_P, _P, _P, _I, _P, _I, _I, _N, _N, _N, _I, _F, _P, _P, _P, _U64, _P]),
+    "muon_distill_loss_grads": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _N, _N, _N, _I, _F, _P, _P, _P, _P, _P, _U64,
+                                     _P]),
+    "muon_distill_loss_backward": (_I, [_P, _P, _P, _P, _I, _P, _P, _I, _I, _N, _N, _N, _I, _F, _P, _P, _P, _U64,
+                                        _P]),
 }
 
 _lib = None

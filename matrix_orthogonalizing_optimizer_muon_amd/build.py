@@ -44,8 +44,9 @@ def build(verbose: bool = False) -> str:
     with tempfile.TemporaryDirectory(prefix="muon_build_") as tmp:
         objs = []
         for src, kind in (("kernels.hip", "hip"), ("probe.hip", "hip"), ("noalloc.hip", "hip"),
-                          ("expert_rows.hip", "hip"), ("expert_products.hip", "hip"), ("abi.cpp", "hip"),
-                          ("plan.cpp", "host"), ("assign.cpp", "host")):
+                          ("expert_rows.hip", "hip"), ("expert_products.hip", "hip"),
+                          ("vocab_embed.hip", "hip"), ("vocab_loss.hip", "hip"), ("vocab_products.hip", "hip"),
+                          ("abi.cpp", "hip"), ("plan.cpp", "host"), ("assign.cpp", "host")):
             obj = os.path.join(tmp, src + ".o")
             path = os.path.join(CSRC, src)
             if kind == "hip":

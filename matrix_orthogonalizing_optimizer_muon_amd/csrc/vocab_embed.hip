@@ -1,0 +1,342 @@
+// The embedding of tokens and its gradient.
+//
+//   embed           out[t] = scale table[tokens[t]]
+//   embed_backward  dtable[v] = scale sum over the t with tokens[t] = v of dout[t]
+//
+// Both are bound by memory: rows of a table read or written once.  The gradient
+// has no atomics on values: the places of each token come sorted by token, then
+// place, and each table row is summed by one wave (rows of many places in parts
+// that are added in their order), so equal inputs give equal bits.
+#include <hip/hip_runtime.h>
+
+#include "vocab.hpp"
+
+namespace muon {
+namespace vo {
+namespace {
+
+constexpr int kCols = 512;   // columns of a wave: eight a lane
+
+// A wave has 512 columns of one token's row.
+template <class T, class I>
+__global__ __launch_bounds__(256) void k_embed(const I* __restrict__ tokens, const T* __restrict__ table, int64_t n,
+                                               int32_t vocab, int64_t dim, int32_t slabs, float scale,
+                                               T* __restrict__ out) {
+  const int64_t unit = block_index() * 4 + (threadIdx.x >> 6);
+  const int64_t t = unit / slabs;
+  if (t >= n) return;
+  const int64_t c = (unit - t * slabs) * kCols + (threadIdx.x & 63) * 8;
+  if (c >= dim) return;
+  const int cnt = dim - c < 8 ? (int)(dim - c) : 8;
+  const int32_t v = read_index(tokens, t, vocab);
+  float x[8] = {};
+  if (v >= 0) load8(table + (int64_t)v * dim + c, cnt, x);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = v >= 0 ? x[i] * scale : 0.f;
+  store8(out + t * dim + c, cnt, x);
+}
+
+// ------------------------------------------------------------ order of tokens
+
+// Places sorted by token, then place, in one launch without any exchange
+// between blocks: a block has `width` entries of the vocabulary, reads all
+// tokens, counts those below its entries (where its places start) and those of
+// each entry, and reads them again to write their places.  The tokens are cut
+// into a segment for each of the 16 waves; a count for each (entry, wave), added
+// up in that order, tells where a wave's places of an entry go, so each wave
+// goes through its own segment in order and alone.  250 blocks read 16384
+// tokens of 8 bytes from L2 in a few microseconds.
+// start: vocab + 1 first places of the entries; pos and key: places, their tokens.
+constexpr int kOrderThreads = 1024, kOrderWaves = 16, kOrderWidth = 512;
+
+template <class I>
+__global__ __launch_bounds__(kOrderThreads) void k_order(const I* __restrict__ tokens, int32_t n, int32_t vocab,
+                                                         int32_t width, int32_t* __restrict__ start,
+                                                         int32_t* __restrict__ pos, int32_t* __restrict__ key) {
+  __shared__ int32_t count[kOrderWidth * kOrderWaves];
+  __shared__ int32_t sums[kOrderWaves + 1];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int32_t lo = (int32_t)((int64_t)blockIdx.x * width);
+  const int32_t hi = vocab - lo < width ? vocab : lo + width;
+  const int32_t cells = width * kOrderWaves, per = cells / kOrderThreads;   // width: a multiple of 64
+  for (int i = tid; i < cells; i += kOrderThreads) count[i] = 0;
+  __syncthreads();
+  const int64_t segment = ((int64_t)n + kOrderThreads - 1) / kOrderThreads * 64;
+  const int64_t first = w * segment < n ? w * segment : n, last = first + segment < n ? first + segment : n;
+  int32_t below = 0;
+  for (int64_t i = first + lane; i < last; i += 256) {
+    int32_t v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = i + 64 * u < last ? read_index(tokens, i + 64 * u, vocab) : -1;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      below += v[u] >= 0 && v[u] < lo;
+      if (v[u] >= lo && v[u] < hi) atomicAdd(&count[(v[u] - lo) * kOrderWaves + w], 1);   // whole numbers: any order
+    }
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) below += __shfl_xor(below, o, 64);
+  if (lane == 0) sums[w] = below;
+  __syncthreads();
+  int32_t base = 0;
+  for (int i = 0; i < kOrderWaves; ++i) base += sums[i];
+  // exclusive sums over (entry, wave)
+  int32_t mine = 0;
+  for (int i = 0; i < per; ++i) mine += count[tid * per + i];
+  const int32_t upto = wave_scan_add(mine, lane);
+  __syncthreads();
+  if (lane == 63) sums[w] = upto;
+  __syncthreads();
+  int32_t run = base + upto - mine;
+  for (int i = 0; i < w; ++i) run += sums[i];
+  for (int i = 0; i < per; ++i) {
+    const int32_t c = count[tid * per + i];
+    count[tid * per + i] = run;
+    run += c;
+  }
+  __syncthreads();
+  for (int i = tid; i < hi - lo; i += kOrderThreads) start[lo + i] = count[i * kOrderWaves];
+  if (hi == vocab && tid == kOrderThreads - 1) start[vocab] = run;   // cells past vocab are empty
+  __syncthreads();
+  for (int64_t i = first; i < last; i += 256) {
+    int32_t v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      v[u] = i + 64 * u + lane < last ? read_index(tokens, i + 64 * u + lane, vocab) : -1;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const bool in = v[u] >= lo && v[u] < hi;
+      uint64_t left = __ballot(in);
+      while (left) {
+        const int at = __ffsll((unsigned long long)left) - 1;
+        const int32_t e = __builtin_amdgcn_readlane(v[u], at);
+        const uint64_t same = __ballot(in && v[u] == e);
+        const int32_t from = count[(e - lo) * kOrderWaves + w];
+        if (in && v[u] == e) {
+          const int32_t to = from + __popcll(same & ((uint64_t(1) << lane) - 1));
+          pos[to] = (int32_t)(i + 64 * u + lane);
+          key[to] = e;
+          if (lane == at) count[(e - lo) * kOrderWaves + w] = from + __popcll(same);
+        }
+        left &= ~same;
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------- gradient
+
+// Rows of up to kWindow places are summed by the wave that writes them.  The
+// sorted places are also cut into windows of kWindow; the places of a longer row
+// are summed window by window, at most two such rows meeting in one (the row of
+// its first place: part 0, and one that starts behind it: part 1), and the wave
+// of the window where the row starts adds these sums up in the next launch.
+constexpr int kWindow = 64;
+
+// Sum of dout's rows at `cnt` <= 64 places, held one a lane, in their order.
+template <class T>
+__device__ __forceinline__ void sum_rows(const T* __restrict__ dout, int64_t dim, int32_t place, int from, int to,
+                                         int64_t c, int cnt, float (&sum)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum[i] = 0.f;
+  int j = from;
+  for (; j + 4 <= to; j += 4) {
+    float x[4][8];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) load8(dout + (int64_t)__builtin_amdgcn_readlane(place, j + u) * dim + c, cnt, x[u]);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] += x[u][i];
+  }
+  for (; j < to; ++j) {
+    float x[8];
+    load8(dout + (int64_t)__builtin_amdgcn_readlane(place, j) * dim + c, cnt, x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i] += x[i];
+  }
+}
+
+template <class T>
+__global__ __launch_bounds__(256) void k_embed_grad(const T* __restrict__ dout, const int32_t* __restrict__ start,
+                                                    const int32_t* __restrict__ pos, const int32_t* __restrict__ key,
+                                                    int32_t n, int32_t vocab, int64_t dim, int32_t slabs, float scale,
+                                                    T* __restrict__ dtable, float* __restrict__ parts) {
+  const int lane = threadIdx.x & 63;
+  const int64_t windows = ((int64_t)n + kWindow - 1) / kWindow;
+  const int64_t unit = block_index() * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t item = unit / slabs;
+  const int64_t c = (unit - item * slabs) * kCols + lane * 8;
+  const int cnt = c >= dim ? 0 : dim - c < 8 ? (int)(dim - c) : 8;
+  float sum[8];
+  if (item >= windows) {   // a row
+    const int64_t v = item - windows;
+    if (v >= vocab) return;
+    const int32_t s = start[v], e = start[v + 1];
+    if (e - s > kWindow) return;
+    const int32_t place = lane < e - s ? pos[s + lane] : 0;
+    sum_rows(dout, dim, place, 0, e - s, c, cnt, sum);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i] *= scale;
+    if (cnt) store8(dtable + v * dim + c, cnt, sum);
+    return;
+  }
+  const int32_t total = start[vocab];
+  const int64_t begin = item * kWindow;
+  if (begin >= total) return;
+  const int here = total - begin < kWindow ? (int)(total - begin) : kWindow;
+  const int32_t place = lane < here ? pos[begin + lane] : 0;
+  const int32_t row = lane < here ? key[begin + lane] : 0;
+  const int32_t head = __builtin_amdgcn_readlane(row, 0), tail = __builtin_amdgcn_readlane(row, here - 1);
+  const int32_t head_end = start[head + 1], tail_start = start[tail];
+  if (head_end - start[head] > kWindow) {
+    const int to = head_end - begin < here ? (int)(head_end - begin) : here;
+    sum_rows(dout, dim, place, 0, to, c, cnt, sum);
+    if (cnt) store8(parts + item * 2 * dim + c, cnt, sum);
+  }
+  if (tail != head && start[tail + 1] - tail_start > kWindow) {
+    sum_rows(dout, dim, place, (int)(tail_start - begin), here, c, cnt, sum);
+    if (cnt) store8(parts + (item * 2 + 1) * dim + c, cnt, sum);
+  }
+}
+
+// The long rows, each by the waves of the window where it starts.
+template <class T>
+__global__ __launch_bounds__(256) void k_embed_join(const int32_t* __restrict__ start, const int32_t* __restrict__ key,
+                                                    int32_t n, int32_t vocab, int64_t dim, int32_t slabs, float scale,
+                                                    const float* __restrict__ parts, T* __restrict__ dtable) {
+  const int lane = threadIdx.x & 63;
+  const int64_t unit = block_index() * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t item = unit / slabs, begin = item * kWindow;
+  const int32_t total = start[vocab];
+  if (begin >= total) return;
+  const int here = total - begin < kWindow ? (int)(total - begin) : kWindow;
+  const int32_t v = key[begin + here - 1];   // a long row that starts here reaches the window's end
+  const int32_t s = start[v], e = start[v + 1];
+  if (e - s <= kWindow || s < begin) return;
+  const int64_t c = (unit - item * slabs) * kCols + lane * 8;
+  if (c >= dim) return;
+  const int cnt = dim - c < 8 ? (int)(dim - c) : 8;
+  float sum[8];
+  load8(parts + (item * 2 + (s > begin ? 1 : 0)) * dim + c, cnt, sum);
+  const int64_t upto = ((int64_t)e - 1) / kWindow;
+#pragma unroll 4
+  for (int64_t i = item + 1; i <= upto; ++i) {
+    float x[8];
+    load8(parts + i * 2 * dim + c, cnt, x);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) sum[u] += x[u];
+  }
+#pragma unroll
+  for (int u = 0; u < 8; ++u) sum[u] *= scale;
+  store8(dtable + (int64_t)v * dim + c, cnt, sum);
+}
+
+// ----------------------------------------------------------------------- host
+
+int64_t blocks_of(int64_t items, int64_t slabs) { return ceil_div(items * slabs, 4); }
+
+struct GradSpace {
+  uint64_t start, pos, key, parts, bytes;
+};
+GradSpace grad_space(int64_t tokens, int64_t vocab, int64_t dim) {
+  Pieces p;
+  GradSpace g;
+  g.start = p.take((uint64_t)(vocab + 1) * 4);
+  g.pos = p.take((uint64_t)tokens * 4);
+  g.key = p.take((uint64_t)tokens * 4);
+  g.parts = p.take(tokens > kWindow ? (uint64_t)ceil_div(tokens, kWindow) * 2 * dim * 4 : 0);
+  g.bytes = p.used;
+  return g;
+}
+
+template <class T, class I>
+void launch_embed(const void* tokens, const void* table, int64_t n, int64_t vocab, int64_t dim, float scale, void* out,
+                  hipStream_t s) {
+  const int64_t slabs = ceil_div(dim, kCols);
+  hipLaunchKernelGGL((k_embed<T, I>), grid_of_blocks(blocks_of(n, slabs), 256), dim3(256), 0, s,
+                     static_cast<const I*>(tokens), static_cast<const T*>(table), n, (int32_t)vocab, dim,
+                     (int32_t)slabs, scale, static_cast<T*>(out));
+}
+
+template <class T>
+int launch_grad(const void* dout, const int32_t* start, const int32_t* pos, const int32_t* key, int64_t n,
+                int64_t vocab, int64_t dim, float scale, float* parts, void* dtable, hipStream_t s) {
+  const int64_t slabs = ceil_div(dim, kCols), windows = n > kWindow ? ceil_div(n, kWindow) : 0;
+  // without windows no row is long
+  hipLaunchKernelGGL((k_embed_grad<T>), grid_of_blocks(blocks_of(windows + vocab, slabs), 256), dim3(256), 0, s,
+                     static_cast<const T*>(dout), start, pos, key, (int32_t)(windows ? n : 0), (int32_t)vocab, dim,
+                     (int32_t)slabs, scale, static_cast<T*>(dtable), parts);
+  if (windows)
+    hipLaunchKernelGGL((k_embed_join<T>), grid_of_blocks(blocks_of(windows, slabs), 256), dim3(256), 0, s, start, key,
+                       (int32_t)n, (int32_t)vocab, dim, (int32_t)slabs, scale, parts, static_cast<T*>(dtable));
+  return launch_status("embedding gradient launch");
+}
+
+}  // namespace
+}  // namespace vo
+}  // namespace muon
+
+using namespace muon::vo;
+
+extern "C" {
+
+int muon_embed(const void* tokens, int index_bytes, const void* table, int dtype, int64_t n, int64_t vocab, int64_t dim,
+               float scale, void* out, void* stream) {
+  muon::report_error(MUON_OK, "");
+  int rc;
+  if ((rc = check_sizes(dtype, index_bytes, n, vocab, dim))) return rc;
+  if (n == 0) return MUON_OK;
+  if (!tokens || !table || !out) return fail(MUON_EINVAL, "NULL pointer");
+  if ((rc = check_device())) return rc;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (dtype == MUON_BF16) {
+    if (index_bytes == 8) launch_embed<bf16_t, int64_t>(tokens, table, n, vocab, dim, scale, out, s);
+    else launch_embed<bf16_t, int32_t>(tokens, table, n, vocab, dim, scale, out, s);
+  } else {
+    if (index_bytes == 8) launch_embed<float, int64_t>(tokens, table, n, vocab, dim, scale, out, s);
+    else launch_embed<float, int32_t>(tokens, table, n, vocab, dim, scale, out, s);
+  }
+  return launch_status("embedding launch");
+}
+
+int muon_embed_backward_workspace(int64_t n, int64_t vocab, int64_t dim, uint64_t* bytes) {
+  muon::report_error(MUON_OK, "");
+  if (!bytes) return fail(MUON_EINVAL, "NULL bytes");
+  const int rc = check_sizes(MUON_F32, 4, n, vocab, dim);
+  if (rc) return rc;
+  *bytes = grad_space(n, vocab, dim).bytes;
+  return MUON_OK;
+}
+
+int muon_embed_backward(const void* dout, const void* tokens, int index_bytes, int dtype, int64_t n, int64_t vocab,
+                        int64_t dim, float scale, void* dtable, void* workspace, uint64_t workspace_bytes,
+                        void* stream) {
+  muon::report_error(MUON_OK, "");
+  int rc;
+  if ((rc = check_sizes(dtype, index_bytes, n, vocab, dim))) return rc;
+  if (!dtable || (n > 0 && (!dout || !tokens))) return fail(MUON_EINVAL, "NULL pointer");
+  const GradSpace g = grad_space(n, vocab, dim);
+  if ((rc = check_workspace(workspace, workspace_bytes, g.bytes))) return rc;
+  if ((rc = check_device())) return rc;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  int32_t* start = reinterpret_cast<int32_t*>(ws + g.start);
+  int32_t* pos = reinterpret_cast<int32_t*>(ws + g.pos);
+  int32_t* key = reinterpret_cast<int32_t*>(ws + g.key);
+  int64_t width = ceil_div(ceil_div(vocab, 256), 64) * 64;
+  if (width > kOrderWidth) width = kOrderWidth;
+  const dim3 grid((uint32_t)ceil_div(vocab, width));
+  if (index_bytes == 8)
+    hipLaunchKernelGGL((k_order<int64_t>), grid, dim3(kOrderThreads), 0, s, static_cast<const int64_t*>(tokens),
+                       (int32_t)n, (int32_t)vocab, (int32_t)width, start, pos, key);
+  else
+    hipLaunchKernelGGL((k_order<int32_t>), grid, dim3(kOrderThreads), 0, s, static_cast<const int32_t*>(tokens),
+                       (int32_t)n, (int32_t)vocab, (int32_t)width, start, pos, key);
+  if ((rc = launch_status("token order launch"))) return rc;
+  float* parts = reinterpret_cast<float*>(ws + g.parts);
+  if (dtype == MUON_BF16) return launch_grad<bf16_t>(dout, start, pos, key, n, vocab, dim, scale, parts, dtable, s);
+  return launch_grad<float>(dout, start, pos, key, n, vocab, dim, scale, parts, dtable, s);
+}
+
+}  // extern "C"

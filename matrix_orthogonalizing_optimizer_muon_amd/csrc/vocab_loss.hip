@@ -1,0 +1,653 @@
+// The classifier's losses over a vocabulary without the logits in memory: cross
+// entropy against one target a row, and distillation from a teacher's k largest
+// logits, with the gradients of x and w.
+//
+//   l = x w^T;  lse = log sum_v exp(l_v / tau);  q: a row's target distribution
+//   loss = tau^2 (sum_j q_j log q_j + sum_j q_j (lse - l_{id_j} / tau))
+//   dl_v = g tau (exp(l_v / tau - lse) - sum_{j: id_j = v} q_j)
+//   dx = dl w;  dw = dl^T x
+//
+// Cross entropy is k = 1, q = 1, tau = 1.  Around the products
+// (vocab_products.hip) the kernels here find the rows that count and their
+// targets, take the targets' logits as dot products of their own in fp32, join
+// the slabs' sums, and put the targets' part into dl: its entries there are
+// written from the fp32 logits, so that exp(..) - q loses nothing to the
+// rounding of dl before the difference.
+//
+// dl is the products' operand and so in the type of x: bf16 rounds each entry by
+// 2^-9 at the most of what it is, as it would a logits gradient in memory.  With
+// the loss in the same pass an entry is rounded twice (exp of the logit less the
+// largest of its slab before its row's sum is known, the gradient after).
+#include <hip/hip_runtime.h>
+
+#include "vocab_loss.hpp"
+
+namespace muon {
+namespace vo {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// ---------------------------------------------------------------------- rows
+
+// A teacher's entries of a row: ids, or -1 where there is none (an id outside the
+// vocabulary, a logit of -inf or NaN), and the softmax of their logits over tau;
+// term: sum q log q.  A wave a row, entry lane + 64 i.
+template <class TT, class I>
+__global__ __launch_bounds__(256) void k_teacher(const TT* __restrict__ teacher, const I* __restrict__ ids,
+                                                 int64_t tokens, int32_t k, int32_t vocab, float inv_tau,
+                                                 int32_t* __restrict__ id, float* __restrict__ q,
+                                                 float* __restrict__ term) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = block_index() * 4 + (threadIdx.x >> 6);
+  if (t >= tokens) return;
+  constexpr int N = kMaxTeacher / 64;
+  float v[N];
+  int32_t at[N];
+  float top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int j = lane + 64 * i;
+    at[i] = -1;
+    v[i] = -INFINITY;
+    if (j < k) {
+      at[i] = read_index(ids, t * k + j, vocab);
+      const float l = to_f32(teacher[t * k + j]);
+      if (!(l > -INFINITY)) at[i] = -1;
+      if (at[i] >= 0) v[i] = fminf(l, 3.402823466e38f);
+    }
+    top = fmaxf(top, v[i]);
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+  float total = 0.f, e[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    v[i] = at[i] >= 0 ? (v[i] - top) * inv_tau : 0.f;
+    e[i] = at[i] >= 0 ? expf(v[i]) : 0.f;
+    total += e[i];
+  }
+  total = wave_sum(total);
+  const float log_total = total > 0.f ? logf(total) : 0.f;
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int j = lane + 64 * i;
+    const float p = at[i] >= 0 ? e[i] / total : 0.f;
+    if (p > 0.f) sum += p * (v[i] - log_total);
+    if (j < k) {
+      id[t * k + j] = at[i];
+      q[t * k + j] = p;
+    }
+  }
+  sum = wave_sum(sum);
+  if (lane == 0) term[t] = total > 0.f ? sum : NAN;   // NaN: no entry
+}
+
+// The live rows in their order, in one block: each wave has a segment, counts it,
+// and writes it behind those before.  TEACHER: term tells them; else targets, whose
+// ids are written too.  Rows that do not count get loss and lse 0; slot: -1.
+constexpr int kLiveThreads = 1024;
+template <class I, bool TEACHER>
+__global__ __launch_bounds__(kLiveThreads) void k_live(const I* __restrict__ targets, const float* __restrict__ term,
+                                                       int32_t tokens, int32_t vocab, int32_t* __restrict__ id,
+                                                       int32_t* __restrict__ rows, int32_t* __restrict__ slot,
+                                                       int32_t* __restrict__ count, float* __restrict__ loss,
+                                                       float* __restrict__ lse) {
+  __shared__ int32_t sums[16];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t segment = ((int64_t)tokens + kLiveThreads - 1) / kLiveThreads * 64;
+  const int64_t first = w * segment < tokens ? w * segment : tokens;
+  const int64_t last = first + segment < tokens ? first + segment : tokens;
+  int32_t mine = 0;
+  for (int64_t i = first; i < last; i += 256) {
+    bool in[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int64_t t = i + 64 * u + lane;
+      in[u] = t < last && (TEACHER ? term[t] <= INFINITY : read_index(targets, t, vocab) >= 0);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) mine += __popcll(__ballot(in[u]));
+  }
+  if (lane == 0) sums[w] = mine;
+  __syncthreads();
+  int32_t at = 0, all = 0;
+  for (int i = 0; i < 16; ++i) {
+    at += i < w ? sums[i] : 0;
+    all += sums[i];
+  }
+  if (threadIdx.x == 0) *count = all;
+  for (int64_t i = first; i < last; i += 64) {
+    const int64_t t = i + lane;
+    int32_t v = -1;
+    if (t < last) v = TEACHER ? (term[t] <= INFINITY ? 0 : -1) : read_index(targets, t, vocab);
+    const uint64_t in = __ballot(v >= 0);
+    if (t < last) {
+      const int32_t to = at + __popcll(in & ((uint64_t(1) << lane) - 1));
+      if (!TEACHER) id[t] = v;
+      slot[t] = v >= 0 ? to : -1;
+      if (v >= 0) rows[to] = (int32_t)t;
+      else if (loss) loss[t] = lse[t] = 0.f;
+    }
+    at += __popcll(in);
+  }
+}
+
+// Zero rows of dx where a row does not count: a wave has 512 columns of one.
+template <class T>
+__global__ __launch_bounds__(256) void k_dead_rows(const int32_t* __restrict__ slot, int64_t tokens, int64_t dim,
+                                                   int32_t slabs, T* __restrict__ dx) {
+  const int64_t unit = block_index() * 4 + (threadIdx.x >> 6);
+  const int64_t t = unit / slabs;
+  if (t >= tokens || slot[t] >= 0) return;
+  const int64_t c = (unit - t * slabs) * 512 + (threadIdx.x & 63) * 8;
+  if (c >= dim) return;
+  const float zero[8] = {};
+  store8(dx + t * dim + c, dim - c < 8 ? (int)(dim - c) : 8, zero);
+}
+
+// ------------------------------------------------------------------- targets
+
+// The logits of a chunk's targets: a wave has one, picked[slot][j] = <x, w_id>.
+template <class T>
+__global__ __launch_bounds__(256) void k_picked(LossArgs a, const int32_t* __restrict__ id, int32_t k,
+                                                float* __restrict__ picked) {
+  const int lane = threadIdx.x & 63;
+  const int64_t unit = block_index() * 4 + (threadIdx.x >> 6);
+  const int64_t s = unit / k;
+  const int32_t j = (int32_t)(unit - s * k);
+  if (s >= live_slots(a.ch)) return;
+  const int64_t t = a.ch.rows[a.ch.slot0 + s];
+  const int32_t v = id[t * k + j];
+  if (v < 0) return;
+  const T* x = static_cast<const T*>(a.x) + t * a.dim;
+  const T* w = static_cast<const T*>(a.w) + (int64_t)v * a.dim;
+  float sum = 0.f;
+  for (int32_t c = lane * 8; c < a.dim; c += 512) {
+    const int cnt = a.dim - c < 8 ? a.dim - c : 8;
+    float p[8], q[8];
+    load8(x + c, cnt, p);
+    load8(w + c, cnt, q);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += p[i] * q[i];
+  }
+  sum = wave_sum(sum);
+  if (lane == 0) picked[unit] = sum;
+}
+
+struct JoinArgs {
+  const int32_t* id;       // tokens x k
+  const float* q;          // tokens x k, or null: 1
+  const float* term;       // tokens, or null: 0
+  const float* picked;     // [chunk][k]
+  const float* dloss;      // tokens, or null
+  float* base;             // [chunk], these three: LossArgs; null without gradients
+  float* scale;
+  float* g;
+  float* loss;             // tokens, or null
+  float* lse;              // tokens: written with loss, else read
+  int32_t k, slabs;
+  float tau;
+};
+
+// A row's sum over its slabs, and its loss.  A block has RB slots and 256 / RB
+// groups that go through the slabs side by side.
+template <int RB>
+__global__ __launch_bounds__(256) void k_join(LossArgs a, JoinArgs j) {
+  constexpr int GROUPS = 256 / RB;
+  __shared__ float tops[GROUPS][RB], sums[GROUPS][RB];
+  const int r = threadIdx.x % RB, grp = threadIdx.x / RB;
+  const int64_t s = (int64_t)blockIdx.x * RB + r;
+  const bool exists = s < live_slots(a.ch);
+  float top = -INFINITY, sum = 0.f;
+  if (exists) {
+    for (int32_t i = grp; i < j.slabs; i += GROUPS) {
+      const float* p = a.stats + 2 * ((int64_t)i * a.ch.size + s);
+      const float m = p[0], v = p[1], to = fmaxf(top, m);
+      const float base = to == -INFINITY ? 0.f : to;
+      sum = sum * __builtin_amdgcn_exp2f((top - base) * a.to_log2) + v * __builtin_amdgcn_exp2f((m - base) * a.to_log2);
+      top = to;
+    }
+  }
+  tops[grp][r] = top;
+  sums[grp][r] = sum;
+  __syncthreads();
+  if (grp || !exists) return;
+  top = -INFINITY;
+  for (int i = 0; i < GROUPS; ++i) top = fmaxf(top, tops[i][r]);
+  const float base = top == -INFINITY ? 0.f : top;
+  sum = 0.f;
+  for (int i = 0; i < GROUPS; ++i) sum += sums[i][r] * __builtin_amdgcn_exp2f((tops[i][r] - base) * a.to_log2);
+  const int64_t t = a.ch.rows[a.ch.slot0 + s];
+  const float log_sum = logf(sum);
+  float off = 0.f;
+  for (int32_t i = 0; i < j.k; ++i)
+    if (j.id[t * j.k + i] >= 0)
+      off += (j.q ? j.q[t * j.k + i] : 1.f) * ((base - j.picked[s * j.k + i]) * a.inv_tau + log_sum);
+  j.loss[t] = j.tau * j.tau * ((j.term ? j.term[t] : 0.f) + off);
+  j.lse[t] = base * a.inv_tau + log_sum;
+  if (j.g) {
+    j.base[s] = base;
+    j.scale[s] = 1.f / sum;
+    j.g[s] = j.dloss[t] * j.tau;
+  }
+}
+
+// The same by slot where lse is given.
+__global__ __launch_bounds__(256) void k_given(LossArgs a, JoinArgs j) {
+  const int64_t s = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (s >= live_slots(a.ch)) return;
+  const int64_t t = a.ch.rows[a.ch.slot0 + s];
+  j.base[s] = j.lse[t];
+  j.scale[s] = 1.f;
+  j.g[s] = j.dloss[t] * j.tau;
+}
+
+__device__ __forceinline__ void load_exps(const bf16_t* p, int cnt, float (&v)[8]) {
+  u32x4 t = {0u, 0u, 0u, 0u};
+  if (cnt >= 8) {
+    t = *reinterpret_cast<const u32x4_any*>(p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < cnt) t[i / 2] |= (uint32_t)p[i].bits << (16 * (i % 2));
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) unpack_exps(t[i], v[2 * i], v[2 * i + 1]);
+}
+__device__ __forceinline__ void load_exps(const float* p, int cnt, float (&v)[8]) { load8(p, cnt, v); }
+
+// exp((logit - largest of its slab) / tau) into gradients, in place: a wave has
+// 512 columns of a slot.
+template <class T>
+__global__ __launch_bounds__(256) void k_rescale(LossArgs a, int32_t units) {
+  const int64_t unit = block_index() * 4 + (threadIdx.x >> 6);
+  const int64_t s = unit / units;
+  if (s >= live_slots(a.ch)) return;
+  const int64_t c = (unit - s * units) * 512 + (threadIdx.x & 63) * 8;
+  if (c >= a.vocab) return;
+  const int cnt = a.vocab - c < 8 ? (int)(a.vocab - c) : 8;
+  const float top = a.stats[2 * (c / Slab<T>::kCols * a.ch.size + s)];
+  const float by = __builtin_amdgcn_exp2f((top - a.base[s]) * a.to_log2) * (a.scale[s] * a.g[s]);
+  T* p = static_cast<T*>(a.dl) + s * a.vocab + c;
+  float v[8];
+  load_exps(p, cnt, v);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] *= by;
+  store8(p, cnt, v);
+}
+
+// The targets' entries of dl, a wave a slot.  An id that comes more than once
+// counts with the sum of its weights, which each of them writes.
+template <class T>
+__global__ __launch_bounds__(256) void k_targets(LossArgs a, JoinArgs j) {
+  const int lane = threadIdx.x & 63;
+  const int64_t s = block_index() * 4 + (threadIdx.x >> 6);
+  if (s >= live_slots(a.ch)) return;
+  const int64_t t = a.ch.rows[a.ch.slot0 + s];
+  const float base = a.base[s], scale = a.scale[s], g = a.g[s];
+  T* dl = static_cast<T*>(a.dl) + s * a.vocab;
+  for (int32_t j0 = 0; j0 < j.k; j0 += 64) {
+    const int32_t at = j0 + lane;
+    const int32_t v = at < j.k ? j.id[t * j.k + at] : -1;
+    float q = 0.f;
+    for (int32_t i0 = 0; i0 < j.k; i0 += 64) {
+      const int32_t o = i0 + lane;
+      const int32_t id = o < j.k ? j.id[t * j.k + o] : -1;
+      const float weight = o < j.k ? (j.q ? j.q[t * j.k + o] : 1.f) : 0.f;
+      const int n = j.k - i0 < 64 ? j.k - i0 : 64;
+      for (int i = 0; i < n; ++i) {
+        const int32_t other = __builtin_amdgcn_readlane(id, i);
+        const float add = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(weight), i));
+        q += other == v ? add : 0.f;
+      }
+    }
+    if (v >= 0) store1(dl + v, (probability(a, j.picked[s * j.k + at], base, scale) - q) * g);
+  }
+}
+
+// ----------------------------------------------------------------------- host
+
+struct Call {
+  const void* x;
+  const void* w;
+  int dtype;
+  int64_t tokens, vocab, dim;
+  const void* targets;     // tokens x k
+  int index_bytes;
+  const void* teacher;     // tokens x k, or null: targets alone
+  int teacher_dtype, k;
+  float tau;
+  const float* dloss;
+  const float* lse_in;     // or null: the losses come with them
+  float* loss;
+  float* lse;
+  void* dx;
+  void* dw;                // or null: no gradients
+};
+
+// Slots of a chunk: as many as keep dl within 2 GiB and the slabs' sums within
+// 256 MiB (whole batches of most models; a chunk more costs another pass over the
+// sums of dw, 8 bytes an element of w).
+int64_t chunk_slots(int dtype, int64_t tokens, int64_t vocab, bool grads, bool stats) {
+  int64_t most = tokens;
+  auto cap = [&](int64_t bytes, int64_t each) {
+    int64_t n = bytes / each / 64 * 64;
+    if (n < 64) n = 64;
+    if (n < most) most = n;
+  };
+  if (grads) cap(int64_t(1) << 31, vocab * (dtype == MUON_BF16 ? 2 : 4));
+  if (stats) cap(int64_t(1) << 28, ceil_div(vocab, slab_cols(dtype)) * 8);
+  return most < 1 ? 1 : most;
+}
+
+struct LossSpace {
+  int64_t chunk, slabs;
+  uint64_t id, q, term, rows, slot, count, stats, picked, base, scale, g, dl, sums, bytes;
+};
+LossSpace loss_space(int dtype, int64_t tokens, int64_t vocab, int64_t dim, int k, bool teacher, bool grads,
+                     bool given) {
+  Pieces p;
+  LossSpace l;
+  const int64_t es = dtype == MUON_BF16 ? 2 : 4;
+  l.chunk = chunk_slots(dtype, tokens, vocab, grads, !given);
+  l.slabs = ceil_div(vocab, slab_cols(dtype));
+  l.id = p.take((uint64_t)tokens * k * 4);
+  l.q = p.take(teacher ? (uint64_t)tokens * k * 4 : 0);
+  l.term = p.take(teacher ? (uint64_t)tokens * 4 : 0);
+  l.rows = p.take((uint64_t)tokens * 4);
+  l.slot = p.take((uint64_t)tokens * 4);
+  l.count = p.take(4);
+  l.stats = p.take(given ? 0 : (uint64_t)l.slabs * l.chunk * 8);
+  l.picked = p.take((uint64_t)l.chunk * k * 4);
+  l.base = p.take((uint64_t)l.chunk * 4);
+  l.scale = p.take((uint64_t)l.chunk * 4);
+  l.g = p.take((uint64_t)l.chunk * 4);
+  l.dl = p.take(grads ? (uint64_t)l.chunk * vocab * es : 0);
+  l.sums = p.take(grads && l.chunk < tokens ? (uint64_t)vocab * dim * 4 : 0);
+  l.bytes = p.used;
+  return l;
+}
+
+template <class I>
+int find_rows(const Call& c, const LossSpace& l, char* ws, hipStream_t s) {
+  int32_t* id = reinterpret_cast<int32_t*>(ws + l.id);
+  float* q = reinterpret_cast<float*>(ws + l.q);
+  float* term = reinterpret_cast<float*>(ws + l.term);
+  int32_t* rows = reinterpret_cast<int32_t*>(ws + l.rows);
+  int32_t* slot = reinterpret_cast<int32_t*>(ws + l.slot);
+  int32_t* count = reinterpret_cast<int32_t*>(ws + l.count);
+  const I* ids = static_cast<const I*>(c.targets);
+  if (c.teacher && c.tokens) {
+    const dim3 grid = grid_of_blocks(ceil_div(c.tokens, 4), 256);
+    if (c.teacher_dtype == MUON_BF16)
+      hipLaunchKernelGGL((k_teacher<bf16_t, I>), grid, dim3(256), 0, s, static_cast<const bf16_t*>(c.teacher), ids,
+                         c.tokens, c.k, (int32_t)c.vocab, 1.f / c.tau, id, q, term);
+    else
+      hipLaunchKernelGGL((k_teacher<float, I>), grid, dim3(256), 0, s, static_cast<const float*>(c.teacher), ids,
+                         c.tokens, c.k, (int32_t)c.vocab, 1.f / c.tau, id, q, term);
+    hipLaunchKernelGGL((k_live<I, true>), dim3(1), dim3(kLiveThreads), 0, s, ids, term, (int32_t)c.tokens,
+                       (int32_t)c.vocab, id, rows, slot, count, c.loss, c.lse);
+  } else {
+    hipLaunchKernelGGL((k_live<I, false>), dim3(1), dim3(kLiveThreads), 0, s, ids, term, (int32_t)c.tokens,
+                       (int32_t)c.vocab, id, rows, slot, count, c.loss, c.lse);
+  }
+  return launch_status("target launch");
+}
+
+template <class T>
+int run(const Call& c, const LossSpace& l, char* ws, hipStream_t s) {
+  const bool grads = c.dw != nullptr, given = c.lse_in != nullptr;
+  int rc;
+  if ((rc = c.index_bytes == 8 ? find_rows<int64_t>(c, l, ws, s) : find_rows<int32_t>(c, l, ws, s))) return rc;
+  if (grads && c.tokens) {
+    const int64_t slabs = ceil_div(c.dim, 512);
+    hipLaunchKernelGGL((k_dead_rows<T>), grid_of_blocks(ceil_div(c.tokens * slabs, 4), 256), dim3(256), 0, s,
+                       reinterpret_cast<int32_t*>(ws + l.slot), c.tokens, c.dim, (int32_t)slabs,
+                       static_cast<T*>(c.dx));
+  }
+  LossArgs a = {};
+  a.ch.rows = reinterpret_cast<int32_t*>(ws + l.rows);
+  a.ch.count = reinterpret_cast<int32_t*>(ws + l.count);
+  a.ch.size = (int32_t)l.chunk;
+  a.x = c.x;
+  a.w = c.w;
+  a.tokens = c.tokens;
+  a.vocab = (int32_t)c.vocab;
+  a.dim = (int32_t)c.dim;
+  a.inv_tau = 1.f / c.tau;
+  a.to_log2 = kLog2e / c.tau;
+  a.stats = given ? nullptr : reinterpret_cast<float*>(ws + l.stats);
+  a.base = reinterpret_cast<float*>(ws + l.base);
+  a.scale = reinterpret_cast<float*>(ws + l.scale);
+  a.given = given;
+  a.g = reinterpret_cast<float*>(ws + l.g);
+  a.dl = grads ? ws + l.dl : nullptr;
+  a.dx = c.dx;
+  a.dw = c.dw;
+  a.sums = reinterpret_cast<float*>(ws + l.sums);
+  JoinArgs j = {};
+  j.id = reinterpret_cast<int32_t*>(ws + l.id);
+  j.q = c.teacher ? reinterpret_cast<float*>(ws + l.q) : nullptr;
+  j.term = c.teacher ? reinterpret_cast<float*>(ws + l.term) : nullptr;
+  j.picked = reinterpret_cast<float*>(ws + l.picked);
+  j.dloss = c.dloss;
+  j.base = reinterpret_cast<float*>(ws + l.base);
+  j.scale = reinterpret_cast<float*>(ws + l.scale);
+  j.g = grads ? reinterpret_cast<float*>(ws + l.g) : nullptr;
+  j.loss = c.loss;
+  j.lse = given ? const_cast<float*>(c.lse_in) : c.lse;
+  j.k = c.k;
+  j.slabs = (int32_t)l.slabs;
+  j.tau = c.tau;
+  if (!c.tokens) {   // no rows: dw is zeros
+    a.first = a.last = true;
+    return grads ? dw_product(a, c.dtype, s) : MUON_OK;
+  }
+  const int64_t chunks = ceil_div(c.tokens, l.chunk);
+  for (int64_t i = 0; i < chunks; ++i) {
+    a.ch.slot0 = i * l.chunk;
+    a.first = i == 0;
+    a.last = i + 1 == chunks;
+    const int64_t slots = l.chunk;
+    hipLaunchKernelGGL((k_picked<T>), grid_of_blocks(ceil_div(slots * c.k, 4), 256), dim3(256), 0, s, a, j.id, c.k,
+                       reinterpret_cast<float*>(ws + l.picked));
+    if (given) {
+      hipLaunchKernelGGL(k_given, dim3((uint32_t)ceil_div(slots, 256)), dim3(256), 0, s, a, j);
+      if ((rc = logits_product(a, c.dtype, kGradient, s))) return rc;
+    } else {
+      if ((rc = logits_product(a, c.dtype, grads ? kStatsExp : kStats, s))) return rc;
+      if (slots <= 4) hipLaunchKernelGGL((k_join<1>), dim3((uint32_t)slots), dim3(256), 0, s, a, j);
+      else hipLaunchKernelGGL((k_join<32>), dim3((uint32_t)ceil_div(slots, 32)), dim3(256), 0, s, a, j);
+      if (grads) {
+        const int64_t units = ceil_div(c.vocab, 512);
+        hipLaunchKernelGGL((k_rescale<T>), grid_of_blocks(ceil_div(slots * units, 4), 256), dim3(256), 0, s, a,
+                           (int32_t)units);
+      }
+    }
+    if ((rc = launch_status("classifier loss launch"))) return rc;
+    if (!grads) continue;
+    hipLaunchKernelGGL((k_targets<T>), grid_of_blocks(ceil_div(slots, 4), 256), dim3(256), 0, s, a, j);
+    if ((rc = dx_product(a, c.dtype, s)) || (rc = dw_product(a, c.dtype, s))) return rc;
+  }
+  return launch_status("classifier loss launch");
+}
+
+int check_loss(const Call& c) {
+  const int rc = check_sizes(c.dtype, c.index_bytes, c.tokens, c.vocab, c.dim);
+  if (rc) return rc;
+  if (c.teacher_dtype >= 0) {
+    if (!good_dtype(c.teacher_dtype)) return fail(MUON_EUNSUPPORTED, "unsupported teacher dtype");
+    if (c.k < 1) return fail(MUON_EINVAL, "k must be >= 1");
+    if (c.k > kMaxTeacher) return fail(MUON_EUNSUPPORTED, "more than 256 teacher entries");
+    if (c.tokens * c.k > kMaxCount) return fail(MUON_EUNSUPPORTED, "2^31 teacher entries or more");
+    if (!(c.tau > 0.f && c.tau < INFINITY)) return fail(MUON_EINVAL, "temperature must be positive and finite");
+  }
+  return MUON_OK;
+}
+
+int loss_bytes(int dtype, int64_t tokens, int64_t vocab, int64_t dim, int k, int gradients, uint64_t* bytes) {
+  muon::report_error(MUON_OK, "");
+  if (!bytes) return fail(MUON_EINVAL, "NULL bytes");
+  Call c = {};
+  c.dtype = dtype;
+  c.index_bytes = 4;
+  c.tokens = tokens;
+  c.vocab = vocab;
+  c.dim = dim;
+  c.k = k ? k : 1;
+  c.teacher_dtype = k ? MUON_F32 : -1;
+  c.tau = 1.f;
+  const int rc = check_loss(c);
+  if (rc) return rc;
+  if (gradients < 0 || gradients > 2) return fail(MUON_EINVAL, "gradients must be 0, 1 or 2");
+  *bytes = loss_space(dtype, tokens, vocab, dim, c.k, k != 0, gradients != 0, gradients == 2).bytes;
+  return MUON_OK;
+}
+
+int launch_loss(const Call& c, void* workspace, uint64_t workspace_bytes, void* stream) {
+  int rc;
+  const bool teacher = c.teacher_dtype >= 0, grads = c.dw != nullptr;
+  const LossSpace l = loss_space(c.dtype, c.tokens, c.vocab, c.dim, c.k, teacher, grads, c.lse_in != nullptr);
+  if ((rc = check_workspace(workspace, workspace_bytes, l.bytes))) return rc;
+  if ((rc = check_device())) return rc;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  return c.dtype == MUON_BF16 ? run<bf16_t>(c, l, ws, s) : run<float>(c, l, ws, s);
+}
+
+}  // namespace
+}  // namespace vo
+}  // namespace muon
+
+using namespace muon::vo;
+
+namespace {
+
+Call targets_call(const void* x, const void* w, const void* targets, int index_bytes, int dtype, int64_t tokens,
+                  int64_t vocab, int64_t dim) {
+  Call c = {};
+  c.x = x;
+  c.w = w;
+  c.dtype = dtype;
+  c.tokens = tokens;
+  c.vocab = vocab;
+  c.dim = dim;
+  c.targets = targets;
+  c.index_bytes = index_bytes;
+  c.teacher_dtype = -1;
+  c.k = 1;
+  c.tau = 1.f;
+  return c;
+}
+
+Call teacher_call(const void* x, const void* w, const void* teacher, int teacher_dtype, const void* ids,
+                  int index_bytes, int dtype, int64_t tokens, int64_t vocab, int64_t dim, int k, float temperature) {
+  Call c = targets_call(x, w, ids, index_bytes, dtype, tokens, vocab, dim);
+  c.teacher = teacher;
+  c.teacher_dtype = teacher_dtype < 0 ? 1 << 20 : teacher_dtype;   // negative: no dtype either
+  c.k = k;
+  c.tau = temperature;
+  return c;
+}
+
+bool inputs(const Call& c) { return c.x && c.w && c.targets && (c.teacher_dtype < 0 || c.teacher); }
+
+int forward(Call c, float* loss, float* lse, void* workspace, uint64_t workspace_bytes, void* stream) {
+  const int rc = check_loss(c);
+  if (rc || c.tokens == 0) return rc;
+  if (!inputs(c) || !loss || !lse) return fail(MUON_EINVAL, "NULL pointer");
+  c.loss = loss;
+  c.lse = lse;
+  return launch_loss(c, workspace, workspace_bytes, stream);
+}
+
+int with_gradients(Call c, const float* dloss, float* loss, float* lse, const float* lse_in, void* dx, void* dw,
+                   void* workspace, uint64_t workspace_bytes, void* stream) {
+  const int rc = check_loss(c);
+  if (rc) return rc;
+  if (!dw || (c.tokens > 0 && (!inputs(c) || !dloss || !dx || (lse_in ? false : !loss || !lse))))
+    return fail(MUON_EINVAL, "NULL pointer");
+  c.dloss = dloss;
+  c.loss = loss;
+  c.lse = lse;
+  c.lse_in = lse_in;
+  c.dx = dx;
+  c.dw = dw;
+  return launch_loss(c, workspace, workspace_bytes, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+int muon_classifier_loss_workspace(int dtype, int64_t tokens, int64_t vocab, int64_t dim, int gradients,
+                                   uint64_t* bytes) {
+  return loss_bytes(dtype, tokens, vocab, dim, 0, gradients, bytes);
+}
+
+int muon_classifier_loss(const void* x, const void* w, const void* targets, int index_bytes, int dtype, int64_t tokens,
+                         int64_t vocab, int64_t dim, float* loss, float* lse, void* workspace,
+                         uint64_t workspace_bytes, void* stream) {
+  muon::report_error(MUON_OK, "");
+  return forward(targets_call(x, w, targets, index_bytes, dtype, tokens, vocab, dim), loss, lse, workspace,
+                 workspace_bytes, stream);
+}
+
+int muon_classifier_loss_grads(const float* dloss, const void* x, const void* w, const void* targets, int index_bytes,
+                               int dtype, int64_t tokens, int64_t vocab, int64_t dim, float* loss, float* lse,
+                               void* dx, void* dw, void* workspace, uint64_t workspace_bytes, void* stream) {
+  muon::report_error(MUON_OK, "");
+  return with_gradients(targets_call(x, w, targets, index_bytes, dtype, tokens, vocab, dim), dloss, loss, lse, nullptr,
+                        dx, dw, workspace, workspace_bytes, stream);
+}
+
+int muon_classifier_loss_backward(const float* dloss, const void* x, const void* w, const void* targets,
+                                  const float* lse, int index_bytes, int dtype, int64_t tokens, int64_t vocab,
+                                  int64_t dim, void* dx, void* dw, void* workspace, uint64_t workspace_bytes,
+                                  void* stream) {
+  muon::report_error(MUON_OK, "");
+  if (tokens > 0 && !lse) return fail(MUON_EINVAL, "NULL pointer");
+  static const float none = 0.f;   // no rows: lse is not read
+  return with_gradients(targets_call(x, w, targets, index_bytes, dtype, tokens, vocab, dim), dloss, nullptr, nullptr,
+                        lse ? lse : &none, dx, dw, workspace, workspace_bytes, stream);
+}
+
+int muon_distill_loss_workspace(int dtype, int64_t tokens, int64_t vocab, int64_t dim, int k, int gradients,
+                                uint64_t* bytes) {
+  if (k < 1) return fail(MUON_EINVAL, "k must be >= 1");
+  return loss_bytes(dtype, tokens, vocab, dim, k, gradients, bytes);
+}
+
+int muon_distill_loss(const void* x, const void* w, const void* teacher, int teacher_dtype, const void* ids,
+                      int index_bytes, int dtype, int64_t tokens, int64_t vocab, int64_t dim, int k, float temperature,
+                      float* loss, float* lse, void* workspace, uint64_t workspace_bytes, void* stream) {
+  muon::report_error(MUON_OK, "");
+  return forward(teacher_call(x, w, teacher, teacher_dtype, ids, index_bytes, dtype, tokens, vocab, dim, k, temperature),
+                 loss, lse, workspace, workspace_bytes, stream);
+}
+
+int muon_distill_loss_grads(const float* dloss, const void* x, const void* w, const void* teacher, int teacher_dtype,
+                            const void* ids, int index_bytes, int dtype, int64_t tokens, int64_t vocab, int64_t dim,
+                            int k, float temperature, float* loss, float* lse, void* dx, void* dw, void* workspace,
+                            uint64_t workspace_bytes, void* stream) {
+  muon::report_error(MUON_OK, "");
+  return with_gradients(teacher_call(x, w, teacher, teacher_dtype, ids, index_bytes, dtype, tokens, vocab, dim, k,
+                                     temperature),
+                        dloss, loss, lse, nullptr, dx, dw, workspace, workspace_bytes, stream);
+}
+
+int muon_distill_loss_backward(const float* dloss, const void* x, const void* w, const void* teacher,
+                               int teacher_dtype, const void* ids, const float* lse, int index_bytes, int dtype,
+                               int64_t tokens, int64_t vocab, int64_t dim, int k, float temperature, void* dx,
+                               void* dw, void* workspace, uint64_t workspace_bytes, void* stream) {
+  muon::report_error(MUON_OK, "");
+  if (tokens > 0 && !lse) return fail(MUON_EINVAL, "NULL pointer");
+  static const float none = 0.f;
+  return with_gradients(teacher_call(x, w, teacher, teacher_dtype, ids, index_bytes, dtype, tokens, vocab, dim, k,
+                                     temperature),
+                        dloss, nullptr, nullptr, lse ? lse : &none, dx, dw, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

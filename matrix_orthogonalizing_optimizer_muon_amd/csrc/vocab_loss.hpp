@@ -1,0 +1,93 @@
+// What the classifier's losses (vocab_loss.hip) and their products
+// (vocab_products.hip) share.
+//
+// Rows that count ("live": a target or a teacher entry names something) are
+// numbered by slots, in their order; the products run over slots, so that work
+// goes with the live rows, and read rows[slot], their number and nothing else
+// from the device.  Large calls go through chunks of slots.
+#pragma once
+#include "vocab.hpp"
+
+namespace muon {
+namespace vo {
+
+enum Epilogue { kStats = 0, kStatsExp = 1, kGradient = 2 };
+
+// A product of one chunk.  Slots [slot0, slot0 + chunk), of which the first
+// live(count) exist.
+struct Chunk {
+  const int32_t* rows;     // row of each slot
+  const int32_t* count;    // live slots of the call
+  int64_t slot0;
+  int32_t size;            // slots a chunk can hold: rows of stats and of dl
+};
+
+struct LossArgs {
+  Chunk ch;
+  const void* x;           // tokens x dim
+  const void* w;           // vocab x dim
+  int64_t tokens;
+  int32_t vocab, dim;
+  float inv_tau;           // 1 / temperature
+  float to_log2;           // log2(e) / temperature: exp(l / tau) = 2^(l to_log2)
+  // logits
+  float* stats;            // [slab][chunk] pairs (largest logit, sum of exp((logit - it) / tau)), or null
+  // by slot of the chunk: a row's probabilities are exp((l - base) / tau) scale, or, where lse was given
+  // (`given`: base is it, scale 1), exp(l / tau - base); g is dloss times temperature.  Differences are taken of
+  // unscaled logits, so that nothing is rounded at a logit's size before them.
+  const float* base;
+  const float* scale;
+  const float* g;
+  bool given;
+  void* dl;                // [chunk][vocab], or null
+  // gradients
+  void* dx;                // tokens x dim
+  void* dw;                // vocab x dim
+  float* sums;             // vocab x dim: of the chunks so far, or null where there is one
+  bool first, last;        // chunk
+};
+
+__device__ __forceinline__ int32_t live_slots(const Chunk& c) {
+  const int64_t left = *c.count - c.slot0;
+  return left < 0 ? 0 : left < c.size ? (int32_t)left : c.size;
+}
+
+__device__ __forceinline__ float probability(const LossArgs& a, float l, float base, float scale) {
+  const float d = a.given ? (l * a.inv_tau - base) * 1.4426950408889634f : (l - base) * a.to_log2;
+  return __builtin_amdgcn_exp2f(d) * scale;
+}
+
+// exp of a logit less its slab's largest, between the first product and k_rescale.
+// In 16 bits: no sign and seven bits of the exponent, which values up to 1 do
+// without the rest of, leave nine of the fraction, so that this rounding (2^-10 at
+// the most) hardly adds to that of the gradient in bf16 (2^-8): a row's sum of dw
+// off by 1.03 of what one rounding gives, where two to bf16 give 1.4.  A NaN comes
+// out as anything; its row's scale is NaN.
+__device__ __forceinline__ uint32_t pack_exps(float lo, float hi) {
+  return ((__float_as_uint(lo) + 0x2000u) >> 14 & 0xffffu) | ((__float_as_uint(hi) + 0x2000u) << 2 & 0xffff0000u);
+}
+__device__ __forceinline__ void unpack_exps(uint32_t p, float& lo, float& hi) {
+  lo = __uint_as_float((p & 0xffffu) << 14);
+  hi = __uint_as_float(p >> 16 << 14);
+}
+
+// Columns whose largest logit and sum are kept together.
+template <class T>
+struct Slab;
+template <>
+struct Slab<bf16_t> {
+  static constexpr int kCols = 64;
+};
+template <>
+struct Slab<float> {
+  static constexpr int kCols = 32;
+};
+inline int slab_cols(int dtype) { return dtype == MUON_BF16 ? Slab<bf16_t>::kCols : Slab<float>::kCols; }
+
+// The products, of one chunk.
+int logits_product(const LossArgs& a, int dtype, Epilogue e, hipStream_t s);
+int dx_product(const LossArgs& a, int dtype, hipStream_t s);
+int dw_product(const LossArgs& a, int dtype, hipStream_t s);
+
+}  // namespace vo
+}  // namespace muon
