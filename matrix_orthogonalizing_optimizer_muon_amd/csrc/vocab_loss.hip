@@ -26,7 +26,9 @@ namespace muon {
 namespace vo {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
+// log2(e) and ln 2, each in two parts
+constexpr float kLog2e = 1.4426950408889634f, kLog2eLow = (float)(1.4426950408889634 - (double)kLog2e);
+constexpr float kLn2 = 0.6931471805599453f, kLn2Low = (float)(0.6931471805599453 - (double)kLn2);
 
 // ---------------------------------------------------------------------- rows
 
@@ -134,17 +136,26 @@ __global__ __launch_bounds__(kLiveThreads) void k_live(const I* __restrict__ tar
   }
 }
 
-// Zero rows of dx where a row does not count: a wave has 512 columns of one.
+// Every row by itself: a live one to its slot of xs (null: not), another's dx to
+// zeros (null: not).  A wave has 512 columns of one.
 template <class T>
-__global__ __launch_bounds__(256) void k_dead_rows(const int32_t* __restrict__ slot, int64_t tokens, int64_t dim,
-                                                   int32_t slabs, T* __restrict__ dx) {
+__global__ __launch_bounds__(256) void k_rows(const int32_t* __restrict__ slot, const T* __restrict__ x, int64_t tokens,
+                                              int64_t dim, int32_t slabs, T* __restrict__ xs, T* __restrict__ dx) {
   const int64_t unit = block_index() * 4 + (threadIdx.x >> 6);
   const int64_t t = unit / slabs;
-  if (t >= tokens || slot[t] >= 0) return;
+  if (t >= tokens) return;
   const int64_t c = (unit - t * slabs) * 512 + (threadIdx.x & 63) * 8;
   if (c >= dim) return;
-  const float zero[8] = {};
-  store8(dx + t * dim + c, dim - c < 8 ? (int)(dim - c) : 8, zero);
+  const int32_t s = slot[t];
+  const int cnt = dim - c < 8 ? (int)(dim - c) : 8;
+  float v[8] = {};
+  if (s >= 0) {
+    if (!xs) return;
+    load8(x + t * dim + c, cnt, v);
+    store8(xs + s * dim + c, cnt, v);
+  } else if (dx) {
+    store8(dx + t * dim + c, cnt, v);
+  }
 }
 
 // ------------------------------------------------------------------- targets
@@ -204,9 +215,9 @@ __global__ __launch_bounds__(256) void k_join(LossArgs a, JoinArgs j) {
   if (exists) {
     for (int32_t i = grp; i < j.slabs; i += GROUPS) {
       const float* p = a.stats + 2 * ((int64_t)i * a.ch.size + s);
-      const float m = p[0], v = p[1], to = fmaxf(top, m);
-      const float base = to == -INFINITY ? 0.f : to;
-      sum = sum * __builtin_amdgcn_exp2f((top - base) * a.to_log2) + v * __builtin_amdgcn_exp2f((m - base) * a.to_log2);
+      const float n = p[0], v = p[1], to = fmaxf(top, n);
+      if (v == 0.f) continue;   // logits of -inf alone
+      sum = sum * __builtin_amdgcn_exp2f(top - to) + v * __builtin_amdgcn_exp2f(n - to);
       top = to;
     }
   }
@@ -214,21 +225,20 @@ __global__ __launch_bounds__(256) void k_join(LossArgs a, JoinArgs j) {
   sums[grp][r] = sum;
   __syncthreads();
   if (grp || !exists) return;
-  top = -INFINITY;
-  for (int i = 0; i < GROUPS; ++i) top = fmaxf(top, tops[i][r]);
-  const float base = top == -INFINITY ? 0.f : top;
+  for (int i = 1; i < GROUPS; ++i) top = fmaxf(top, tops[i][r]);
   sum = 0.f;
-  for (int i = 0; i < GROUPS; ++i) sum += sums[i][r] * __builtin_amdgcn_exp2f((tops[i][r] - base) * a.to_log2);
+  for (int i = 0; i < GROUPS; ++i)
+    if (sums[i][r] != 0.f) sum += sums[i][r] * __builtin_amdgcn_exp2f(tops[i][r] - top);
   const int64_t t = a.ch.rows[a.ch.slot0 + s];
   const float log_sum = logf(sum);
   float off = 0.f;
   for (int32_t i = 0; i < j.k; ++i)
     if (j.id[t * j.k + i] >= 0)
-      off += (j.q ? j.q[t * j.k + i] : 1.f) * ((base - j.picked[s * j.k + i]) * a.inv_tau + log_sum);
+      off += (j.q ? j.q[t * j.k + i] : 1.f) * (log_sum - exponent(a, j.picked[s * j.k + i], top, 0.f) * kLn2);
   j.loss[t] = j.tau * j.tau * ((j.term ? j.term[t] : 0.f) + off);
-  j.lse[t] = base * a.inv_tau + log_sum;
+  j.lse[t] = fmaf(top, kLn2, fmaf(top, kLn2Low, log_sum));
   if (j.g) {
-    j.base[s] = base;
+    j.base[s] = top;
     j.scale[s] = 1.f / sum;
     j.g[s] = j.dloss[t] * j.tau;
   }
@@ -239,8 +249,10 @@ __global__ __launch_bounds__(256) void k_given(LossArgs a, JoinArgs j) {
   const int64_t s = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (s >= live_slots(a.ch)) return;
   const int64_t t = a.ch.rows[a.ch.slot0 + s];
-  j.base[s] = j.lse[t];
-  j.scale[s] = 1.f;
+  // exp(-lse) = 2^-base scale, base a whole number
+  const float lse = j.lse[t], base = rintf(lse * kLog2e);
+  j.base[s] = base;
+  j.scale[s] = __builtin_amdgcn_exp2f(-fmaf(lse, kLog2eLow, fmaf(lse, kLog2e, -base)));
   j.g[s] = j.dloss[t] * j.tau;
 }
 
@@ -258,8 +270,8 @@ __device__ __forceinline__ void load_exps(const bf16_t* p, int cnt, float (&v)[8
 }
 __device__ __forceinline__ void load_exps(const float* p, int cnt, float (&v)[8]) { load8(p, cnt, v); }
 
-// exp((logit - largest of its slab) / tau) into gradients, in place: a wave has
-// 512 columns of a slot.
+// 2^(exponent - n of its slab) into gradients, in place: a wave has 512 columns of
+// a slot.
 template <class T>
 __global__ __launch_bounds__(256) void k_rescale(LossArgs a, int32_t units) {
   const int64_t unit = block_index() * 4 + (threadIdx.x >> 6);
@@ -269,8 +281,8 @@ __global__ __launch_bounds__(256) void k_rescale(LossArgs a, int32_t units) {
   if (c >= a.vocab) return;
   const int cnt = a.vocab - c < 8 ? (int)(a.vocab - c) : 8;
   const float top = a.stats[2 * (c / Slab<T>::kCols * a.ch.size + s)];
-  const float by = __builtin_amdgcn_exp2f((top - a.base[s]) * a.to_log2) * (a.scale[s] * a.g[s]);
-  T* p = static_cast<T*>(a.dl) + s * a.vocab + c;
+  const float by = __builtin_amdgcn_exp2f(top - a.base[s]) * (a.scale[s] * a.g[s]);
+  T* p = static_cast<T*>(a.dl) + s * a.dl_ld + c;
   float v[8];
   load_exps(p, cnt, v);
 #pragma unroll
@@ -287,7 +299,7 @@ __global__ __launch_bounds__(256) void k_targets(LossArgs a, JoinArgs j) {
   if (s >= live_slots(a.ch)) return;
   const int64_t t = a.ch.rows[a.ch.slot0 + s];
   const float base = a.base[s], scale = a.scale[s], g = a.g[s];
-  T* dl = static_cast<T*>(a.dl) + s * a.vocab;
+  T* dl = static_cast<T*>(a.dl) + s * a.dl_ld;
   for (int32_t j0 = 0; j0 < j.k; j0 += 64) {
     const int32_t at = j0 + lane;
     const int32_t v = at < j.k ? j.id[t * j.k + at] : -1;
@@ -303,7 +315,7 @@ __global__ __launch_bounds__(256) void k_targets(LossArgs a, JoinArgs j) {
         q += other == v ? add : 0.f;
       }
     }
-    if (v >= 0) store1(dl + v, (probability(a, j.picked[s * j.k + at], base, scale) - q) * g);
+    if (v >= 0) store1(dl + v, (__builtin_amdgcn_exp2f(exponent(a, j.picked[s * j.k + at], base, 0.f)) * scale - q) * g);
   }
 }
 
@@ -337,14 +349,15 @@ int64_t chunk_slots(int dtype, int64_t tokens, int64_t vocab, bool grads, bool s
     if (n < 64) n = 64;
     if (n < most) most = n;
   };
-  if (grads) cap(int64_t(1) << 31, vocab * (dtype == MUON_BF16 ? 2 : 4));
+  if (grads) cap(int64_t(1) << 31, ceil_div(vocab, 64) * 64 * (dtype == MUON_BF16 ? 2 : 4));
   if (stats) cap(int64_t(1) << 28, ceil_div(vocab, slab_cols(dtype)) * 8);
   return most < 1 ? 1 : most;
 }
 
 struct LossSpace {
-  int64_t chunk, slabs;
-  uint64_t id, q, term, rows, slot, count, stats, picked, base, scale, g, dl, sums, bytes;
+  int64_t chunk, slabs, dl_ld;
+  int parts;
+  uint64_t xs, dx_parts, id, q, term, rows, slot, count, stats, picked, base, scale, g, dl, sums, bytes;
 };
 LossSpace loss_space(int dtype, int64_t tokens, int64_t vocab, int64_t dim, int k, bool teacher, bool grads,
                      bool given) {
@@ -353,6 +366,11 @@ LossSpace loss_space(int dtype, int64_t tokens, int64_t vocab, int64_t dim, int 
   const int64_t es = dtype == MUON_BF16 ? 2 : 4;
   l.chunk = chunk_slots(dtype, tokens, vocab, grads, !given);
   l.slabs = ceil_div(vocab, slab_cols(dtype));
+  l.dl_ld = ceil_div(vocab, 64) * 64;
+  const bool large = large_sizes(dtype, tokens, vocab, dim);
+  l.parts = large && grads ? dx_parts(l.chunk, vocab, dim) : 1;
+  l.xs = p.take(large ? (uint64_t)tokens * dim * 2 : 0);
+  l.dx_parts = p.take(l.parts > 1 ? (uint64_t)l.parts * l.chunk * dim * 4 : 0);
   l.id = p.take((uint64_t)tokens * k * 4);
   l.q = p.take(teacher ? (uint64_t)tokens * k * 4 : 0);
   l.term = p.take(teacher ? (uint64_t)tokens * 4 : 0);
@@ -364,7 +382,7 @@ LossSpace loss_space(int dtype, int64_t tokens, int64_t vocab, int64_t dim, int 
   l.base = p.take((uint64_t)l.chunk * 4);
   l.scale = p.take((uint64_t)l.chunk * 4);
   l.g = p.take((uint64_t)l.chunk * 4);
-  l.dl = p.take(grads ? (uint64_t)l.chunk * vocab * es : 0);
+  l.dl = p.take(grads ? (uint64_t)l.chunk * l.dl_ld * es : 0);
   l.sums = p.take(grads && l.chunk < tokens ? (uint64_t)vocab * dim * 4 : 0);
   l.bytes = p.used;
   return l;
@@ -396,16 +414,21 @@ int find_rows(const Call& c, const LossSpace& l, char* ws, hipStream_t s) {
   return launch_status("target launch");
 }
 
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
 template <class T>
 int run(const Call& c, const LossSpace& l, char* ws, hipStream_t s) {
   const bool grads = c.dw != nullptr, given = c.lse_in != nullptr;
   int rc;
   if ((rc = c.index_bytes == 8 ? find_rows<int64_t>(c, l, ws, s) : find_rows<int32_t>(c, l, ws, s))) return rc;
-  if (grads && c.tokens) {
+  const bool large = large_sizes(c.dtype, c.tokens, c.vocab, c.dim) && aligned16(c.w) &&
+                     (!grads || (aligned16(c.dx) && aligned16(c.dw)));
+  if (c.tokens && (grads || large)) {
     const int64_t slabs = ceil_div(c.dim, 512);
-    hipLaunchKernelGGL((k_dead_rows<T>), grid_of_blocks(ceil_div(c.tokens * slabs, 4), 256), dim3(256), 0, s,
-                       reinterpret_cast<int32_t*>(ws + l.slot), c.tokens, c.dim, (int32_t)slabs,
-                       static_cast<T*>(c.dx));
+    hipLaunchKernelGGL((k_rows<T>), grid_of_blocks(ceil_div(c.tokens * slabs, 4), 256), dim3(256), 0, s,
+                       reinterpret_cast<int32_t*>(ws + l.slot), static_cast<const T*>(c.x), c.tokens, c.dim,
+                       (int32_t)slabs, large ? reinterpret_cast<T*>(ws + l.xs) : nullptr,
+                       grads ? static_cast<T*>(c.dx) : nullptr);
   }
   LossArgs a = {};
   a.ch.rows = reinterpret_cast<int32_t*>(ws + l.rows);
@@ -416,17 +439,21 @@ int run(const Call& c, const LossSpace& l, char* ws, hipStream_t s) {
   a.tokens = c.tokens;
   a.vocab = (int32_t)c.vocab;
   a.dim = (int32_t)c.dim;
-  a.inv_tau = 1.f / c.tau;
-  a.to_log2 = kLog2e / c.tau;
+  a.xs = large ? ws + l.xs : nullptr;
+  a.dl_ld = l.dl_ld;
+  a.dx_parts = reinterpret_cast<float*>(ws + l.dx_parts);
+  a.parts = l.parts;
+  const double to_log2 = 1.4426950408889634 / (double)c.tau;
+  a.to_log2 = (float)to_log2;
+  a.to_log2_low = (float)(to_log2 - (double)a.to_log2);
   a.stats = given ? nullptr : reinterpret_cast<float*>(ws + l.stats);
   a.base = reinterpret_cast<float*>(ws + l.base);
   a.scale = reinterpret_cast<float*>(ws + l.scale);
-  a.given = given;
   a.g = reinterpret_cast<float*>(ws + l.g);
   a.dl = grads ? ws + l.dl : nullptr;
   a.dx = c.dx;
   a.dw = c.dw;
-  a.sums = reinterpret_cast<float*>(ws + l.sums);
+  a.sums = l.chunk < c.tokens ? reinterpret_cast<float*>(ws + l.sums) : nullptr;
   JoinArgs j = {};
   j.id = reinterpret_cast<int32_t*>(ws + l.id);
   j.q = c.teacher ? reinterpret_cast<float*>(ws + l.q) : nullptr;

@@ -26,23 +26,25 @@ struct LossArgs {
   Chunk ch;
   const void* x;           // tokens x dim
   const void* w;           // vocab x dim
+  const void* xs;          // x's live rows by slot, or null where the products gather them
   int64_t tokens;
   int32_t vocab, dim;
-  float inv_tau;           // 1 / temperature
-  float to_log2;           // log2(e) / temperature: exp(l / tau) = 2^(l to_log2)
-  // logits
-  float* stats;            // [slab][chunk] pairs (largest logit, sum of exp((logit - it) / tau)), or null
-  // by slot of the chunk: a row's probabilities are exp((l - base) / tau) scale, or, where lse was given
-  // (`given`: base is it, scale 1), exp(l / tau - base); g is dloss times temperature.  Differences are taken of
-  // unscaled logits, so that nothing is rounded at a logit's size before them.
+  int64_t dl_ld;           // elements of a row of dl: vocab in whole slabs of 64
+  // exp(l / temperature) = 2^(l (to_log2 + to_log2_low)): log2(e) / temperature in two parts
+  float to_log2, to_log2_low;
+  // logits: exponents of two come as a whole number n and a sum of 2^(l to_log2 - n), so that differences of
+  // exponents are exact and nothing is rounded at a logit's size
+  float* stats;            // [slab][chunk] pairs (n, the smallest at or above the largest exponent; sum), or null
+  // by slot of the chunk: probabilities are 2^(l to_log2 - base) scale; g is dloss times temperature
   const float* base;
   const float* scale;
   const float* g;
-  bool given;
-  void* dl;                // [chunk][vocab], or null
+  void* dl;                // [chunk][dl_ld], or null
   // gradients
   void* dx;                // tokens x dim
   void* dw;                // vocab x dim
+  float* dx_parts;         // [part][chunk][dim]: sums of parts of the vocabulary, where there are more than one
+  int32_t parts;
   float* sums;             // vocab x dim: of the chunks so far, or null where there is one
   bool first, last;        // chunk
 };
@@ -52,12 +54,17 @@ __device__ __forceinline__ int32_t live_slots(const Chunk& c) {
   return left < 0 ? 0 : left < c.size ? (int32_t)left : c.size;
 }
 
-__device__ __forceinline__ float probability(const LossArgs& a, float l, float base, float scale) {
-  const float d = a.given ? (l * a.inv_tau - base) * 1.4426950408889634f : (l - base) * a.to_log2;
-  return __builtin_amdgcn_exp2f(d) * scale;
+// The exponent of two of a logit, less n.  In fp32 with both parts of the factor.
+__device__ __forceinline__ float exponent(const LossArgs& a, float l, float n, float) {
+  return fmaf(l, a.to_log2_low, fmaf(l, a.to_log2, -n));
+}
+__device__ __forceinline__ float exponent(const LossArgs& a, float l, float n, bf16_t) { return fmaf(l, a.to_log2, -n); }
+// n of a largest logit (0 for one of -inf).
+__device__ __forceinline__ float whole_exponent(const LossArgs& a, float top) {
+  return top == -INFINITY ? 0.f : ceilf(top * a.to_log2);
 }
 
-// exp of a logit less its slab's largest, between the first product and k_rescale.
+// 2^(exponent - n) of a slab's n, between the first product and k_rescale.
 // In 16 bits: no sign and seven bits of the exponent, which values up to 1 do
 // without the rest of, leave nine of the fraction, so that this rounding (2^-10 at
 // the most) hardly adds to that of the gradient in bf16 (2^-8): a row's sum of dw
@@ -71,7 +78,7 @@ __device__ __forceinline__ void unpack_exps(uint32_t p, float& lo, float& hi) {
   hi = __uint_as_float(p >> 16 << 14);
 }
 
-// Columns whose largest logit and sum are kept together.
+// Columns whose n and sum are kept together.
 template <class T>
 struct Slab;
 template <>
@@ -83,6 +90,13 @@ struct Slab<float> {
   static constexpr int kCols = 32;
 };
 inline int slab_cols(int dtype) { return dtype == MUON_BF16 ? Slab<bf16_t>::kCols : Slab<float>::kCols; }
+
+// Whether the large tiles take a call's sizes: bf16 rows of whole 16-byte chunks
+// that 31 bits address 256 of; and the rest of what they need of a call.
+inline bool large_sizes(int dtype, int64_t tokens, int64_t vocab, int64_t dim) {
+  return dtype == MUON_BF16 && dim % 8 == 0 && vocab < (1 << 21) && dim < (1 << 21) && tokens > 0;
+}
+int dx_parts(int64_t tokens, int64_t vocab, int64_t dim);
 
 // The products, of one chunk.
 int logits_product(const LossArgs& a, int dtype, Epilogue e, hipStream_t s);

@@ -5,14 +5,19 @@
 //   dw      dw[v][i]  = sum_s dl[s][v] x[rows[s]][i]     both k-major
 //
 // Logits are never stored: what leaves the first product is, for each slab of
-// columns, a row's largest logit and the sum over it (kStats), these and
-// exp((logit - largest) / tau) in as many bits as x has (kStatsExp, which k_rescale makes
+// columns, a row's largest exponent of two, rounded up, and the sum of 2^ the rest
+// (kStats), these and 2^ the rest in as many bits as x has (kStatsExp, which k_rescale makes
 // gradients of once the row's sum is known), or the logits' gradient without
 // the targets' part (kGradient, where the sum is known before).
 #include <hip/hip_runtime.h>
 
+#include <math.h>
+
+#include <type_traits>
+
 #include "expert_stage.hpp"
 #include "vocab_loss.hpp"
+#include "vocab_walk.hpp"
 
 namespace muon {
 namespace vo {
@@ -68,12 +73,14 @@ __global__ __launch_bounds__(256) void k_tile(LossArgs a, int32_t tiles_n) {
     if (m_left <= 0) return;
     K = a.vocab;
     sp.init(a.dl, nullptr, m0, m_left, 0, 0, a.vocab);
+    sp.ld = a.dl_ld;
     sq.init(a.w, nullptr, 0, K, 0, n0, a.dim);
   } else {
     m_left = a.vocab - m0;
     if (m_left <= 0) return;
     K = live;
     sp.init(a.dl, nullptr, 0, K, 0, (int32_t)m0, a.vocab);
+    sp.ld = a.dl_ld;
     sq.init(a.x, rows, 0, K, a.tokens, n0, a.dim);
   }
   f32x16_t acc[NT][NT];
@@ -141,31 +148,30 @@ __global__ __launch_bounds__(256) void k_tile(LossArgs a, int32_t tiles_n) {
 #pragma unroll
           for (int v = 0; v < 16; ++v)
             if (c0 + 32 * j + 8 * (v / 4) + v % 4 < a.vocab) top = fmaxf(top, e[j][v]);
-        top = fmaxf(top, __shfl_xor(top, 32, 64));
-        const float base = top == -INFINITY ? 0.f : top;
+        const float n = whole_exponent(a, fmaxf(top, __shfl_xor(top, 32, 64)));
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int v = 0; v < 16; ++v) {
-            e[j][v] = __builtin_amdgcn_exp2f((e[j][v] - base) * a.to_log2);
+            e[j][v] = __builtin_amdgcn_exp2f(exponent(a, e[j][v], n, T()));
             if (c0 + 32 * j + 8 * (v / 4) + v % 4 < a.vocab) sum += e[j][v];
           }
         sum += __shfl_xor(sum, 32, 64);
         if (exists && lane < 32) {
           float* st = a.stats + 2 * ((int64_t)((n0 + wx * W) / W) * a.ch.size + r);
-          st[0] = top;
+          st[0] = n;
           st[1] = sum;
         }
       } else {
-        const float base = exists ? a.base[r] : 0.f, g = exists ? a.g[r] : 0.f;
+        const float base = exists ? a.base[r] : 0.f, by = exists ? a.scale[r] * a.g[r] : 0.f;
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int v = 0; v < 16; ++v) e[j][v] = probability(a, e[j][v], base, g);
+          for (int v = 0; v < 16; ++v) e[j][v] = __builtin_amdgcn_exp2f(exponent(a, e[j][v], base, T())) * by;
       }
       if constexpr (EPI != kStats) {
         if (exists) {
-          T* out = static_cast<T*>(a.dl) + r * a.vocab;
+          T* out = static_cast<T*>(a.dl) + r * a.dl_ld;
 #pragma unroll
           for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -197,6 +203,234 @@ __global__ __launch_bounds__(256) void k_tile(LossArgs a, int32_t tiles_n) {
   }
 }
 
+// --------------------------------------------------------------- large tiles
+
+// Logits, 256 x 256 a tile.  A wave's 64 columns are a slab, 32 of them in each
+// half of a row's two lanes.
+template <int EPI>
+struct LogitsWalk {
+  typedef Shapes<false, false> Sh;
+  typedef RowPanel PC;
+  typedef RowPanel QC;
+  const LossArgs& a;
+  Walk walk;
+  int32_t live;
+  __device__ __forceinline__ bool next(OutTile& t) { return walk.next(t); }
+  __device__ __forceinline__ int64_t m_left(const OutTile& t) const { return live - t.m0; }
+  __device__ __forceinline__ int64_t n_left(const OutTile& t) const { return a.vocab - t.n0; }
+  __device__ __forceinline__ Panel p(const OutTile& t) const {
+    return Panel{static_cast<const char*>(a.xs) + (a.ch.slot0 + t.m0) * a.dim * 2, (uint32_t)a.dim * 2u, live - t.m0,
+                 a.dim};
+  }
+  __device__ __forceinline__ Panel q(const OutTile& t) const {
+    return Panel{static_cast<const char*>(a.w) + (int64_t)t.n0 * a.dim * 2, (uint32_t)a.dim * 2u, a.vocab - t.n0, a.dim};
+  }
+  __device__ __forceinline__ int store(Acc& acc, const OutTile& t, int mt, int row0, int col0, MUON_LDS char* buf,
+                                       int lane) const {
+    const int32_t first = t.n0 + col0;
+    if (first >= a.vocab) return 0;
+    const int32_t left = a.vocab - first;   // columns of the slab that exist, where less than 64
+    const int c = 4 * (lane >> 5);
+    const auto rs = nt::make_rsrc(static_cast<char*>(a.dl) + ((int64_t)t.m0 * a.dl_ld + first) * 2, kRange);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i >= mt) break;
+      const int32_t r = t.m0 + row0 + 32 * i + (lane & 31);
+      const bool exists = r < live;
+      if (left < 64) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int v = 0; v < 16; ++v)
+            if (c + 32 * j + 8 * (v / 4) + v % 4 >= left) acc[i][j][v] = -INFINITY;
+      }
+      float n, by = 1.f;
+      if constexpr (EPI != kGradient) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) top = fmaxf(top, acc[i][j][v]);
+        n = whole_exponent(a, fmaxf(top, __shfl_xor(top, 32, 64)));
+      } else {
+        n = exists ? a.base[r] : 0.f;
+        by = exists ? a.scale[r] * a.g[r] : 0.f;
+      }
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          float e[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            e[u] = __builtin_amdgcn_exp2f(exponent(a, acc[i][j][4 * g + u], n, bf16_t()));
+            if (EPI == kGradient) e[u] = left >= 64 || c + 32 * j + 8 * g + u < left ? e[u] * by : 0.f;
+            else sum += e[u];
+          }
+          if constexpr (EPI == kStatsExp) put_row(buf, lane, 4 * j + g, u32x2{pack_exps(e[0], e[1]), pack_exps(e[2], e[3])});
+          if constexpr (EPI == kGradient) put_row(buf, lane, 4 * j + g, u32x2{pack2(e[0], e[1]), pack2(e[2], e[3])});
+        }
+      if constexpr (EPI != kGradient) {
+        sum += __shfl_xor(sum, 32, 64);
+        if (exists && lane < 32) {
+          typedef float f32x2 __attribute__((ext_vector_type(2)));
+          *reinterpret_cast<f32x2*>(a.stats + 2 * ((int64_t)(first / 64) * a.ch.size + r)) = f32x2{n, sum};
+        }
+      }
+      if constexpr (EPI != kStats) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const u32x4 v = get_row(buf, lane, u);
+          const int q = row0 + 32 * i + u * 8 + lane / 8;
+          const uint32_t at = t.m0 + q < live ? (uint32_t)q * (uint32_t)(a.dl_ld * 2) + 16u * (lane & 7) : kNone;
+          __builtin_amdgcn_raw_buffer_store_b128(v, rs, at, 0, 0);
+        }
+      }
+    }
+    return 0;
+  }
+};
+
+template <int EPI>
+__global__ __launch_bounds__(512, 2) void k_logits(LossArgs a) {
+  __shared__ __attribute__((aligned(16))) char lds[Shapes<false, false>::LDS];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  LogitsWalk<EPI> o{a, {}, __builtin_amdgcn_readfirstlane(live_slots(a.ch))};
+  o.walk.init(o.live, a.vocab, a.dim, 1);
+  walk_tiles(lds, lane, w, o);
+}
+
+// The gradients' products.  Outputs go through LDS in fp32, 32 columns at a time,
+// or in bf16, 64 at a time.
+template <int PRODUCT>
+struct GradWalk {
+  static constexpr bool kX = PRODUCT == kDx;
+  typedef Shapes<!kX, true> Sh;
+  typedef typename std::conditional<kX, RowPanel, ColPanel>::type PC;
+  typedef ColPanel QC;
+  const LossArgs& a;
+  Walk walk;
+  int32_t live;
+  __device__ __forceinline__ bool next(OutTile& t) { return walk.next(t); }
+  __device__ __forceinline__ int32_t rows() const { return kX ? live : a.vocab; }
+  __device__ __forceinline__ int64_t m_left(const OutTile& t) const { return rows() - t.m0; }
+  __device__ __forceinline__ int64_t n_left(const OutTile& t) const { return a.dim - t.n0; }
+  __device__ __forceinline__ Panel p(const OutTile& t) const {
+    const char* dl = static_cast<const char*>(a.dl);
+    const int64_t k = (int64_t)t.k0 * kBK;
+    if (kX)
+      return Panel{dl + (t.m0 * a.dl_ld + k) * 2, (uint32_t)a.dl_ld * 2u, live - t.m0, (int32_t)(a.dl_ld - k)};
+    return Panel{dl + t.m0 * 2ll, (uint32_t)a.dl_ld * 2u, (int32_t)a.dl_ld - t.m0, live};
+  }
+  __device__ __forceinline__ Panel q(const OutTile& t) const {
+    const int64_t k = (int64_t)t.k0 * kBK;
+    const char* from = kX ? static_cast<const char*>(a.w) + k * a.dim * 2
+                          : static_cast<const char*>(a.xs) + a.ch.slot0 * a.dim * 2;
+    return Panel{from + t.n0 * 2ll, (uint32_t)a.dim * 2u, a.dim - t.n0, (int32_t)((kX ? a.vocab : live) - k)};
+  }
+  __device__ __forceinline__ int store(Acc& acc, const OutTile& t, int mt, int row0, int col0, MUON_LDS char* buf,
+                                       int lane) const {
+    const int32_t c0 = t.n0 + col0, m = rows() - t.m0;
+    if (kX ? a.parts > 1 : a.sums != nullptr) {   // sums: of a part, or of the chunks so far
+      float* out = kX ? a.dx_parts + ((int64_t)t.part * a.ch.size + t.m0) * a.dim : a.sums + (int64_t)t.m0 * a.dim;
+      bf16_t* dw = static_cast<bf16_t*>(a.dw) + (int64_t)t.m0 * a.dim;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i >= mt) break;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            put_row(buf, lane, g, u32x4{__float_as_uint(acc[i][j][4 * g]), __float_as_uint(acc[i][j][4 * g + 1]),
+                                        __float_as_uint(acc[i][j][4 * g + 2]), __float_as_uint(acc[i][j][4 * g + 3])});
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            u32x4 v = get_row(buf, lane, u);
+            const int q = row0 + 32 * i + u * 8 + lane / 8, c = c0 + 32 * j + 4 * (lane & 7);
+            if (q >= m || c >= a.dim) continue;
+            const int64_t at = (int64_t)q * a.dim + c;
+            if (!kX && !a.first) {
+              const u32x4 before = *reinterpret_cast<const u32x4*>(out + at);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) + __uint_as_float(before[x]));
+            }
+            if (!kX && a.last)
+              *reinterpret_cast<u32x2*>(dw + at) =
+                  u32x2{pack2(__uint_as_float(v[0]), __uint_as_float(v[1])), pack2(__uint_as_float(v[2]), __uint_as_float(v[3]))};
+            else
+              *reinterpret_cast<u32x4*>(out + at) = v;
+          }
+        }
+      }
+      return 0;
+    }
+    if (!kX)
+      return tile_store(acc, mt, buf, static_cast<bf16_t*>(a.dw) + (int64_t)t.m0 * a.dim, row0, m < 256 ? m : 256, c0,
+                        a.dim, lane);
+    // rows of dx lie where rows[slot] says
+    const int32_t* rows = a.ch.rows + a.ch.slot0 + t.m0;
+    bf16_t* dx = static_cast<bf16_t*>(a.dx);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i >= mt) break;
+      int32_t to[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int q = row0 + 32 * i + u * 8 + lane / 8;
+        to[u] = q < m ? rows[q] : -1;
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          put_row(buf, lane, 4 * j + g, u32x2{pack2(acc[i][j][4 * g], acc[i][j][4 * g + 1]),
+                                              pack2(acc[i][j][4 * g + 2], acc[i][j][4 * g + 3])});
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const u32x4 v = get_row(buf, lane, u);
+        const int c = c0 + 8 * (lane & 7);
+        if (to[u] >= 0 && c < a.dim) *reinterpret_cast<u32x4*>(dx + (int64_t)to[u] * a.dim + c) = v;
+      }
+    }
+    return 0;
+  }
+};
+
+template <int PRODUCT>
+__global__ __launch_bounds__(512, 2) void k_grad(LossArgs a) {
+  __shared__ __attribute__((aligned(16))) char lds[GradWalk<PRODUCT>::Sh::LDS];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  GradWalk<PRODUCT> o{a, {}, __builtin_amdgcn_readfirstlane(live_slots(a.ch))};
+  if (PRODUCT == kDx) o.walk.init(o.live, a.dim, a.vocab, (uint32_t)a.parts);
+  else o.walk.init(a.vocab, a.dim, o.live, 1);
+  walk_tiles(lds, lane, w, o);
+}
+
+// The parts' sums of dx, in their order, to the rows where they belong: a wave has
+// 512 columns of a slot.
+__global__ __launch_bounds__(256) void k_dx_join(LossArgs a, int32_t units) {
+  const int64_t unit = block_index() * 4 + (threadIdx.x >> 6);
+  const int64_t s = unit / units;
+  if (s >= live_slots(a.ch)) return;
+  const int64_t c = (unit - s * units) * 512 + (threadIdx.x & 63) * 8;
+  if (c >= a.dim) return;
+  float sum[8] = {};
+  for (int32_t p = 0; p < a.parts; ++p) {
+    float v[8];
+    load8(a.dx_parts + ((int64_t)p * a.ch.size + s) * a.dim + c, 8, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i] += v[i];
+  }
+  store8(static_cast<bf16_t*>(a.dx) + (int64_t)a.ch.rows[a.ch.slot0 + s] * a.dim + c, 8, sum);
+}
+
+template <int EPI>
+int launch_logits_large(const LossArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((k_logits<EPI>), dim3(kWalkers), dim3(512), 0, s, a);
+  return launch_status("classifier product launch");
+}
+
 template <class T, int PRODUCT, int EPI>
 int launch_tile(const LossArgs& a, int64_t m, int64_t n, hipStream_t s) {
   const int64_t tiles_n = ceil_div(n, Tile<T>::B), blocks = ceil_div(m, Tile<T>::B) * tiles_n;
@@ -214,15 +448,51 @@ int launch_logits(const LossArgs& a, Epilogue e, hipStream_t s) {
 }  // namespace
 
 int logits_product(const LossArgs& a, int dtype, Epilogue e, hipStream_t s) {
+  if (a.xs) {
+    if (e == kStats) return launch_logits_large<kStats>(a, s);
+    return e == kStatsExp ? launch_logits_large<kStatsExp>(a, s) : launch_logits_large<kGradient>(a, s);
+  }
   return dtype == MUON_BF16 ? launch_logits<bf16_t>(a, e, s) : launch_logits<float>(a, e, s);
 }
 
+// Parts of the vocabulary whose sums a dx of at most `tokens` rows is made of: 256
+// walkers share the tiles of all parts, so a part more brings the last round's
+// walkers work and costs 8 bytes an element of dx (written and read).  A k-tile
+// takes a walker about 1.7 us; those bytes go at 4 TB/s.
+int dx_parts(int64_t tokens, int64_t vocab, int64_t dim) {
+  const double tiles = (double)ceil_div(tokens, 256) * ceil_div(dim, 256), k_tiles = (double)ceil_div(vocab, kBK);
+  int best = 1;
+  double least = 0;
+  for (int p = 1; p <= 32 && k_tiles >= 8.0 * p; ++p) {
+    const double rounds = ceil(tiles * p / kWalkers), us = rounds * ceil(k_tiles / p) * 1.7 +
+                          (p > 1 ? 4 + p * (double)tokens * dim * 8 / 4e6 : 0);
+    if (p == 1 || us < least) {
+      least = us;
+      best = p;
+    }
+  }
+  return best;
+}
+
 int dx_product(const LossArgs& a, int dtype, hipStream_t s) {
+  if (a.xs) {
+    hipLaunchKernelGGL((k_grad<kDx>), dim3(kWalkers), dim3(512), 0, s, a);
+    if (a.parts > 1) {
+      const int64_t units = ceil_div(a.dim, 512);
+      hipLaunchKernelGGL(k_dx_join, grid_of_blocks(ceil_div(a.ch.size * units, 4), 256), dim3(256), 0, s, a,
+                         (int32_t)units);
+    }
+    return launch_status("classifier product launch");
+  }
   return dtype == MUON_BF16 ? launch_tile<bf16_t, kDx, kStats>(a, a.ch.size, a.dim, s)
                             : launch_tile<float, kDx, kStats>(a, a.ch.size, a.dim, s);
 }
 
 int dw_product(const LossArgs& a, int dtype, hipStream_t s) {
+  if (a.xs) {
+    hipLaunchKernelGGL((k_grad<kDw>), dim3(kWalkers), dim3(512), 0, s, a);
+    return launch_status("classifier product launch");
+  }
   return dtype == MUON_BF16 ? launch_tile<bf16_t, kDw, kStats>(a, a.vocab, a.dim, s)
                             : launch_tile<float, kDw, kStats>(a, a.vocab, a.dim, s);
 }

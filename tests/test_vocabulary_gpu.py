@@ -136,7 +136,8 @@ def test_embed_passes_values_on():
 # ---------------------------------------------------------------------- losses
 
 SIZES = [(1, 1, 1), (1, 16, 16), (1, 1000, 64), (5, 33, 7), (17, 129, 200), (64, 128, 64), (130, 300, 72),
-         (257, 515, 129), (300, 1024, 256), (513, 70, 520)]
+         (257, 515, 129), (300, 1024, 256), (513, 70, 520), (700, 1111, 264), (520, 2050, 128), (385, 6007, 136),
+         (129, 129, 8), (2100, 40, 16)]
 
 
 def inputs(tokens, vocab, dim, dtype, k, seed, absent=0.2, index=J):
