@@ -614,7 +614,7 @@ int muon_embed_backward(const void* dout, const void* tokens, int index_bytes, i
  * Cross entropy of the logits l = x w^T, which are never in memory whole:
  *   lse[t] = log sum_v exp(l_tv),  loss[t] = lse[t] - l_t,targets[t]
  * A target that names nothing takes its row out: loss and lse 0, its gradient
- * zeros, its x not read.  Work goes with the rows that are left.
+ * zeros, and its x reaches nothing.  Work goes with the rows that are left.
  *   muon_classifier_loss           loss and lse (fp32, tokens)
  *   muon_classifier_loss_grads     these and, for the loss's gradient dloss (fp32,
  *                                  tokens), dx (tokens x dim) and dw (vocab x dim):

@@ -46,6 +46,7 @@ def build(verbose: bool = False) -> str:
         for src, kind in (("kernels.hip", "hip"), ("probe.hip", "hip"), ("noalloc.hip", "hip"),
                           ("expert_rows.hip", "hip"), ("expert_products.hip", "hip"),
                           ("vocab_embed.hip", "hip"), ("vocab_loss.hip", "hip"), ("vocab_products.hip", "hip"),
+                          ("vocab_few.hip", "hip"),
                           ("abi.cpp", "hip"), ("plan.cpp", "host"), ("assign.cpp", "host")):
             obj = os.path.join(tmp, src + ".o")
             path = os.path.join(CSRC, src)

@@ -47,7 +47,7 @@ __global__ __launch_bounds__(256) void k_embed(const I* __restrict__ tokens, con
 // goes through its own segment in order and alone.  250 blocks read 16384
 // tokens of 8 bytes from L2 in a few microseconds.
 // start: vocab + 1 first places of the entries; pos and key: places, their tokens.
-constexpr int kOrderThreads = 1024, kOrderWaves = 16, kOrderWidth = 512;
+constexpr int kOrderThreads = 1024, kOrderWaves = 16, kOrderWidth = 512, kOrderRound = 16;
 
 template <class I>
 __global__ __launch_bounds__(kOrderThreads) void k_order(const I* __restrict__ tokens, int32_t n, int32_t vocab,
@@ -64,12 +64,12 @@ __global__ __launch_bounds__(kOrderThreads) void k_order(const I* __restrict__ t
   const int64_t segment = ((int64_t)n + kOrderThreads - 1) / kOrderThreads * 64;
   const int64_t first = w * segment < n ? w * segment : n, last = first + segment < n ? first + segment : n;
   int32_t below = 0;
-  for (int64_t i = first + lane; i < last; i += 256) {
-    int32_t v[4];
+  int32_t v[kOrderRound];   // the last round's tokens
+  for (int64_t i = first + lane; i - lane < last; i += 64 * kOrderRound) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) v[u] = i + 64 * u < last ? read_index(tokens, i + 64 * u, vocab) : -1;
+    for (int u = 0; u < kOrderRound; ++u) v[u] = i + 64 * u < last ? read_index(tokens, i + 64 * u, vocab) : -1;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < kOrderRound; ++u) {
       below += v[u] >= 0 && v[u] < lo;
       if (v[u] >= lo && v[u] < hi) atomicAdd(&count[(v[u] - lo) * kOrderWaves + w], 1);   // whole numbers: any order
     }
@@ -98,13 +98,15 @@ __global__ __launch_bounds__(kOrderThreads) void k_order(const I* __restrict__ t
   for (int i = tid; i < hi - lo; i += kOrderThreads) start[lo + i] = count[i * kOrderWaves];
   if (hi == vocab && tid == kOrderThreads - 1) start[vocab] = run;   // cells past vocab are empty
   __syncthreads();
-  for (int64_t i = first; i < last; i += 256) {
-    int32_t v[4];
+  const bool once = last - first <= 64 * kOrderRound;   // v still holds them
+  for (int64_t i = first; i < last; i += 64 * kOrderRound) {
+    if (!once) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      v[u] = i + 64 * u + lane < last ? read_index(tokens, i + 64 * u + lane, vocab) : -1;
+      for (int u = 0; u < kOrderRound; ++u)
+        v[u] = i + 64 * u + lane < last ? read_index(tokens, i + 64 * u + lane, vocab) : -1;
+    }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < kOrderRound; ++u) {
       const bool in = v[u] >= lo && v[u] < hi;
       uint64_t left = __ballot(in);
       while (left) {
@@ -131,7 +133,7 @@ __global__ __launch_bounds__(kOrderThreads) void k_order(const I* __restrict__ t
 // are summed window by window, at most two such rows meeting in one (the row of
 // its first place: part 0, and one that starts behind it: part 1), and the wave
 // of the window where the row starts adds these sums up in the next launch.
-constexpr int kWindow = 64;
+constexpr int kWindow = 64, kGradRows = 4;   // kGradRows rows a wave
 
 // Sum of dout's rows at `cnt` <= 64 places, held one a lane, in their order.
 template <class T>
@@ -169,16 +171,25 @@ __global__ __launch_bounds__(256) void k_embed_grad(const T* __restrict__ dout, 
   const int64_t c = (unit - item * slabs) * kCols + lane * 8;
   const int cnt = c >= dim ? 0 : dim - c < 8 ? (int)(dim - c) : 8;
   float sum[8];
-  if (item >= windows) {   // a row
-    const int64_t v = item - windows;
-    if (v >= vocab) return;
-    const int32_t s = start[v], e = start[v + 1];
-    if (e - s > kWindow) return;
-    const int32_t place = lane < e - s ? pos[s + lane] : 0;
-    sum_rows(dout, dim, place, 0, e - s, c, cnt, sum);
+  if (item >= windows) {   // rows
+    const int64_t v0 = (item - windows) * kGradRows;
+    if (v0 >= vocab) return;
+    const int32_t bound = start[v0 + lane < vocab ? v0 + lane : vocab];
+    const int32_t first = __builtin_amdgcn_readlane(bound, 0);
+    const bool together = __builtin_amdgcn_readlane(bound, kGradRows) - first <= 64;   // their places in one load
+    int32_t place = together && first + lane < __builtin_amdgcn_readlane(bound, kGradRows) ? pos[first + lane] : 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum[i] *= scale;
-    if (cnt) store8(dtable + v * dim + c, cnt, sum);
+    for (int r = 0; r < kGradRows; ++r) {
+      if (v0 + r >= vocab) return;
+      const int32_t s = __builtin_amdgcn_readlane(bound, r), e = __builtin_amdgcn_readlane(bound, r + 1);
+      if (e - s > kWindow) continue;
+      if (!together) place = lane < e - s ? pos[s + lane] : 0;
+      const int from = together ? s - first : 0;
+      sum_rows(dout, dim, place, from, from + (e - s), c, cnt, sum);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] *= scale;
+      if (cnt) store8(dtable + (v0 + r) * dim + c, cnt, sum);
+    }
     return;
   }
   const int32_t total = start[vocab];
@@ -264,7 +275,7 @@ int launch_grad(const void* dout, const int32_t* start, const int32_t* pos, cons
                 int64_t vocab, int64_t dim, float scale, float* parts, void* dtable, hipStream_t s) {
   const int64_t slabs = ceil_div(dim, kCols), windows = n > kWindow ? ceil_div(n, kWindow) : 0;
   // without windows no row is long
-  hipLaunchKernelGGL((k_embed_grad<T>), grid_of_blocks(blocks_of(windows + vocab, slabs), 256), dim3(256), 0, s,
+  hipLaunchKernelGGL((k_embed_grad<T>), grid_of_blocks(blocks_of(windows + ceil_div(vocab, kGradRows), slabs), 256), dim3(256), 0, s,
                      static_cast<const T*>(dout), start, pos, key, (int32_t)(windows ? n : 0), (int32_t)vocab, dim,
                      (int32_t)slabs, scale, static_cast<T*>(dtable), parts);
   if (windows)

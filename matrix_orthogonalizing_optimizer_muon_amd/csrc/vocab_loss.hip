@@ -14,10 +14,9 @@
 // written from the fp32 logits, so that exp(..) - q loses nothing to the
 // rounding of dl before the difference.
 //
-// dl is the products' operand and so in the type of x: bf16 rounds each entry by
-// 2^-9 at the most of what it is, as it would a logits gradient in memory.  With
-// the loss in the same pass an entry is rounded twice (exp of the logit less the
-// largest of its slab before its row's sum is known, the gradient after).
+// dl is the products' operand and so in the type of x: bf16 rounds an entry by
+// 2^-8 of what it is at the most, as it would a logits gradient in memory (in the
+// loss's own pass it is rounded before, too, to 16 bits of its own: pack_exps).
 #include <hip/hip_runtime.h>
 
 #include "vocab_loss.hpp"
@@ -26,15 +25,8 @@ namespace muon {
 namespace vo {
 namespace {
 
-// log2(e) and ln 2, each in two parts
-constexpr float kLog2e = 1.4426950408889634f, kLog2eLow = (float)(1.4426950408889634 - (double)kLog2e);
-constexpr float kLn2 = 0.6931471805599453f, kLn2Low = (float)(0.6931471805599453 - (double)kLn2);
-
 // ---------------------------------------------------------------------- rows
 
-// A teacher's entries of a row: ids, or -1 where there is none (an id outside the
-// vocabulary, a logit of -inf or NaN), and the softmax of their logits over tau;
-// term: sum q log q.  A wave a row, entry lane + 64 i.
 template <class TT, class I>
 __global__ __launch_bounds__(256) void k_teacher(const TT* __restrict__ teacher, const I* __restrict__ ids,
                                                  int64_t tokens, int32_t k, int32_t vocab, float inv_tau,
@@ -43,47 +35,17 @@ __global__ __launch_bounds__(256) void k_teacher(const TT* __restrict__ teacher,
   const int lane = threadIdx.x & 63;
   const int64_t t = block_index() * 4 + (threadIdx.x >> 6);
   if (t >= tokens) return;
-  constexpr int N = kMaxTeacher / 64;
-  float v[N];
-  int32_t at[N];
-  float top = -INFINITY;
+  TeacherRow r;
+  r.read(teacher + t * k, ids + t * k, k, vocab, inv_tau, lane);
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
+  for (int i = 0; i < TeacherRow::N; ++i) {
     const int j = lane + 64 * i;
-    at[i] = -1;
-    v[i] = -INFINITY;
     if (j < k) {
-      at[i] = read_index(ids, t * k + j, vocab);
-      const float l = to_f32(teacher[t * k + j]);
-      if (!(l > -INFINITY)) at[i] = -1;
-      if (at[i] >= 0) v[i] = fminf(l, 3.402823466e38f);
-    }
-    top = fmaxf(top, v[i]);
-  }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
-  float total = 0.f, e[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    v[i] = at[i] >= 0 ? (v[i] - top) * inv_tau : 0.f;
-    e[i] = at[i] >= 0 ? expf(v[i]) : 0.f;
-    total += e[i];
-  }
-  total = wave_sum(total);
-  const float log_total = total > 0.f ? logf(total) : 0.f;
-  float sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int j = lane + 64 * i;
-    const float p = at[i] >= 0 ? e[i] / total : 0.f;
-    if (p > 0.f) sum += p * (v[i] - log_total);
-    if (j < k) {
-      id[t * k + j] = at[i];
-      q[t * k + j] = p;
+      id[t * k + j] = r.at[i];
+      q[t * k + j] = r.q[i];
     }
   }
-  sum = wave_sum(sum);
-  if (lane == 0) term[t] = total > 0.f ? sum : NAN;   // NaN: no entry
+  if (lane == 0) term[t] = r.live ? r.term : NAN;   // NaN: no entry
 }
 
 // The live rows in their order, in one block: each wave has a segment, counts it,
@@ -136,54 +98,73 @@ __global__ __launch_bounds__(kLiveThreads) void k_live(const I* __restrict__ tar
   }
 }
 
-// Every row by itself: a live one to its slot of xs (null: not), another's dx to
-// zeros (null: not).  A wave has 512 columns of one.
+struct RowsArgs {
+  const int32_t* slot;
+  const int32_t* id;       // tokens: the target of each row, or null: picked by k_picked
+  float* picked;           // tokens x k, the targets' logits
+  const float* lse;        // tokens, or null: base, scale and g are k_join's
+  const float* dloss;
+  float* base;             // by slot of the call
+  float* scale;
+  float* g;
+  float tau;
+};
+
+// Every row by itself, a wave each: a live one goes to its slot of xs (null: not),
+// its target's logit is the dot product with a row of w; another's dx is zeros.
 template <class T>
-__global__ __launch_bounds__(256) void k_rows(const int32_t* __restrict__ slot, const T* __restrict__ x, int64_t tokens,
-                                              int64_t dim, int32_t slabs, T* __restrict__ xs, T* __restrict__ dx) {
-  const int64_t unit = block_index() * 4 + (threadIdx.x >> 6);
-  const int64_t t = unit / slabs;
-  if (t >= tokens) return;
-  const int64_t c = (unit - t * slabs) * 512 + (threadIdx.x & 63) * 8;
-  if (c >= dim) return;
-  const int32_t s = slot[t];
-  const int cnt = dim - c < 8 ? (int)(dim - c) : 8;
-  float v[8] = {};
-  if (s >= 0) {
-    if (!xs) return;
-    load8(x + t * dim + c, cnt, v);
-    store8(xs + s * dim + c, cnt, v);
-  } else if (dx) {
-    store8(dx + t * dim + c, cnt, v);
+__global__ __launch_bounds__(256) void k_rows(LossArgs a, RowsArgs o, T* __restrict__ xs, T* __restrict__ dx) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = block_index() * 4 + (threadIdx.x >> 6);
+  if (t >= a.tokens) return;
+  const int32_t s = o.slot[t], v = s >= 0 && o.id ? o.id[t] : -1;
+  const T* x = static_cast<const T*>(a.x) + t * a.dim;
+  const T* w = static_cast<const T*>(a.w) + (int64_t)(v < 0 ? 0 : v) * a.dim;
+  if (s < 0) {
+    const float zero[8] = {};
+    if (dx)
+      for (int32_t c = lane * 8; c < a.dim; c += 512) store8(dx + t * a.dim + c, a.dim - c < 8 ? a.dim - c : 8, zero);
+    return;
+  }
+  float sum = 0.f;
+  if (xs || v >= 0) {
+#pragma unroll 4
+    for (int32_t c = lane * 8; c < a.dim; c += 512) {
+      const int cnt = a.dim - c < 8 ? a.dim - c : 8;
+      float p[8], q[8];
+      load8(x + c, cnt, p);
+      load8(w + c, v >= 0 ? cnt : 0, q);
+      if (xs) store8(xs + (int64_t)s * a.dim + c, cnt, p);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += p[i] * q[i];
+    }
+  }
+  if (v >= 0) {
+    sum = wave_sum(sum);
+    if (lane == 0) o.picked[t] = sum;
+  }
+  if (o.lse && lane == 0) {   // exp(-lse) = 2^-base scale, base a whole number
+    const float lse = o.lse[t], base = rintf(lse * kLog2e);
+    o.base[s] = base;
+    o.scale[s] = __builtin_amdgcn_exp2f(-fmaf(lse, kLog2eLow, fmaf(lse, kLog2e, -base)));
+    o.g[s] = o.dloss[t] * o.tau;
   }
 }
 
 // ------------------------------------------------------------------- targets
 
-// The logits of a chunk's targets: a wave has one, picked[slot][j] = <x, w_id>.
+// The logits of a teacher's entries: a wave has one, picked[t][j] = <x, w_id>.
 template <class T>
 __global__ __launch_bounds__(256) void k_picked(LossArgs a, const int32_t* __restrict__ id, int32_t k,
                                                 float* __restrict__ picked) {
   const int lane = threadIdx.x & 63;
-  const int64_t unit = block_index() * 4 + (threadIdx.x >> 6);
-  const int64_t s = unit / k;
-  const int32_t j = (int32_t)(unit - s * k);
-  if (s >= live_slots(a.ch)) return;
-  const int64_t t = a.ch.rows[a.ch.slot0 + s];
-  const int32_t v = id[t * k + j];
+  const int64_t unit = block_index() * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t = unit / k;
+  if (t >= a.tokens) return;
+  const int32_t v = id[unit];
   if (v < 0) return;
-  const T* x = static_cast<const T*>(a.x) + t * a.dim;
-  const T* w = static_cast<const T*>(a.w) + (int64_t)v * a.dim;
-  float sum = 0.f;
-  for (int32_t c = lane * 8; c < a.dim; c += 512) {
-    const int cnt = a.dim - c < 8 ? a.dim - c : 8;
-    float p[8], q[8];
-    load8(x + c, cnt, p);
-    load8(w + c, cnt, q);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sum += p[i] * q[i];
-  }
-  sum = wave_sum(sum);
+  const float sum = row_dot(static_cast<const T*>(a.x) + t * a.dim, static_cast<const T*>(a.w) + (int64_t)v * a.dim,
+                            a.dim, lane);
   if (lane == 0) picked[unit] = sum;
 }
 
@@ -191,69 +172,86 @@ struct JoinArgs {
   const int32_t* id;       // tokens x k
   const float* q;          // tokens x k, or null: 1
   const float* term;       // tokens, or null: 0
-  const float* picked;     // [chunk][k]
+  const float* picked;     // tokens x k
   const float* dloss;      // tokens, or null
-  float* base;             // [chunk], these three: LossArgs; null without gradients
+  float* base;             // [chunk], these three: LossArgs; g null without gradients
   float* scale;
   float* g;
-  float* loss;             // tokens, or null
-  float* lse;              // tokens: written with loss, else read
+  float* loss;             // tokens
+  float* lse;              // tokens
   int32_t k, slabs;
   float tau;
 };
 
-// A row's sum over its slabs, and its loss.  A block has RB slots and 256 / RB
-// groups that go through the slabs side by side.
-template <int RB>
-__global__ __launch_bounds__(256) void k_join(LossArgs a, JoinArgs j) {
-  constexpr int GROUPS = 256 / RB;
-  __shared__ float tops[GROUPS][RB], sums[GROUPS][RB];
-  const int r = threadIdx.x % RB, grp = threadIdx.x / RB;
-  const int64_t s = (int64_t)blockIdx.x * RB + r;
-  const bool exists = s < live_slots(a.ch);
-  float top = -INFINITY, sum = 0.f;
-  if (exists) {
-    for (int32_t i = grp; i < j.slabs; i += GROUPS) {
-      const float* p = a.stats + 2 * ((int64_t)i * a.ch.size + s);
-      const float n = p[0], v = p[1], to = fmaxf(top, n);
-      if (v == 0.f) continue;   // logits of -inf alone
-      sum = sum * __builtin_amdgcn_exp2f(top - to) + v * __builtin_amdgcn_exp2f(n - to);
-      top = to;
+// Rows' sums over their slabs, and their losses.  A block has 16 slots (128 bytes
+// of each slab's pairs) and 64 groups that go through the slabs side by side, then
+// a wave for each slot.  8192 rows of 500 slabs (33 MB): 10 us; one row: 5 us.
+constexpr int kJoinRows = 16;
+__global__ __launch_bounds__(1024) void k_join(LossArgs a, JoinArgs j) {
+  __shared__ float tops[16][kJoinRows + 1], sums[16][kJoinRows + 1];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int32_t live = live_slots(a.ch);
+  const int64_t s0 = (int64_t)blockIdx.x * kJoinRows;
+  if (s0 >= live) return;
+  {
+    const int r = threadIdx.x % kJoinRows;
+    const int64_t s = s0 + r < live ? s0 + r : live - 1;
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    const f32x2* p = reinterpret_cast<const f32x2*>(a.stats) + s;
+    float n = -INFINITY, sum = 0.f;
+    int32_t i = threadIdx.x / kJoinRows;
+    for (; i + 192 < j.slabs; i += 256) {
+      f32x2 v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] = p[(int64_t)(i + 64 * u) * a.ch.size];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) merge_sums(n, sum, v[u][0], v[u][1]);
+    }
+    for (; i < j.slabs; i += 64) {
+      const f32x2 v = p[(int64_t)i * a.ch.size];
+      merge_sums(n, sum, v[0], v[1]);
+    }
+#pragma unroll
+    for (int o = kJoinRows; o < 64; o <<= 1) merge_sums(n, sum, __shfl_xor(n, o, 64), __shfl_xor(sum, o, 64));
+    if (lane < kJoinRows) {
+      tops[w][r] = n;
+      sums[w][r] = sum;
     }
   }
-  tops[grp][r] = top;
-  sums[grp][r] = sum;
   __syncthreads();
-  if (grp || !exists) return;
-  for (int i = 1; i < GROUPS; ++i) top = fmaxf(top, tops[i][r]);
-  sum = 0.f;
-  for (int i = 0; i < GROUPS; ++i)
-    if (sums[i][r] != 0.f) sum += sums[i][r] * __builtin_amdgcn_exp2f(tops[i][r] - top);
+  const int64_t s = s0 + w;
+  if (s >= live) return;
+  float n = tops[lane & 15][w], sum = sums[lane & 15][w];
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) merge_sums(n, sum, __shfl_xor(n, o, 64), __shfl_xor(sum, o, 64));
   const int64_t t = a.ch.rows[a.ch.slot0 + s];
   const float log_sum = logf(sum);
   float off = 0.f;
-  for (int32_t i = 0; i < j.k; ++i)
+  for (int32_t i = lane; i < j.k; i += 64)
     if (j.id[t * j.k + i] >= 0)
-      off += (j.q ? j.q[t * j.k + i] : 1.f) * (log_sum - exponent(a, j.picked[s * j.k + i], top, 0.f) * kLn2);
+      off += (j.q ? j.q[t * j.k + i] : 1.f) * loss_term(a, j.picked[t * j.k + i], n, log_sum);
+  off = wave_sum(off);
+  if (lane) return;
   j.loss[t] = j.tau * j.tau * ((j.term ? j.term[t] : 0.f) + off);
-  j.lse[t] = fmaf(top, kLn2, fmaf(top, kLn2Low, log_sum));
+  j.lse[t] = log_of(n, log_sum);
   if (j.g) {
-    j.base[s] = top;
+    j.base[s] = n;
     j.scale[s] = 1.f / sum;
     j.g[s] = j.dloss[t] * j.tau;
   }
 }
 
-// The same by slot where lse is given.
-__global__ __launch_bounds__(256) void k_given(LossArgs a, JoinArgs j) {
-  const int64_t s = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (s >= live_slots(a.ch)) return;
-  const int64_t t = a.ch.rows[a.ch.slot0 + s];
-  // exp(-lse) = 2^-base scale, base a whole number
-  const float lse = j.lse[t], base = rintf(lse * kLog2e);
-  j.base[s] = base;
-  j.scale[s] = __builtin_amdgcn_exp2f(-fmaf(lse, kLog2eLow, fmaf(lse, kLog2e, -base)));
-  j.g[s] = j.dloss[t] * j.tau;
+// A target's entry of dl: an id that comes more than once counts with the sum of
+// its weights.  All lanes bring the same row and id.
+__device__ __forceinline__ float weight_of(const JoinArgs& j, int64_t t, int32_t v, int lane) {
+  if (!j.q) return 1.f;   // k is 1
+  float q = 0.f;
+  for (int32_t i = lane; i < j.k; i += 64) q += j.id[t * j.k + i] == v ? j.q[t * j.k + i] : 0.f;
+  return wave_sum(q);
+}
+__device__ __forceinline__ float target_entry(const LossArgs& a, float picked, float q, float base, float scale,
+                                              float g) {
+  return (__builtin_amdgcn_exp2f(exponent(a, picked, base, 0.f)) * scale - q) * g;
 }
 
 __device__ __forceinline__ void load_exps(const bf16_t* p, int cnt, float (&v)[8]) {
@@ -270,28 +268,51 @@ __device__ __forceinline__ void load_exps(const bf16_t* p, int cnt, float (&v)[8
 }
 __device__ __forceinline__ void load_exps(const float* p, int cnt, float (&v)[8]) { load8(p, cnt, v); }
 
-// 2^(exponent - n of its slab) into gradients, in place: a wave has 512 columns of
-// a slot.
+// 2^(exponent - n of its slab) into gradients, in place, and the targets' entries:
+// a wave has 1024 columns of a slot.  8192 x 32000 bf16, 1.05 GB: 174 us.
+constexpr int kScaleRuns = 2, kScaleCols = 512 * kScaleRuns;
 template <class T>
-__global__ __launch_bounds__(256) void k_rescale(LossArgs a, int32_t units) {
-  const int64_t unit = block_index() * 4 + (threadIdx.x >> 6);
+__global__ __launch_bounds__(256) void k_rescale(LossArgs a, JoinArgs j, int32_t units) {
+  const int lane = threadIdx.x & 63;
+  const int64_t unit = block_index() * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t s = unit / units;
   if (s >= live_slots(a.ch)) return;
-  const int64_t c = (unit - s * units) * 512 + (threadIdx.x & 63) * 8;
-  if (c >= a.vocab) return;
-  const int cnt = a.vocab - c < 8 ? (int)(a.vocab - c) : 8;
-  const float top = a.stats[2 * (c / Slab<T>::kCols * a.ch.size + s)];
-  const float by = __builtin_amdgcn_exp2f(top - a.base[s]) * (a.scale[s] * a.g[s]);
-  T* p = static_cast<T*>(a.dl) + s * a.dl_ld + c;
-  float v[8];
-  load_exps(p, cnt, v);
+  const int32_t first = (int32_t)(unit - s * units) * kScaleCols;
+  const int64_t t = a.ch.rows[a.ch.slot0 + s];
+  const float base = a.base[s], scale = a.scale[s], g = a.g[s];
+  T* p = static_cast<T*>(a.dl) + s * a.dl_ld;
+  float v[kScaleRuns][8];
+  int cnt[kScaleRuns];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] *= by;
-  store8(p, cnt, v);
+  for (int u = 0; u < kScaleRuns; ++u) {
+    const int32_t c = first + 512 * u + lane * 8, left = a.vocab - c;
+    cnt[u] = left <= 0 ? 0 : left < 8 ? left : 8;
+    load_exps(p + c, cnt[u], v[u]);
+    const float n = cnt[u] ? a.stats[2 * ((int64_t)(c / Slab<T>::kCols) * a.ch.size + s)] : 0.f;
+    const float by = __builtin_amdgcn_exp2f(n - base) * (scale * g);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[u][i] *= by;
+  }
+  for (int32_t j0 = 0; j0 < j.k; j0 += 64) {
+    const int32_t at = j0 + lane;
+    const int32_t id = at < j.k ? j.id[t * j.k + at] : -1;
+    uint64_t hits = __ballot(id >= first && id - first < kScaleCols);
+    while (hits) {
+      const int h = __ffsll((unsigned long long)hits) - 1;
+      hits &= hits - 1;
+      const int32_t e = __builtin_amdgcn_readlane(id, h), c = e - first;
+      const float d = target_entry(a, j.picked[t * j.k + j0 + h], weight_of(j, t, e, lane), base, scale, g);
+#pragma unroll
+      for (int u = 0; u < kScaleRuns; ++u)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[u][i] = c == 512 * u + lane * 8 + i ? d : v[u][i];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kScaleRuns; ++u) store8(p + first + 512 * u + lane * 8, cnt[u], v[u]);
 }
 
-// The targets' entries of dl, a wave a slot.  An id that comes more than once
-// counts with the sum of its weights, which each of them writes.
+// The targets' entries of dl where the logits' gradients are there, a wave a slot.
 template <class T>
 __global__ __launch_bounds__(256) void k_targets(LossArgs a, JoinArgs j) {
   const int lane = threadIdx.x & 63;
@@ -300,22 +321,11 @@ __global__ __launch_bounds__(256) void k_targets(LossArgs a, JoinArgs j) {
   const int64_t t = a.ch.rows[a.ch.slot0 + s];
   const float base = a.base[s], scale = a.scale[s], g = a.g[s];
   T* dl = static_cast<T*>(a.dl) + s * a.dl_ld;
-  for (int32_t j0 = 0; j0 < j.k; j0 += 64) {
-    const int32_t at = j0 + lane;
-    const int32_t v = at < j.k ? j.id[t * j.k + at] : -1;
-    float q = 0.f;
-    for (int32_t i0 = 0; i0 < j.k; i0 += 64) {
-      const int32_t o = i0 + lane;
-      const int32_t id = o < j.k ? j.id[t * j.k + o] : -1;
-      const float weight = o < j.k ? (j.q ? j.q[t * j.k + o] : 1.f) : 0.f;
-      const int n = j.k - i0 < 64 ? j.k - i0 : 64;
-      for (int i = 0; i < n; ++i) {
-        const int32_t other = __builtin_amdgcn_readlane(id, i);
-        const float add = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(weight), i));
-        q += other == v ? add : 0.f;
-      }
-    }
-    if (v >= 0) store1(dl + v, (__builtin_amdgcn_exp2f(exponent(a, j.picked[s * j.k + at], base, 0.f)) * scale - q) * g);
+  for (int32_t i = 0; i < j.k; ++i) {
+    const int32_t v = __builtin_amdgcn_readfirstlane(j.id[t * j.k + i]);
+    if (v < 0) continue;
+    const float d = target_entry(a, j.picked[t * j.k + i], weight_of(j, t, v, lane), base, scale, g);
+    if (lane == 0) store1(dl + v, d);
   }
 }
 
@@ -355,22 +365,31 @@ int64_t chunk_slots(int dtype, int64_t tokens, int64_t vocab, bool grads, bool s
 }
 
 struct LossSpace {
+  bool few;
   int64_t chunk, slabs, dl_ld;
-  int parts;
-  uint64_t xs, dx_parts, id, q, term, rows, slot, count, stats, picked, base, scale, g, dl, sums, bytes;
+  ProductParts parts;
+  uint64_t xs, sums_of_parts, id, q, term, rows, slot, count, stats, picked, base, scale, g, dl, sums, bytes;
 };
 LossSpace loss_space(int dtype, int64_t tokens, int64_t vocab, int64_t dim, int k, bool teacher, bool grads,
                      bool given) {
   Pieces p;
-  LossSpace l;
+  LossSpace l = {};
+  if (!grads && few_rows(dtype, tokens, dim)) {
+    l.few = true;
+    l.stats = p.take((uint64_t)few_blocks(vocab) * tokens * 8);
+    l.bytes = p.used;
+    return l;
+  }
   const int64_t es = dtype == MUON_BF16 ? 2 : 4;
   l.chunk = chunk_slots(dtype, tokens, vocab, grads, !given);
   l.slabs = ceil_div(vocab, slab_cols(dtype));
   l.dl_ld = ceil_div(vocab, 64) * 64;
   const bool large = large_sizes(dtype, tokens, vocab, dim);
-  l.parts = large && grads ? dx_parts(l.chunk, vocab, dim) : 1;
+  l.parts = grads ? product_parts(dtype, l.chunk, vocab, dim, large) : ProductParts{1, 1};
   l.xs = p.take(large ? (uint64_t)tokens * dim * 2 : 0);
-  l.dx_parts = p.take(l.parts > 1 ? (uint64_t)l.parts * l.chunk * dim * 4 : 0);
+  const uint64_t of_dx = l.parts.dx > 1 ? (uint64_t)l.parts.dx * l.chunk * dim * 4 : 0;
+  const uint64_t of_dw = l.parts.dw > 1 ? (uint64_t)l.parts.dw * vocab * dim * 4 : 0;
+  l.sums_of_parts = p.take(of_dx > of_dw ? of_dx : of_dw);   // one after the other
   l.id = p.take((uint64_t)tokens * k * 4);
   l.q = p.take(teacher ? (uint64_t)tokens * k * 4 : 0);
   l.term = p.take(teacher ? (uint64_t)tokens * 4 : 0);
@@ -378,10 +397,10 @@ LossSpace loss_space(int dtype, int64_t tokens, int64_t vocab, int64_t dim, int 
   l.slot = p.take((uint64_t)tokens * 4);
   l.count = p.take(4);
   l.stats = p.take(given ? 0 : (uint64_t)l.slabs * l.chunk * 8);
-  l.picked = p.take((uint64_t)l.chunk * k * 4);
-  l.base = p.take((uint64_t)l.chunk * 4);
-  l.scale = p.take((uint64_t)l.chunk * 4);
-  l.g = p.take((uint64_t)l.chunk * 4);
+  l.picked = p.take((uint64_t)tokens * k * 4);
+  l.base = p.take((uint64_t)tokens * 4);
+  l.scale = p.take((uint64_t)tokens * 4);
+  l.g = p.take((uint64_t)tokens * 4);
   l.dl = p.take(grads ? (uint64_t)l.chunk * l.dl_ld * es : 0);
   l.sums = p.take(grads && l.chunk < tokens ? (uint64_t)vocab * dim * 4 : 0);
   l.bytes = p.used;
@@ -420,16 +439,8 @@ template <class T>
 int run(const Call& c, const LossSpace& l, char* ws, hipStream_t s) {
   const bool grads = c.dw != nullptr, given = c.lse_in != nullptr;
   int rc;
-  if ((rc = c.index_bytes == 8 ? find_rows<int64_t>(c, l, ws, s) : find_rows<int32_t>(c, l, ws, s))) return rc;
   const bool large = large_sizes(c.dtype, c.tokens, c.vocab, c.dim) && aligned16(c.w) &&
                      (!grads || (aligned16(c.dx) && aligned16(c.dw)));
-  if (c.tokens && (grads || large)) {
-    const int64_t slabs = ceil_div(c.dim, 512);
-    hipLaunchKernelGGL((k_rows<T>), grid_of_blocks(ceil_div(c.tokens * slabs, 4), 256), dim3(256), 0, s,
-                       reinterpret_cast<int32_t*>(ws + l.slot), static_cast<const T*>(c.x), c.tokens, c.dim,
-                       (int32_t)slabs, large ? reinterpret_cast<T*>(ws + l.xs) : nullptr,
-                       grads ? static_cast<T*>(c.dx) : nullptr);
-  }
   LossArgs a = {};
   a.ch.rows = reinterpret_cast<int32_t*>(ws + l.rows);
   a.ch.count = reinterpret_cast<int32_t*>(ws + l.count);
@@ -441,61 +452,67 @@ int run(const Call& c, const LossSpace& l, char* ws, hipStream_t s) {
   a.dim = (int32_t)c.dim;
   a.xs = large ? ws + l.xs : nullptr;
   a.dl_ld = l.dl_ld;
-  a.dx_parts = reinterpret_cast<float*>(ws + l.dx_parts);
+  a.sums_of_parts = reinterpret_cast<float*>(ws + l.sums_of_parts);
   a.parts = l.parts;
   const double to_log2 = 1.4426950408889634 / (double)c.tau;
   a.to_log2 = (float)to_log2;
   a.to_log2_low = (float)(to_log2 - (double)a.to_log2);
   a.stats = given ? nullptr : reinterpret_cast<float*>(ws + l.stats);
-  a.base = reinterpret_cast<float*>(ws + l.base);
-  a.scale = reinterpret_cast<float*>(ws + l.scale);
-  a.g = reinterpret_cast<float*>(ws + l.g);
   a.dl = grads ? ws + l.dl : nullptr;
   a.dx = c.dx;
   a.dw = c.dw;
   a.sums = l.chunk < c.tokens ? reinterpret_cast<float*>(ws + l.sums) : nullptr;
-  JoinArgs j = {};
-  j.id = reinterpret_cast<int32_t*>(ws + l.id);
-  j.q = c.teacher ? reinterpret_cast<float*>(ws + l.q) : nullptr;
-  j.term = c.teacher ? reinterpret_cast<float*>(ws + l.term) : nullptr;
-  j.picked = reinterpret_cast<float*>(ws + l.picked);
-  j.dloss = c.dloss;
-  j.base = reinterpret_cast<float*>(ws + l.base);
-  j.scale = reinterpret_cast<float*>(ws + l.scale);
-  j.g = grads ? reinterpret_cast<float*>(ws + l.g) : nullptr;
-  j.loss = c.loss;
-  j.lse = given ? const_cast<float*>(c.lse_in) : c.lse;
-  j.k = c.k;
-  j.slabs = (int32_t)l.slabs;
-  j.tau = c.tau;
+  if (l.few)
+    return few_loss(a, c.dtype, FewCall{c.targets, c.index_bytes, c.teacher, c.teacher_dtype, c.k, c.tau, c.loss, c.lse},
+                    s);
+  if ((rc = c.index_bytes == 8 ? find_rows<int64_t>(c, l, ws, s) : find_rows<int32_t>(c, l, ws, s))) return rc;
   if (!c.tokens) {   // no rows: dw is zeros
     a.first = a.last = true;
     return grads ? dw_product(a, c.dtype, s) : MUON_OK;
   }
-  const int64_t chunks = ceil_div(c.tokens, l.chunk);
+  float* base = reinterpret_cast<float*>(ws + l.base);
+  float* scale = reinterpret_cast<float*>(ws + l.scale);
+  float* g = reinterpret_cast<float*>(ws + l.g);
+  float* picked = reinterpret_cast<float*>(ws + l.picked);
+  const int32_t* id = reinterpret_cast<int32_t*>(ws + l.id);
+  RowsArgs o = {reinterpret_cast<int32_t*>(ws + l.slot), c.k == 1 ? id : nullptr, picked, c.lse_in, c.dloss, base, scale,
+                g, c.tau};
+  hipLaunchKernelGGL((k_rows<T>), grid_of_blocks(ceil_div(c.tokens, 4), 256), dim3(256), 0, s, a, o,
+                     large ? reinterpret_cast<T*>(ws + l.xs) : nullptr, grads ? static_cast<T*>(c.dx) : nullptr);
+  if (c.k > 1)
+    hipLaunchKernelGGL((k_picked<T>), grid_of_blocks(ceil_div(c.tokens * c.k, 4), 256), dim3(256), 0, s, a, id, c.k,
+                       picked);
+  JoinArgs j = {};
+  j.id = id;
+  j.q = c.teacher ? reinterpret_cast<float*>(ws + l.q) : nullptr;
+  j.term = c.teacher ? reinterpret_cast<float*>(ws + l.term) : nullptr;
+  j.picked = picked;
+  j.dloss = c.dloss;
+  j.loss = c.loss;
+  j.lse = c.lse;
+  j.k = c.k;
+  j.slabs = (int32_t)l.slabs;
+  j.tau = c.tau;
+  const int64_t chunks = ceil_div(c.tokens, l.chunk), slots = l.chunk;
   for (int64_t i = 0; i < chunks; ++i) {
     a.ch.slot0 = i * l.chunk;
     a.first = i == 0;
     a.last = i + 1 == chunks;
-    const int64_t slots = l.chunk;
-    hipLaunchKernelGGL((k_picked<T>), grid_of_blocks(ceil_div(slots * c.k, 4), 256), dim3(256), 0, s, a, j.id, c.k,
-                       reinterpret_cast<float*>(ws + l.picked));
+    a.base = j.base = base + a.ch.slot0;
+    a.scale = j.scale = scale + a.ch.slot0;
+    a.g = g + a.ch.slot0;
+    j.g = grads ? g + a.ch.slot0 : nullptr;
+    if ((rc = logits_product(a, c.dtype, given ? kGradient : grads ? kStatsExp : kStats, s))) return rc;
+    if (!given) hipLaunchKernelGGL(k_join, dim3((uint32_t)ceil_div(slots, kJoinRows)), dim3(1024), 0, s, a, j);
+    if (!grads) continue;
     if (given) {
-      hipLaunchKernelGGL(k_given, dim3((uint32_t)ceil_div(slots, 256)), dim3(256), 0, s, a, j);
-      if ((rc = logits_product(a, c.dtype, kGradient, s))) return rc;
+      hipLaunchKernelGGL((k_targets<T>), grid_of_blocks(ceil_div(slots, 4), 256), dim3(256), 0, s, a, j);
     } else {
-      if ((rc = logits_product(a, c.dtype, grads ? kStatsExp : kStats, s))) return rc;
-      if (slots <= 4) hipLaunchKernelGGL((k_join<1>), dim3((uint32_t)slots), dim3(256), 0, s, a, j);
-      else hipLaunchKernelGGL((k_join<32>), dim3((uint32_t)ceil_div(slots, 32)), dim3(256), 0, s, a, j);
-      if (grads) {
-        const int64_t units = ceil_div(c.vocab, 512);
-        hipLaunchKernelGGL((k_rescale<T>), grid_of_blocks(ceil_div(slots * units, 4), 256), dim3(256), 0, s, a,
-                           (int32_t)units);
-      }
+      const int64_t units = ceil_div(c.vocab, kScaleCols);
+      hipLaunchKernelGGL((k_rescale<T>), grid_of_blocks(ceil_div(slots * units, 4), 256), dim3(256), 0, s, a, j,
+                         (int32_t)units);
     }
     if ((rc = launch_status("classifier loss launch"))) return rc;
-    if (!grads) continue;
-    hipLaunchKernelGGL((k_targets<T>), grid_of_blocks(ceil_div(slots, 4), 256), dim3(256), 0, s, a, j);
     if ((rc = dx_product(a, c.dtype, s)) || (rc = dw_product(a, c.dtype, s))) return rc;
   }
   return launch_status("classifier loss launch");

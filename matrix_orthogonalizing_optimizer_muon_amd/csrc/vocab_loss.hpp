@@ -22,6 +22,12 @@ struct Chunk {
   int32_t size;            // slots a chunk can hold: rows of stats and of dl
 };
 
+// Parts into which the long sums of dx (over the vocabulary) and dw (over the rows)
+// are cut.
+struct ProductParts {
+  int32_t dx, dw;
+};
+
 struct LossArgs {
   Chunk ch;
   const void* x;           // tokens x dim
@@ -43,11 +49,15 @@ struct LossArgs {
   // gradients
   void* dx;                // tokens x dim
   void* dw;                // vocab x dim
-  float* dx_parts;         // [part][chunk][dim]: sums of parts of the vocabulary, where there are more than one
-  int32_t parts;
+  ProductParts parts;
+  float* sums_of_parts;    // [part][chunk][dim] of dx, then [part][vocab][dim] of dw, where there are more than one
   float* sums;             // vocab x dim: of the chunks so far, or null where there is one
   bool first, last;        // chunk
 };
+
+// log2(e) and ln 2, each in two parts
+constexpr float kLog2e = 1.4426950408889634f, kLog2eLow = (float)(1.4426950408889634 - (double)kLog2e);
+constexpr float kLn2 = 0.6931471805599453f, kLn2Low = (float)(0.6931471805599453 - (double)kLn2);
 
 __device__ __forceinline__ int32_t live_slots(const Chunk& c) {
   const int64_t left = *c.count - c.slot0;
@@ -63,6 +73,84 @@ __device__ __forceinline__ float exponent(const LossArgs& a, float l, float n, b
 __device__ __forceinline__ float whole_exponent(const LossArgs& a, float top) {
   return top == -INFINITY ? 0.f : ceilf(top * a.to_log2);
 }
+
+// Joins two sums of 2^(exponent - n) with their n; a sum of zero (exponents of -inf
+// alone) has none.
+__device__ __forceinline__ void merge_sums(float& n, float& sum, float n2, float sum2) {
+  if (sum2 == 0.f) n2 = -INFINITY;
+  const float to = fmaxf(n, n2), base = to == -INFINITY ? 0.f : to;
+  sum = sum * __builtin_amdgcn_exp2f(n - base) + sum2 * __builtin_amdgcn_exp2f(n2 - base);
+  n = to;
+}
+// The log of sum 2^n, from that of sum; and lse - l / tau of a logit.
+__device__ __forceinline__ float log_of(float n, float log_sum) { return fmaf(n, kLn2, fmaf(n, kLn2Low, log_sum)); }
+__device__ __forceinline__ float loss_term(const LossArgs& a, float l, float n, float log_sum) {
+  return log_sum - exponent(a, l, n, 0.f) * kLn2;
+}
+
+// <x, w> of two rows, by a wave.
+template <class T>
+__device__ __forceinline__ float row_dot(const T* x, const T* w, int32_t dim, int lane) {
+  float sum = 0.f;
+#pragma unroll 4
+  for (int32_t c = lane * 8; c < dim; c += 512) {
+    const int cnt = dim - c < 8 ? dim - c : 8;
+    float p[8], q[8];
+    load8(x + c, cnt, p);
+    load8(w + c, cnt, q);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += p[i] * q[i];
+  }
+  return wave_sum(sum);
+}
+
+// A teacher's entries of a row, lane l those of l + 64 i: ids, -1 where there is
+// none (an id outside the vocabulary, a logit of -inf or NaN), the softmax of their
+// logits over tau, and the sum of q log q.
+struct TeacherRow {
+  static constexpr int N = kMaxTeacher / 64;
+  int32_t at[N];
+  float q[N];
+  float term;
+  bool live;
+  template <class TT, class I>
+  __device__ __forceinline__ void read(const TT* teacher, const I* ids, int32_t k, int32_t vocab, float inv_tau,
+                                       int lane) {
+    float v[N], top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int j = lane + 64 * i;
+      at[i] = -1;
+      v[i] = -INFINITY;
+      if (j < k) {
+        at[i] = read_index(ids, j, vocab);
+        const float l = to_f32(teacher[j]);
+        if (!(l > -INFINITY)) at[i] = -1;
+        if (at[i] >= 0) v[i] = fminf(l, 3.402823466e38f);
+      }
+      top = fmaxf(top, v[i]);
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+    float total = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      v[i] = at[i] >= 0 ? (v[i] - top) * inv_tau : 0.f;
+      q[i] = at[i] >= 0 ? expf(v[i]) : 0.f;
+      total += q[i];
+    }
+    total = wave_sum(total);
+    live = total > 0.f;
+    const float log_total = live ? logf(total) : 0.f;
+    term = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      q[i] = at[i] >= 0 ? q[i] / total : 0.f;
+      if (q[i] > 0.f) term += q[i] * (v[i] - log_total);
+    }
+    term = wave_sum(term);
+  }
+};
 
 // 2^(exponent - n) of a slab's n, between the first product and k_rescale.
 // In 16 bits: no sign and seven bits of the exponent, which values up to 1 do
@@ -96,7 +184,23 @@ inline int slab_cols(int dtype) { return dtype == MUON_BF16 ? Slab<bf16_t>::kCol
 inline bool large_sizes(int dtype, int64_t tokens, int64_t vocab, int64_t dim) {
   return dtype == MUON_BF16 && dim % 8 == 0 && vocab < (1 << 21) && dim < (1 << 21) && tokens > 0;
 }
-int dx_parts(int64_t tokens, int64_t vocab, int64_t dim);
+ProductParts product_parts(int dtype, int64_t tokens, int64_t vocab, int64_t dim, bool large);
+
+// Losses of few rows without gradients: whether vocab_few.hip takes them, and its
+// blocks, each of which has a pair for every row in stats.
+struct FewCall {
+  const void* ids;
+  int index_bytes;
+  const void* teacher;     // or null
+  int teacher_dtype;
+  int32_t k;
+  float tau;
+  float* loss;
+  float* lse;
+};
+bool few_rows(int dtype, int64_t tokens, int64_t dim);
+int64_t few_blocks(int64_t vocab);
+int few_loss(const LossArgs& a, int dtype, const FewCall& c, hipStream_t s);
 
 // The products, of one chunk.
 int logits_product(const LossArgs& a, int dtype, Epilogue e, hipStream_t s);

@@ -68,20 +68,21 @@ __global__ __launch_bounds__(256) void k_tile(LossArgs a, int32_t tiles_n) {
     K = a.dim;
     sp.init(a.x, rows, m0, m_left, a.tokens, 0, a.dim);
     sq.init(a.w, nullptr, n0, a.vocab - n0, 0, 0, a.dim);
-  } else if constexpr (PRODUCT == kDx) {
-    m_left = live - m0;
-    if (m_left <= 0) return;
-    K = a.vocab;
-    sp.init(a.dl, nullptr, m0, m_left, 0, 0, a.vocab);
-    sp.ld = a.dl_ld;
-    sq.init(a.w, nullptr, 0, K, 0, n0, a.dim);
   } else {
-    m_left = a.vocab - m0;
+    m_left = (PRODUCT == kDx ? live : a.vocab) - m0;
     if (m_left <= 0) return;
-    K = live;
-    sp.init(a.dl, nullptr, 0, K, 0, (int32_t)m0, a.vocab);
+    // this block's part of the sum, of whole k-tiles
+    const int32_t all = PRODUCT == kDx ? a.vocab : live, parts = PRODUCT == kDx ? a.parts.dx : a.parts.dw;
+    const int64_t part = ((int64_t)all + parts * G::BK - 1) / (parts * G::BK) * G::BK, k0 = part * blockIdx.z;
+    K = (int32_t)(all - k0 < 0 ? 0 : all - k0 < part ? all - k0 : part);
+    if constexpr (PRODUCT == kDx) {
+      sp.init(static_cast<const T*>(a.dl) + k0, nullptr, m0, m_left, 0, 0, K);
+      sq.init(a.w, nullptr, k0, K, 0, n0, a.dim);
+    } else {
+      sp.init(a.dl, nullptr, k0, K, 0, (int32_t)m0, a.vocab);
+      sq.init(a.x, rows, k0, K, a.tokens, n0, a.dim);
+    }
     sp.ld = a.dl_ld;
-    sq.init(a.x, rows, 0, K, a.tokens, n0, a.dim);
   }
   f32x16_t acc[NT][NT];
 #pragma unroll
@@ -183,21 +184,23 @@ __global__ __launch_bounds__(256) void k_tile(LossArgs a, int32_t tiles_n) {
         }
       }
     } else if (exists) {
-      const int64_t at = (PRODUCT == kDx ? (int64_t)rows[r] : r) * a.dim;
+      constexpr bool DX = PRODUCT == kDx;
+      const bool whole = (DX ? a.parts.dx : a.parts.dw) == 1;
+      const int64_t at = (DX && whole ? (int64_t)rows[r] : r) * a.dim;
+      float* sums = whole ? a.sums : a.sums_of_parts + (int64_t)blockIdx.z * (DX ? a.ch.size : a.vocab) * a.dim;
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int32_t c = c0 + 32 * j + 8 * q;
           float v[4] = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-          if (PRODUCT == kDw && !a.first) {
-            const u32x4 before = load16(a.sums + at + c, a.dim - c);
+          if (!DX && whole && !a.first) {
+            const u32x4 before = load16(sums + at + c, a.dim - c);
 #pragma unroll
             for (int u = 0; u < 4; ++u) v[u] += __uint_as_float(before[u]);
           }
-          if (PRODUCT == kDx) store4(static_cast<T*>(a.dx) + at + c, a.dim - c, v);
-          else if (a.last) store4(static_cast<T*>(a.dw) + at + c, a.dim - c, v);
-          else store4(a.sums + at + c, a.dim - c, v);
+          if (whole && (DX || a.last)) store4(static_cast<T*>(DX ? a.dx : a.dw) + at + c, a.dim - c, v);
+          else store4(sums + at + c, a.dim - c, v);
         }
     }
   }
@@ -321,19 +324,21 @@ struct GradWalk {
     const int64_t k = (int64_t)t.k0 * kBK;
     if (kX)
       return Panel{dl + (t.m0 * a.dl_ld + k) * 2, (uint32_t)a.dl_ld * 2u, live - t.m0, (int32_t)(a.dl_ld - k)};
-    return Panel{dl + t.m0 * 2ll, (uint32_t)a.dl_ld * 2u, (int32_t)a.dl_ld - t.m0, live};
+    return Panel{dl + (k * a.dl_ld + t.m0) * 2, (uint32_t)a.dl_ld * 2u, (int32_t)a.dl_ld - t.m0, (int32_t)(live - k)};
   }
   __device__ __forceinline__ Panel q(const OutTile& t) const {
     const int64_t k = (int64_t)t.k0 * kBK;
     const char* from = kX ? static_cast<const char*>(a.w) + k * a.dim * 2
-                          : static_cast<const char*>(a.xs) + a.ch.slot0 * a.dim * 2;
+                          : static_cast<const char*>(a.xs) + (a.ch.slot0 + k) * a.dim * 2;
     return Panel{from + t.n0 * 2ll, (uint32_t)a.dim * 2u, a.dim - t.n0, (int32_t)((kX ? a.vocab : live) - k)};
   }
   __device__ __forceinline__ int store(Acc& acc, const OutTile& t, int mt, int row0, int col0, MUON_LDS char* buf,
                                        int lane) const {
     const int32_t c0 = t.n0 + col0, m = rows() - t.m0;
-    if (kX ? a.parts > 1 : a.sums != nullptr) {   // sums: of a part, or of the chunks so far
-      float* out = kX ? a.dx_parts + ((int64_t)t.part * a.ch.size + t.m0) * a.dim : a.sums + (int64_t)t.m0 * a.dim;
+    const bool parts = (kX ? a.parts.dx : a.parts.dw) > 1;
+    if (parts || (!kX && a.sums)) {   // sums: of a part, or of the chunks so far
+      float* out = parts ? a.sums_of_parts + ((int64_t)t.part * (kX ? a.ch.size : a.vocab) + t.m0) * a.dim
+                         : a.sums + (int64_t)t.m0 * a.dim;
       bf16_t* dw = static_cast<bf16_t*>(a.dw) + (int64_t)t.m0 * a.dim;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -350,12 +355,12 @@ struct GradWalk {
             const int q = row0 + 32 * i + u * 8 + lane / 8, c = c0 + 32 * j + 4 * (lane & 7);
             if (q >= m || c >= a.dim) continue;
             const int64_t at = (int64_t)q * a.dim + c;
-            if (!kX && !a.first) {
+            if (!kX && !parts && !a.first) {
               const u32x4 before = *reinterpret_cast<const u32x4*>(out + at);
 #pragma unroll
               for (int x = 0; x < 4; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) + __uint_as_float(before[x]));
             }
-            if (!kX && a.last)
+            if (!kX && !parts && a.last)
               *reinterpret_cast<u32x2*>(dw + at) =
                   u32x2{pack2(__uint_as_float(v[0]), __uint_as_float(v[1])), pack2(__uint_as_float(v[2]), __uint_as_float(v[3]))};
             else
@@ -402,27 +407,35 @@ __global__ __launch_bounds__(512, 2) void k_grad(LossArgs a) {
   __shared__ __attribute__((aligned(16))) char lds[GradWalk<PRODUCT>::Sh::LDS];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   GradWalk<PRODUCT> o{a, {}, __builtin_amdgcn_readfirstlane(live_slots(a.ch))};
-  if (PRODUCT == kDx) o.walk.init(o.live, a.dim, a.vocab, (uint32_t)a.parts);
-  else o.walk.init(a.vocab, a.dim, o.live, 1);
+  if (PRODUCT == kDx) o.walk.init(o.live, a.dim, a.vocab, (uint32_t)a.parts.dx);
+  else o.walk.init(a.vocab, a.dim, o.live, (uint32_t)a.parts.dw);
   walk_tiles(lds, lane, w, o);
 }
 
-// The parts' sums of dx, in their order, to the rows where they belong: a wave has
-// 512 columns of a slot.
-__global__ __launch_bounds__(256) void k_dx_join(LossArgs a, int32_t units) {
+// The parts' sums, in their order: a wave has 512 columns of a slot of dx, which
+// goes to its row, or of a row of dw, which goes on from the chunks before.
+template <class T, int PRODUCT>
+__global__ __launch_bounds__(256) void k_add(LossArgs a, int32_t units) {
+  constexpr bool DX = PRODUCT == kDx;
   const int64_t unit = block_index() * 4 + (threadIdx.x >> 6);
   const int64_t s = unit / units;
-  if (s >= live_slots(a.ch)) return;
+  if (s >= (DX ? live_slots(a.ch) : a.vocab)) return;
   const int64_t c = (unit - s * units) * 512 + (threadIdx.x & 63) * 8;
   if (c >= a.dim) return;
+  const int cnt = a.dim - c < 8 ? (int)(a.dim - c) : 8, parts = DX ? a.parts.dx : a.parts.dw;
+  const int64_t size = (int64_t)(DX ? a.ch.size : a.vocab) * a.dim, at = s * a.dim + c;
   float sum[8] = {};
-  for (int32_t p = 0; p < a.parts; ++p) {
+  if (!DX && !a.first) load8(a.sums + at, cnt, sum);
+#pragma unroll 4
+  for (int32_t p = 0; p < parts; ++p) {
     float v[8];
-    load8(a.dx_parts + ((int64_t)p * a.ch.size + s) * a.dim + c, 8, v);
+    load8(a.sums_of_parts + p * size + at, cnt, v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum[i] += v[i];
   }
-  store8(static_cast<bf16_t*>(a.dx) + (int64_t)a.ch.rows[a.ch.slot0 + s] * a.dim + c, 8, sum);
+  if (DX) store8(static_cast<T*>(a.dx) + (int64_t)a.ch.rows[a.ch.slot0 + s] * a.dim + c, cnt, sum);
+  else if (a.last) store8(static_cast<T*>(a.dw) + at, cnt, sum);
+  else store8(a.sums + at, cnt, sum);
 }
 
 template <int EPI>
@@ -432,20 +445,63 @@ int launch_logits_large(const LossArgs& a, hipStream_t s) {
 }
 
 template <class T, int PRODUCT, int EPI>
-int launch_tile(const LossArgs& a, int64_t m, int64_t n, hipStream_t s) {
+int launch_tile(const LossArgs& a, int64_t m, int64_t n, int parts, hipStream_t s) {
   const int64_t tiles_n = ceil_div(n, Tile<T>::B), blocks = ceil_div(m, Tile<T>::B) * tiles_n;
-  hipLaunchKernelGGL((k_tile<T, PRODUCT, EPI>), grid_of_blocks(blocks, 256), dim3(256), 0, s, a, (int32_t)tiles_n);
+  hipLaunchKernelGGL((k_tile<T, PRODUCT, EPI>), grid_of_blocks(blocks, 256, (uint32_t)parts), dim3(256), 0, s, a,
+                     (int32_t)tiles_n);
   return launch_status("classifier product launch");
 }
 
 template <class T>
 int launch_logits(const LossArgs& a, Epilogue e, hipStream_t s) {
-  if (e == kStats) return launch_tile<T, kLogits, kStats>(a, a.ch.size, a.vocab, s);
-  if (e == kStatsExp) return launch_tile<T, kLogits, kStatsExp>(a, a.ch.size, a.vocab, s);
-  return launch_tile<T, kLogits, kGradient>(a, a.ch.size, a.vocab, s);
+  if (e == kStats) return launch_tile<T, kLogits, kStats>(a, a.ch.size, a.vocab, 1, s);
+  if (e == kStatsExp) return launch_tile<T, kLogits, kStatsExp>(a, a.ch.size, a.vocab, 1, s);
+  return launch_tile<T, kLogits, kGradient>(a, a.ch.size, a.vocab, 1, s);
+}
+
+template <class T, int PRODUCT>
+int launch_grad(const LossArgs& a, hipStream_t s) {
+  const int64_t m = PRODUCT == kDx ? a.ch.size : a.vocab, units = ceil_div(a.dim, 512);
+  const int parts = PRODUCT == kDx ? a.parts.dx : a.parts.dw;
+  if (a.xs) {
+    hipLaunchKernelGGL((k_grad<PRODUCT>), dim3(kWalkers), dim3(512), 0, s, a);
+  } else {
+    const int rc = launch_tile<T, PRODUCT, kStats>(a, m, a.dim, parts, s);
+    if (rc) return rc;
+  }
+  if (parts > 1)
+    hipLaunchKernelGGL((k_add<T, PRODUCT>), grid_of_blocks(ceil_div(m * units, 4), 256), dim3(256), 0, s, a,
+                       (int32_t)units);
+  return launch_status("classifier product launch");
+}
+
+// Parts of a sum over k for the outputs of m x n: `at_once` tiles of b run side by
+// side, so a part more brings the last round's idle ones work and costs 8 bytes an
+// output (written and read, 4 TB/s).  us: what a k-tile takes one of them.
+int parts_of(int64_t m, int64_t n, int64_t k, int64_t b, int64_t k_tile, int at_once, double us) {
+  const double tiles = (double)ceil_div(m, b) * ceil_div(n, b), k_tiles = (double)ceil_div(k, k_tile);
+  int best = 1;
+  double least = 0;
+  for (int p = 1; p <= 64 && (p == 1 || k_tiles >= 8.0 * p); ++p) {
+    const double cost = ceil(tiles * p / at_once) * ceil(k_tiles / p) * us +
+                        (p > 1 ? 4 + p * (double)m * n * 8 / 4e6 : 0);
+    if (p == 1 || cost < least) {
+      least = cost;
+      best = p;
+    }
+  }
+  return best;
 }
 
 }  // namespace
+
+ProductParts product_parts(int dtype, int64_t tokens, int64_t vocab, int64_t dim, bool large) {
+  const bool bf16 = dtype == MUON_BF16;
+  const int64_t b = large ? 256 : bf16 ? Tile<bf16_t>::B : Tile<float>::B, k = bf16 ? kBK : Tile<float>::BK;
+  const int at_once = large ? kWalkers : 2 * kWalkers;
+  const double us = large ? 1.7 : 2;
+  return ProductParts{parts_of(tokens, dim, vocab, b, k, at_once, us), parts_of(vocab, dim, tokens, b, k, at_once, us)};
+}
 
 int logits_product(const LossArgs& a, int dtype, Epilogue e, hipStream_t s) {
   if (a.xs) {
@@ -455,46 +511,12 @@ int logits_product(const LossArgs& a, int dtype, Epilogue e, hipStream_t s) {
   return dtype == MUON_BF16 ? launch_logits<bf16_t>(a, e, s) : launch_logits<float>(a, e, s);
 }
 
-// Parts of the vocabulary whose sums a dx of at most `tokens` rows is made of: 256
-// walkers share the tiles of all parts, so a part more brings the last round's
-// walkers work and costs 8 bytes an element of dx (written and read).  A k-tile
-// takes a walker about 1.7 us; those bytes go at 4 TB/s.
-int dx_parts(int64_t tokens, int64_t vocab, int64_t dim) {
-  const double tiles = (double)ceil_div(tokens, 256) * ceil_div(dim, 256), k_tiles = (double)ceil_div(vocab, kBK);
-  int best = 1;
-  double least = 0;
-  for (int p = 1; p <= 32 && k_tiles >= 8.0 * p; ++p) {
-    const double rounds = ceil(tiles * p / kWalkers), us = rounds * ceil(k_tiles / p) * 1.7 +
-                          (p > 1 ? 4 + p * (double)tokens * dim * 8 / 4e6 : 0);
-    if (p == 1 || us < least) {
-      least = us;
-      best = p;
-    }
-  }
-  return best;
-}
-
 int dx_product(const LossArgs& a, int dtype, hipStream_t s) {
-  if (a.xs) {
-    hipLaunchKernelGGL((k_grad<kDx>), dim3(kWalkers), dim3(512), 0, s, a);
-    if (a.parts > 1) {
-      const int64_t units = ceil_div(a.dim, 512);
-      hipLaunchKernelGGL(k_dx_join, grid_of_blocks(ceil_div(a.ch.size * units, 4), 256), dim3(256), 0, s, a,
-                         (int32_t)units);
-    }
-    return launch_status("classifier product launch");
-  }
-  return dtype == MUON_BF16 ? launch_tile<bf16_t, kDx, kStats>(a, a.ch.size, a.dim, s)
-                            : launch_tile<float, kDx, kStats>(a, a.ch.size, a.dim, s);
+  return dtype == MUON_BF16 ? launch_grad<bf16_t, kDx>(a, s) : launch_grad<float, kDx>(a, s);
 }
 
 int dw_product(const LossArgs& a, int dtype, hipStream_t s) {
-  if (a.xs) {
-    hipLaunchKernelGGL((k_grad<kDw>), dim3(kWalkers), dim3(512), 0, s, a);
-    return launch_status("classifier product launch");
-  }
-  return dtype == MUON_BF16 ? launch_tile<bf16_t, kDw, kStats>(a, a.vocab, a.dim, s)
-                            : launch_tile<float, kDw, kStats>(a, a.vocab, a.dim, s);
+  return dtype == MUON_BF16 ? launch_grad<bf16_t, kDw>(a, s) : launch_grad<float, kDw>(a, s);
 }
 
 }  // namespace vo

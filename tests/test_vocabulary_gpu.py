@@ -54,7 +54,7 @@ def close(got, want, bound, what):
 # ------------------------------------------------------------------- embedding
 
 EMBED = [(1, 1, 1), (1, 1000, 64), (3, 7, 33), (64, 5, 520), (65, 5, 8), (200, 300, 136), (1000, 3, 17),
-         (1025, 40000, 24), (777, 129, 1031), (4099, 513, 512)]
+         (1025, 40000, 24), (777, 129, 1031), (4099, 513, 512), (20000, 700, 8), (300, 140000, 16)]
 
 
 def tokens_of(n, vocab, seed, index=J, absent=0.1):
@@ -137,7 +137,7 @@ def test_embed_passes_values_on():
 
 SIZES = [(1, 1, 1), (1, 16, 16), (1, 1000, 64), (5, 33, 7), (17, 129, 200), (64, 128, 64), (130, 300, 72),
          (257, 515, 129), (300, 1024, 256), (513, 70, 520), (700, 1111, 264), (520, 2050, 128), (385, 6007, 136),
-         (129, 129, 8), (2100, 40, 16)]
+         (129, 129, 8), (2100, 40, 16), (16, 5003, 136), (33, 40000, 72), (64, 777, 1096), (65, 777, 1096)]
 
 
 def inputs(tokens, vocab, dim, dtype, k, seed, absent=0.2, index=J):
@@ -248,7 +248,7 @@ def test_classifier_loss(tokens, vocab, dim, dtype):
 
 @pytest.mark.parametrize("k,tau", [(1, 1.0), (5, 2.0), (64, 0.7), (65, 1.0), (256, 3.0)])
 @pytest.mark.parametrize("dtype", [F, B], ids=str)
-@pytest.mark.parametrize("tokens,vocab,dim", [(1, 16, 16), (5, 33, 7), (130, 300, 72), (257, 515, 129)])
+@pytest.mark.parametrize("tokens,vocab,dim", [(1, 16, 16), (5, 33, 7), (40, 2050, 264), (130, 300, 72), (257, 515, 129)])
 def test_distill_loss(tokens, vocab, dim, dtype, k, tau):
     x, w, dloss, ids, teacher = inputs(tokens, vocab, dim, dtype, k, tokens + k)
     check_losses(x, w, dloss, ids, teacher, tau, on_gpu, "aligned")
