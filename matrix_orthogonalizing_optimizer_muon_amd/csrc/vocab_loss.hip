@@ -64,15 +64,15 @@ __global__ __launch_bounds__(kLiveThreads) void k_live(const I* __restrict__ tar
   const int64_t first = w * segment < tokens ? w * segment : tokens;
   const int64_t last = first + segment < tokens ? first + segment : tokens;
   int32_t mine = 0;
-  for (int64_t i = first; i < last; i += 256) {
-    bool in[4];
+  for (int64_t i = first; i < last; i += 512) {
+    bool in[8];   // loads without conditions, so that they are in flight together
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int64_t t = i + 64 * u + lane;
-      in[u] = t < last && (TEACHER ? term[t] <= INFINITY : read_index(targets, t, vocab) >= 0);
+    for (int u = 0; u < 8; ++u) {
+      const int64_t t = i + 64 * u + lane < last ? i + 64 * u + lane : last - 1;
+      in[u] = TEACHER ? term[t] <= INFINITY : read_index(targets, t, vocab) >= 0;
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) mine += __popcll(__ballot(in[u]));
+    for (int u = 0; u < 8; ++u) mine += __popcll(__ballot(in[u] && i + 64 * u + lane < last));
   }
   if (lane == 0) sums[w] = mine;
   __syncthreads();
