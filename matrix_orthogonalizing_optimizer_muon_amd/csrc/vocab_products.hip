@@ -235,6 +235,16 @@ struct LogitsWalk {
     const int32_t left = a.vocab - first;   // columns of the slab that exist, where less than 64
     const int c = 4 * (lane >> 5);
     const auto rs = nt::make_rsrc(static_cast<char*>(a.dl) + ((int64_t)t.m0 * a.dl_ld + first) * 2, kRange);
+    float bases[4], scales[4];
+    if constexpr (EPI == kGradient) {   // all rows' at once
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int32_t r = t.m0 + row0 + 32 * i + (lane & 31);
+        const bool exists = i < mt && r < live;
+        bases[i] = exists ? a.base[r] : 0.f;
+        scales[i] = exists ? a.scale[r] * a.g[r] : 0.f;
+      }
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (i >= mt) break;
@@ -256,8 +266,8 @@ struct LogitsWalk {
           for (int v = 0; v < 16; ++v) top = fmaxf(top, acc[i][j][v]);
         n = whole_exponent(a, fmaxf(top, __shfl_xor(top, 32, 64)));
       } else {
-        n = exists ? a.base[r] : 0.f;
-        by = exists ? a.scale[r] * a.g[r] : 0.f;
+        n = bases[i];
+        by = scales[i];
       }
       float sum = 0.f;
 #pragma unroll

@@ -1,7 +1,9 @@
-// Large bf16 tiles of the classifier's products: the contraction core of the
-// expert layer (expert_mfma.hpp) with operands of one matrix each, walked by one
-// block of eight waves a CU, and epilogues that a caller gives.
+// Large bf16 tiles of the classifier's products: the stages and fragments of the
+// expert layer's core (expert_mfma.hpp) with operands of one matrix each, walked by
+// one block of eight waves a CU, a k loop of its own and epilogues that a caller gives.
 #pragma once
+#include <type_traits>
+
 #include "expert_mfma.hpp"
 #include "vocab.hpp"
 
@@ -49,18 +51,16 @@ struct RowPanel {
       voff[u] = r < o.extent ? (uint32_t)r * o.ld + (uint32_t)chunk * 16u : kNone;
     }
   }
-  __device__ __forceinline__ void ahead(int, int, int) {}
-  template <int NR, int U = 0>
-  __device__ __forceinline__ void step(MUON_LDS char* dst, u32x4 rs, const bool (&in)[2], int w) const {
-    if constexpr (U < NR) {
-      copy_to_lds(dst + (w * NR + U) * 1024, rs, in[U & 1] ? voff[U] : kNone);
-      step<NR, U + 1>(dst, rs, in, w);
-    }
+  struct At {
+    u32x4 rs;
+    bool in[2];
+  };
+  __device__ __forceinline__ At at(int kt) const {
+    return At{copy_rsrc(base + (int64_t)kt * 128, kRange), {kt * kBK + col[0] < k, kt * kBK + col[1] < k}};
   }
-  template <int NR>
-  __device__ __forceinline__ void issue(MUON_LDS char* dst, int kt, int, int w) const {
-    const bool in[2] = {kt * kBK + col[0] < k, kt * kBK + col[1] < k};
-    step<NR>(dst, copy_rsrc(base + (int64_t)kt * 128, kRange), in, w);
+  // copy u of a wave's nr of a k-tile
+  __device__ __forceinline__ void copy(const At& t, MUON_LDS char* dst, int nr, int u, int w) const {
+    copy_to_lds(dst + (w * nr + u) * 1024, t.rs, t.in[u & 1] ? voff[u] : kNone);
   }
 };
 
@@ -82,21 +82,125 @@ struct ColPanel {
       voff[u] = c < o.extent ? (uint32_t)c * 2u + (uint32_t)r * ld : kNone;
     }
   }
-  __device__ __forceinline__ void ahead(int, int, int) {}
-  template <int NR, int U = 0>
-  __device__ __forceinline__ void step(MUON_LDS char* dst, u32x4 rs, int w) const {
-    if constexpr (U < NR) {
-      copy_to_lds(dst + (w * NR + U) * 1024, rs, voff[U]);
-      step<NR, U + 1>(dst, rs, w);
-    }
-  }
-  template <int NR>
-  __device__ __forceinline__ void issue(MUON_LDS char* dst, int kt, int, int w) const {
+  typedef u32x4 At;
+  __device__ __forceinline__ At at(int kt) const {
     // the last row ends with its columns, not with ld: what lies behind it is another's memory
     const int64_t left = (k - (int64_t)kt * kBK) * (int64_t)ld;
-    step<NR>(dst, copy_rsrc(base + (int64_t)kt * kBK * ld, left <= 0 ? 0u : left < kRange ? (uint32_t)left : kRange), w);
+    return copy_rsrc(base + (int64_t)kt * kBK * ld, left <= 0 ? 0u : left < kRange ? (uint32_t)left : kRange);
+  }
+  __device__ __forceinline__ void copy(const At& t, MUON_LDS char* dst, int nr, int u, int w) const {
+    copy_to_lds(dst + (w * nr + u) * 1024, t, voff[u]);
   }
 };
+
+// All copies of a k-tile of one operand.
+template <class C>
+__device__ __forceinline__ void copy_all(MUON_LDS char* dst, const C& c, int nr, int kt, int w) {
+  const typename C::At t = c.at(kt);
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    if (u < nr) c.copy(t, dst, nr, u, w);
+}
+
+// Fragment reads of a k-group one by one: first b, then a.
+template <class S, int FROM, int TO>
+__device__ __forceinline__ void read_frags(TileFrags<S>& f, const MUON_LDS char* st, int kg, int lane, int wy, int wx) {
+  if constexpr (FROM < TO) {
+    u32x4 v[1];
+    if constexpr (FROM < S::NT) {
+      slab_frags<S::QT, S::BN, 1>(v, st + kQAt, wx * S::WN + 32 * FROM, kg, lane);
+      f.b[FROM] = v[0];
+    } else {
+      slab_frags<S::PT, S::BM, 1>(v, st, wy * S::WM + 32 * (FROM - S::NT), kg, lane);
+      f.a[FROM - S::NT] = v[0];
+    }
+    read_frags<S, FROM + 1, TO>(f, st, kg, lane, wy, wx);
+  }
+}
+
+// The products of one k-group, in this order, the fragment reads of another group
+// spread behind them, and behind product m what copy(m) does.
+template <class S, bool READ, int M = 0, class Copy>
+__device__ __forceinline__ void products(Acc& acc, const TileFrags<S>& f, TileFrags<S>& next, const MUON_LDS char* st,
+                                         int kg, int lane, int wy, int wx, Copy copy) {
+  constexpr int N = S::MT * S::NT, R = S::MT + S::NT;
+  if constexpr (M < N) {
+    constexpr int i = M / S::NT, j = M % S::NT;
+    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(nt::bf16x8_t, f.b[j]),
+                                                       __builtin_bit_cast(nt::bf16x8_t, f.a[i]), acc[i][j], 0, 0, 0);
+    if constexpr (READ) read_frags<S, M * R / N, (M + 1) * R / N>(next, st, kg, lane, wy, wx);
+    copy(std::integral_constant<int, M>());
+    __builtin_amdgcn_sched_barrier(0);
+    products<S, READ, M + 1>(acc, f, next, st, kg, lane, wy, wx, copy);
+  }
+}
+
+// The k loop over nk >= 2 tiles of 64, with tile_loop's stages and waits: the first
+// has landed in stage `stage`, the second is on its way to the other, followed by
+// `stored` stores.  The copies of the k-tile after next go out one at a time between
+// products: Q's behind the barrier that frees their stage, in the k-tile's last
+// group, P's in the first group of the next k-tile.  8192 x 32000 x 4096, us (logits
+// with 16-bit results, dx, dw): both operands' copies in two runs 1729, 1696, 1748; one
+// at a time in the last group 1781, 1646, 1796; so 1657, 1615, 1683.  The rest is
+// power: with copies that always hit L2 the MFMA pipes are busy 0.81 of the time
+// at 1.57 GHz instead of 0.74 at 1.71 (dx), in the same time.
+// For the last two k-tiles the copies are the next tile's first two: turn() makes cp,
+// cq, nrp and nrq that tile's and tells whether there is one.
+template <class S, class PC, class QC, class Turn>
+__device__ __forceinline__ void walk_loop(Acc& acc, MUON_LDS char* lds, PC& cp, QC& cq, const int& nrp, const int& nrq,
+                                          int nk, int stored, int& stage, int lane, int w, Turn turn) {
+  constexpr int N = S::MT * S::NT;
+  static_assert(N % S::PR == 0 && N % S::QR == 0, "the copies are spread evenly");
+  const int wy = w / S::WGN, wx = w % S::WGN;
+#pragma unroll
+  for (int i = 0; i < S::MT; ++i)
+#pragma unroll
+    for (int j = 0; j < S::NT; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  TileFrags<S> f0, f1;
+  auto none = [](auto) {};
+  f0.load(lds + stage * kStage, 0, lane, wy, wx);
+  auto first_groups = [&](const MUON_LDS char* st, auto copies) {
+    products<S, true>(acc, f0, f1, st, 1, lane, wy, wx, copies);
+    products<S, true>(acc, f1, f0, st, 2, lane, wy, wx, none);
+    products<S, true>(acc, f0, f1, st, 3, lane, wy, wx, none);
+    wait_behind<0, true>(stored);   // the next k-tile landed, own reads done
+    stored = 0;
+    nt::block_barrier();
+  };
+  for (int kt = 0; kt < nk - 2; ++kt) {
+    MUON_LDS char* st = lds + stage * kStage;
+    MUON_LDS char* other = lds + (stage ^ 1) * kStage;
+    const typename PC::At tp = cp.at(kt + 1);
+    if (kt)
+      first_groups(st, [&](auto m) {
+        constexpr int at = decltype(m)::value;
+        if constexpr (at % (N / S::PR) == 0) cp.copy(tp, other, S::PR, at / (N / S::PR), w);
+      });
+    else first_groups(st, none);
+    stage ^= 1;
+    const typename QC::At tq = cq.at(kt + 2);
+    products<S, true>(acc, f1, f0, other, 0, lane, wy, wx, [&](auto m) {
+      constexpr int at = decltype(m)::value;
+      if constexpr (at % (N / S::QR) == 0) cq.copy(tq, st + kQAt, S::QR, at / (N / S::QR), w);
+    });
+  }
+  if (nk > 2) copy_all(lds + (stage ^ 1) * kStage, cp, S::PR, nk - 1, w);
+  const bool more = turn();
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    MUON_LDS char* st = lds + stage * kStage;
+    first_groups(st, none);
+    if (more) {
+      copy_all(st, cp, nrp, t, w);
+      copy_all(st + kQAt, cq, nrq, t, w);
+    }
+    stage ^= 1;
+    if (t == 0) f0.load(lds + stage * kStage, 0, lane, wy, wx);
+    tile_mfma<S>(acc, f1);
+  }
+}
 
 // An output tile: rows from m0, columns from n0, k-tiles [k0, k0 + nk) of part `part`.
 struct OutTile {
@@ -164,20 +268,24 @@ __device__ __forceinline__ void walk_tiles(char* lds_, int lane0, int w, O& o) {
   typename O::QC cq;
   Acc acc;
   OutTile cur, next;
+  int nrp = 0, nrq = 0;   // copies a wave makes of the operands of the tile that cp and cq are at
   auto cut = [&](const OutTile& t) { return cut_of(o.m_left(t), o.n_left(t)); };
-  auto nrp = [&](const OutTile& t) { return cut(t) == kFlat ? Flat::PR : Full::PR; };
-  auto nrq = [&](const OutTile& t) { return cut(t) == kThin ? Thin::QR : Full::QR; };
   auto init = [&](const OutTile& t) {
-    const int lane = fresh(lane0);
-    cp.init(o.p(t), nrp(t), lane, w);
-    cq.init(o.q(t), nrq(t), lane, w);
+    const int lane = fresh(lane0), c = cut(t);
+    nrp = c == kFlat ? Flat::PR : Full::PR;
+    nrq = c == kThin ? Thin::QR : Full::QR;
+    cp.init(o.p(t), nrp, lane, w);
+    cq.init(o.q(t), nrq, lane, w);
   };
   bool more = o.next(cur);
   int stage = 0, stored = 0;
   if (more) {
     init(cur);
-    tile_issue(lds, cp, cq, nrp(cur), nrq(cur), 0, lane0, w);
-    tile_issue(lds + kStage, cp, cq, nrp(cur), nrq(cur), 1, lane0, w);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      copy_all(lds + t * kStage, cp, nrp, t, w);
+      copy_all(lds + t * kStage + kQAt, cq, nrq, t, w);
+    }
     __builtin_amdgcn_s_waitcnt(nt::kWaitVmLgkm0);
     nt::block_barrier();
   }
@@ -189,10 +297,9 @@ __device__ __forceinline__ void walk_tiles(char* lds_, int lane0, int w, O& o) {
       if (more) init(next);
       return more;
     };
-    auto then = [&](MUON_LDS char* st, int t) { tile_issue(st, cp, cq, nrp(next), nrq(next), t, lane, w); };
-    if (c == kFull) tile_loop<Full>(acc, lds, cp, cq, nk, stored, stage, lane, w, turn, then);
-    else if (c == kFlat) tile_loop<Flat>(acc, lds, cp, cq, nk, stored, stage, lane, w, turn, then);
-    else tile_loop<Thin>(acc, lds, cp, cq, nk, stored, stage, lane, w, turn, then);
+    if (c == kFull) walk_loop<Full>(acc, lds, cp, cq, nrp, nrq, nk, stored, stage, lane, w, turn);
+    else if (c == kFlat) walk_loop<Flat>(acc, lds, cp, cq, nrp, nrq, nk, stored, stage, lane, w, turn);
+    else walk_loop<Thin>(acc, lds, cp, cq, nrp, nrq, nk, stored, stage, lane, w, turn);
     const int row0 = c == kFull ? w / Full::WGN * Full::WM : c == kFlat ? w / Flat::WGN * Flat::WM
                                                                         : w / Thin::WGN * Thin::WM;
     const int col0 = c == kThin ? w % Thin::WGN * Thin::WN : w % Full::WGN * Full::WN;
