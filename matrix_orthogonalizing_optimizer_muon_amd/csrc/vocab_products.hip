@@ -208,6 +208,15 @@ __global__ __launch_bounds__(256) void k_tile(LossArgs a, int32_t tiles_n) {
 
 // --------------------------------------------------------------- large tiles
 
+// The value that lane l ^ 32 has.
+__device__ __forceinline__ float other_half(float v) {
+  typedef uint32_t u32x2_s __attribute__((ext_vector_type(2)));
+  const uint32_t x = __float_as_uint(v);
+  // both registers hold v; the instruction exchanges the upper lanes of one with the lower lanes of the other
+  const u32x2_s r = __builtin_bit_cast(u32x2_s, __builtin_amdgcn_permlane32_swap(x, x, false, false));
+  return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
+}
+
 // Logits, 256 x 256 a tile.  A wave's 64 columns are a slab, 32 of them in each
 // half of a row's two lanes.
 template <int EPI>
@@ -264,7 +273,7 @@ struct LogitsWalk {
         for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int v = 0; v < 16; ++v) top = fmaxf(top, acc[i][j][v]);
-        n = whole_exponent(a, fmaxf(top, __shfl_xor(top, 32, 64)));
+        n = whole_exponent(a, fmaxf(top, other_half(top)));
       } else {
         n = bases[i];
         by = scales[i];
@@ -278,14 +287,14 @@ struct LogitsWalk {
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             e[u] = __builtin_amdgcn_exp2f(exponent(a, acc[i][j][4 * g + u], n, bf16_t()));
-            if (EPI == kGradient) e[u] = left >= 64 || c + 32 * j + 8 * g + u < left ? e[u] * by : 0.f;
+            if (EPI == kGradient) e[u] *= by;   // a column that does not exist: 0, or NaN where the row's are
             else sum += e[u];
           }
           if constexpr (EPI == kStatsExp) put_row(buf, lane, 4 * j + g, u32x2{pack_exps(e[0], e[1]), pack_exps(e[2], e[3])});
           if constexpr (EPI == kGradient) put_row(buf, lane, 4 * j + g, u32x2{pack2(e[0], e[1]), pack2(e[2], e[3])});
         }
       if constexpr (EPI != kGradient) {
-        sum += __shfl_xor(sum, 32, 64);
+        sum += other_half(sum);
         if (exists && lane < 32) {
           typedef float f32x2 __attribute__((ext_vector_type(2)));
           *reinterpret_cast<f32x2*>(a.stats + 2 * ((int64_t)(first / 64) * a.ch.size + r)) = f32x2{n, sum};
