@@ -110,8 +110,7 @@ struct RowsArgs {
   float tau;
 };
 
-// Every row by itself, a wave each: a live one goes to its slot of xs (null: not),
-// its target's logit is the dot product with a row of w; another's dx is zeros.
+// Every row by itself, a wave each: a live one goes to its slot of xs, logit is the dot product with a row of w; another's dx is zeros.
 template <class T>
 __global__ __launch_bounds__(256) void k_rows(LossArgs a, RowsArgs o, T* __restrict__ xs, T* __restrict__ dx) {
   const int lane = threadIdx.x & 63;
@@ -119,7 +118,7 @@ __global__ __launch_bounds__(256) void k_rows(LossArgs a, RowsArgs o, T* __restr
   if (t >= a.tokens) return;
   const int32_t s = o.slot[t], v = s >= 0 && o.id ? o.id[t] : -1;
   const T* x = static_cast<const T*>(a.x) + t * a.dim;
-  const T* w = static_cast<const T*>(a.w) + (int64_t)(v < 0 ? 0 : v) * a.dim;
+  const T* w = static_cast<const T*>(a.w) + (int64_t)(v < 0 ? 0 : v) * a.ld;
   if (s < 0) {
     const float zero[8] = {};
     if (dx)
@@ -127,14 +126,14 @@ __global__ __launch_bounds__(256) void k_rows(LossArgs a, RowsArgs o, T* __restr
     return;
   }
   float sum = 0.f;
-  if (xs || v >= 0) {
+  {
 #pragma unroll 4
     for (int32_t c = lane * 8; c < a.dim; c += 512) {
       const int cnt = a.dim - c < 8 ? a.dim - c : 8;
       float p[8], q[8];
       load8(x + c, cnt, p);
       load8(w + c, v >= 0 ? cnt : 0, q);
-      if (xs) store8(xs + (int64_t)s * a.dim + c, cnt, p);
+      store8(xs + (int64_t)s * a.ld + c, a.ld - c < 8 ? a.ld - c : 8, p);   // past dim: zeros
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum += p[i] * q[i];
     }
@@ -151,6 +150,18 @@ __global__ __launch_bounds__(256) void k_rows(LossArgs a, RowsArgs o, T* __restr
   }
 }
 
+// Rows of dim to rows of ld, zeros behind them: a wave has 512 columns of one.
+__global__ __launch_bounds__(256) void k_pad(const bf16_t* __restrict__ w, int64_t rows, int32_t dim, int32_t ld,
+                                             int32_t units, bf16_t* __restrict__ out) {
+  const int64_t unit = block_index() * 4 + (threadIdx.x >> 6);
+  const int64_t r = unit / units;
+  const int32_t c = (int32_t)(unit - r * units) * 512 + (threadIdx.x & 63) * 8;
+  if (r >= rows || c >= ld) return;
+  float v[8];
+  load8(w + r * dim + c, dim - c < 8 ? dim - c : 8, v);
+  store8(out + r * ld + c, 8, v);
+}
+
 // ------------------------------------------------------------------- targets
 
 // The logits of a teacher's entries: a wave has one, picked[t][j] = <x, w_id>.
@@ -163,7 +174,7 @@ __global__ __launch_bounds__(256) void k_picked(LossArgs a, const int32_t* __res
   if (t >= a.tokens) return;
   const int32_t v = id[unit];
   if (v < 0) return;
-  const float sum = row_dot(static_cast<const T*>(a.x) + t * a.dim, static_cast<const T*>(a.w) + (int64_t)v * a.dim,
+  const float sum = row_dot(static_cast<const T*>(a.x) + t * a.dim, static_cast<const T*>(a.w) + (int64_t)v * a.ld,
                             a.dim, lane);
   if (lane == 0) picked[unit] = sum;
 }
@@ -368,7 +379,8 @@ struct LossSpace {
   bool few;
   int64_t chunk, slabs, dl_ld;
   ProductParts parts;
-  uint64_t xs, sums_of_parts, id, q, term, rows, slot, count, stats, picked, base, scale, g, dl, sums, bytes;
+  int32_t ld;
+  uint64_t xs, w, sums_of_parts, id, q, term, rows, slot, count, stats, picked, base, scale, g, dl, sums, bytes;
 };
 LossSpace loss_space(int dtype, int64_t tokens, int64_t vocab, int64_t dim, int k, bool teacher, bool grads,
                      bool given) {
@@ -386,9 +398,11 @@ LossSpace loss_space(int dtype, int64_t tokens, int64_t vocab, int64_t dim, int 
   l.dl_ld = ceil_div(vocab, 64) * 64;
   const bool large = large_sizes(dtype, tokens, vocab, dim);
   l.parts = grads ? product_parts(dtype, l.chunk, vocab, dim, large) : ProductParts{1, 1};
-  l.xs = p.take(large ? (uint64_t)tokens * dim * 2 : 0);
-  const uint64_t of_dx = l.parts.dx > 1 ? (uint64_t)l.parts.dx * l.chunk * dim * 4 : 0;
-  const uint64_t of_dw = l.parts.dw > 1 ? (uint64_t)l.parts.dw * vocab * dim * 4 : 0;
+  l.ld = (int32_t)(large ? ceil_div(dim, 8) * 8 : dim);
+  l.xs = p.take((uint64_t)tokens * l.ld * es);
+  l.w = p.take(l.ld != dim ? (uint64_t)vocab * l.ld * 2 : 0);
+  const uint64_t of_dx = l.parts.dx > 1 ? (uint64_t)l.parts.dx * l.chunk * l.ld * 4 : 0;
+  const uint64_t of_dw = l.parts.dw > 1 ? (uint64_t)l.parts.dw * vocab * l.ld * 4 : 0;
   l.sums_of_parts = p.take(of_dx > of_dw ? of_dx : of_dw);   // one after the other
   l.id = p.take((uint64_t)tokens * k * 4);
   l.q = p.take(teacher ? (uint64_t)tokens * k * 4 : 0);
@@ -402,7 +416,7 @@ LossSpace loss_space(int dtype, int64_t tokens, int64_t vocab, int64_t dim, int 
   l.scale = p.take((uint64_t)tokens * 4);
   l.g = p.take((uint64_t)tokens * 4);
   l.dl = p.take(grads ? (uint64_t)l.chunk * l.dl_ld * es : 0);
-  l.sums = p.take(grads && l.chunk < tokens ? (uint64_t)vocab * dim * 4 : 0);
+  l.sums = p.take(grads && l.chunk < tokens ? (uint64_t)vocab * l.ld * 4 : 0);
   l.bytes = p.used;
   return l;
 }
@@ -439,8 +453,8 @@ template <class T>
 int run(const Call& c, const LossSpace& l, char* ws, hipStream_t s) {
   const bool grads = c.dw != nullptr, given = c.lse_in != nullptr;
   int rc;
-  const bool large = large_sizes(c.dtype, c.tokens, c.vocab, c.dim) && aligned16(c.w) &&
-                     (!grads || (aligned16(c.dx) && aligned16(c.dw)));
+  // w in rows that the large tiles read: as it is, or copied
+  const bool large = large_sizes(c.dtype, c.tokens, c.vocab, c.dim) && (l.ld != c.dim || aligned16(c.w));
   LossArgs a = {};
   a.ch.rows = reinterpret_cast<int32_t*>(ws + l.rows);
   a.ch.count = reinterpret_cast<int32_t*>(ws + l.count);
@@ -450,21 +464,31 @@ int run(const Call& c, const LossSpace& l, char* ws, hipStream_t s) {
   a.tokens = c.tokens;
   a.vocab = (int32_t)c.vocab;
   a.dim = (int32_t)c.dim;
-  a.xs = large ? ws + l.xs : nullptr;
-  a.dl_ld = l.dl_ld;
-  a.sums_of_parts = reinterpret_cast<float*>(ws + l.sums_of_parts);
-  a.parts = l.parts;
   const double to_log2 = 1.4426950408889634 / (double)c.tau;
   a.to_log2 = (float)to_log2;
   a.to_log2_low = (float)(to_log2 - (double)a.to_log2);
   a.stats = given ? nullptr : reinterpret_cast<float*>(ws + l.stats);
+  if (l.few)
+    return few_loss(a, c.dtype, FewCall{c.targets, c.index_bytes, c.teacher, c.teacher_dtype, c.k, c.tau, c.loss, c.lse},
+                    s);
+  a.xs = ws + l.xs;
+  a.ld = l.ld;
+  a.large = large;
+  a.chunked = l.ld == c.dim && aligned16(c.dx) && aligned16(c.dw);
+  if (l.ld != c.dim) {
+    const int64_t units = ceil_div(l.ld, 512);
+    hipLaunchKernelGGL(k_pad, grid_of_blocks(ceil_div(c.vocab * units, 4), 256), dim3(256), 0, s,
+                       static_cast<const bf16_t*>(c.w), c.vocab, (int32_t)c.dim, l.ld, (int32_t)units,
+                       reinterpret_cast<bf16_t*>(ws + l.w));
+    a.w = ws + l.w;
+  }
+  a.dl_ld = l.dl_ld;
+  a.sums_of_parts = reinterpret_cast<float*>(ws + l.sums_of_parts);
+  a.parts = l.parts;
   a.dl = grads ? ws + l.dl : nullptr;
   a.dx = c.dx;
   a.dw = c.dw;
   a.sums = l.chunk < c.tokens ? reinterpret_cast<float*>(ws + l.sums) : nullptr;
-  if (l.few)
-    return few_loss(a, c.dtype, FewCall{c.targets, c.index_bytes, c.teacher, c.teacher_dtype, c.k, c.tau, c.loss, c.lse},
-                    s);
   if ((rc = c.index_bytes == 8 ? find_rows<int64_t>(c, l, ws, s) : find_rows<int32_t>(c, l, ws, s))) return rc;
   if (!c.tokens) {   // no rows: dw is zeros
     a.first = a.last = true;
@@ -478,7 +502,7 @@ int run(const Call& c, const LossSpace& l, char* ws, hipStream_t s) {
   RowsArgs o = {reinterpret_cast<int32_t*>(ws + l.slot), c.k == 1 ? id : nullptr, picked, c.lse_in, c.dloss, base, scale,
                 g, c.tau};
   hipLaunchKernelGGL((k_rows<T>), grid_of_blocks(ceil_div(c.tokens, 4), 256), dim3(256), 0, s, a, o,
-                     large ? reinterpret_cast<T*>(ws + l.xs) : nullptr, grads ? static_cast<T*>(c.dx) : nullptr);
+                     reinterpret_cast<T*>(ws + l.xs), grads ? static_cast<T*>(c.dx) : nullptr);
   if (c.k > 1)
     hipLaunchKernelGGL((k_picked<T>), grid_of_blocks(ceil_div(c.tokens * c.k, 4), 256), dim3(256), 0, s, a, id, c.k,
                        picked);

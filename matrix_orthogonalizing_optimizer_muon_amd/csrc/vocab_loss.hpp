@@ -31,10 +31,13 @@ struct ProductParts {
 struct LossArgs {
   Chunk ch;
   const void* x;           // tokens x dim
-  const void* w;           // vocab x dim
-  const void* xs;          // x's live rows by slot, or null where the products gather them
+  const void* w;           // vocab x ld
+  const void* xs;          // x's live rows by slot, of ld
   int64_t tokens;
   int32_t vocab, dim;
+  int32_t ld;              // dim, or, for the large tiles, dim in whole 16-byte chunks, filled up with zeros
+  bool large;              // the large tiles take the products
+  bool chunked;            // rows of dx and dw are whole chunks on borders of 16 bytes
   int64_t dl_ld;           // elements of a row of dl: vocab in whole slabs of 64
   // exp(l / temperature) = 2^(l (to_log2 + to_log2_low)): log2(e) / temperature in two parts
   float to_log2, to_log2_low;
@@ -50,8 +53,8 @@ struct LossArgs {
   void* dx;                // tokens x dim
   void* dw;                // vocab x dim
   ProductParts parts;
-  float* sums_of_parts;    // [part][chunk][dim] of dx, then [part][vocab][dim] of dw, where there are more than one
-  float* sums;             // vocab x dim: of the chunks so far, or null where there is one
+  float* sums_of_parts;    // [part][chunk][ld] of dx, then [part][vocab][ld] of dw, where there are more than one
+  float* sums;             // vocab x ld: of the chunks so far, or null where there is one
   bool first, last;        // chunk
 };
 
@@ -179,10 +182,10 @@ struct Slab<float> {
 };
 inline int slab_cols(int dtype) { return dtype == MUON_BF16 ? Slab<bf16_t>::kCols : Slab<float>::kCols; }
 
-// Whether the large tiles take a call's sizes: bf16 rows of whole 16-byte chunks
-// that 31 bits address 256 of; and the rest of what they need of a call.
+// Whether the large tiles take a call's sizes: bf16 rows of which 31 bits address
+// 256.  They read rows of whole 16-byte chunks: w is copied where its are not.
 inline bool large_sizes(int dtype, int64_t tokens, int64_t vocab, int64_t dim) {
-  return dtype == MUON_BF16 && dim % 8 == 0 && vocab < (1 << 21) && dim < (1 << 21) && tokens > 0;
+  return dtype == MUON_BF16 && vocab < (1 << 21) && dim < (1 << 21) && tokens > 0;
 }
 ProductParts product_parts(int dtype, int64_t tokens, int64_t vocab, int64_t dim, bool large);
 

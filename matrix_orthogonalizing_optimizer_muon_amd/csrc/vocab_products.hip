@@ -58,6 +58,7 @@ __global__ __launch_bounds__(256) void k_tile(LossArgs a, int32_t tiles_n) {
   const int64_t m0 = tm * G::B;
   const int32_t live = live_slots(a.ch);
   const int32_t* rows = a.ch.rows + a.ch.slot0;
+  const T* xs = static_cast<const T*>(a.xs) + a.ch.slot0 * a.ld;
   int64_t m_left;
   int32_t K;
   Stager<T, PT> sp;
@@ -66,8 +67,9 @@ __global__ __launch_bounds__(256) void k_tile(LossArgs a, int32_t tiles_n) {
     m_left = live - m0;
     if (m_left <= 0) return;
     K = a.dim;
-    sp.init(a.x, rows, m0, m_left, a.tokens, 0, a.dim);
+    sp.init(xs, nullptr, m0, m_left, 0, 0, a.dim);
     sq.init(a.w, nullptr, n0, a.vocab - n0, 0, 0, a.dim);
+    sp.ld = sq.ld = a.ld;
   } else {
     m_left = (PRODUCT == kDx ? live : a.vocab) - m0;
     if (m_left <= 0) return;
@@ -80,9 +82,10 @@ __global__ __launch_bounds__(256) void k_tile(LossArgs a, int32_t tiles_n) {
       sq.init(a.w, nullptr, k0, K, 0, n0, a.dim);
     } else {
       sp.init(a.dl, nullptr, k0, K, 0, (int32_t)m0, a.vocab);
-      sq.init(a.x, rows, k0, K, a.tokens, n0, a.dim);
+      sq.init(xs, nullptr, k0, K, 0, n0, a.dim);
     }
     sp.ld = a.dl_ld;
+    sq.ld = a.ld;
   }
   f32x16_t acc[NT][NT];
 #pragma unroll
@@ -92,19 +95,26 @@ __global__ __launch_bounds__(256) void k_tile(LossArgs a, int32_t tiles_n) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
   const int nk = (int)(((uint32_t)K + G::BK - 1) / G::BK);
+  // the k-tile after next comes into one pair of stagers while the next one waits in the other
+  Stager<T, PT> sp1 = sp;
+  Stager<T, QT> sq1 = sq;
   if (nk) {
     sp.fetch(0);
     sq.fetch(0);
     sp.commit(lds);
     sq.commit(lds + PB);
   }
-  for (int kt = 0; kt < nk; ++kt) {
+  if (nk > 1) {
+    sp1.fetch(G::BK);
+    sq1.fetch(G::BK);
+  }
+  auto step = [&](int kt, Stager<T, PT>& p2, Stager<T, QT>& q2, const Stager<T, PT>& p1, const Stager<T, QT>& q1) {
     __syncthreads();
     const char* st = lds + (kt & 1) * (PB + QB);
     char* next = lds + (~kt & 1) * (PB + QB);
-    if (kt + 1 < nk) {
-      sp.fetch((int64_t)(kt + 1) * G::BK);
-      sq.fetch((int64_t)(kt + 1) * G::BK);
+    if (kt + 2 < nk) {
+      p2.fetch((int64_t)(kt + 2) * G::BK);
+      q2.fetch((int64_t)(kt + 2) * G::BK);
     }
     f32x16_t total;
     if constexpr (sizeof(T) == 4) {
@@ -125,9 +135,13 @@ __global__ __launch_bounds__(256) void k_tile(LossArgs a, int32_t tiles_n) {
     }
     if constexpr (sizeof(T) == 4) acc[0][0] += total;
     if (kt + 1 < nk) {
-      sp.commit(next);
-      sq.commit(next + PB);
+      p1.commit(next);
+      q1.commit(next + PB);
     }
+  };
+  for (int kt = 0; kt < nk; kt += 2) {
+    step(kt, sp, sq, sp1, sq1);
+    if (kt + 1 < nk) step(kt + 1, sp1, sq1, sp, sq);
   }
   // lane l has row l % 32 of a 32 x 32 tile, registers 4 g + 0..3 columns 8 g + 4 (l / 32) + 0..3
 #pragma unroll
@@ -186,8 +200,8 @@ __global__ __launch_bounds__(256) void k_tile(LossArgs a, int32_t tiles_n) {
     } else if (exists) {
       constexpr bool DX = PRODUCT == kDx;
       const bool whole = (DX ? a.parts.dx : a.parts.dw) == 1;
-      const int64_t at = (DX && whole ? (int64_t)rows[r] : r) * a.dim;
-      float* sums = whole ? a.sums : a.sums_of_parts + (int64_t)blockIdx.z * (DX ? a.ch.size : a.vocab) * a.dim;
+      const int64_t at = (DX && whole ? (int64_t)rows[r] : r) * a.dim, sum_at = r * a.ld;
+      float* sums = whole ? a.sums : a.sums_of_parts + (int64_t)blockIdx.z * (DX ? a.ch.size : a.vocab) * a.ld;
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -195,12 +209,12 @@ __global__ __launch_bounds__(256) void k_tile(LossArgs a, int32_t tiles_n) {
           const int32_t c = c0 + 32 * j + 8 * q;
           float v[4] = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
           if (!DX && whole && !a.first) {
-            const u32x4 before = load16(sums + at + c, a.dim - c);
+            const u32x4 before = load16(sums + sum_at + c, a.dim - c);
 #pragma unroll
             for (int u = 0; u < 4; ++u) v[u] += __uint_as_float(before[u]);
           }
           if (whole && (DX || a.last)) store4(static_cast<T*>(DX ? a.dx : a.dw) + at + c, a.dim - c, v);
-          else store4(sums + at + c, a.dim - c, v);
+          else store4(sums + sum_at + c, a.dim - c, v);
         }
     }
   }
@@ -231,11 +245,10 @@ struct LogitsWalk {
   __device__ __forceinline__ int64_t m_left(const OutTile& t) const { return live - t.m0; }
   __device__ __forceinline__ int64_t n_left(const OutTile& t) const { return a.vocab - t.n0; }
   __device__ __forceinline__ Panel p(const OutTile& t) const {
-    return Panel{static_cast<const char*>(a.xs) + (a.ch.slot0 + t.m0) * a.dim * 2, (uint32_t)a.dim * 2u, live - t.m0,
-                 a.dim};
+    return Panel{static_cast<const char*>(a.xs) + (a.ch.slot0 + t.m0) * a.ld * 2, (uint32_t)a.ld * 2u, live - t.m0, a.ld};
   }
   __device__ __forceinline__ Panel q(const OutTile& t) const {
-    return Panel{static_cast<const char*>(a.w) + (int64_t)t.n0 * a.dim * 2, (uint32_t)a.dim * 2u, a.vocab - t.n0, a.dim};
+    return Panel{static_cast<const char*>(a.w) + (int64_t)t.n0 * a.ld * 2, (uint32_t)a.ld * 2u, a.vocab - t.n0, a.ld};
   }
   __device__ __forceinline__ int store(Acc& acc, const OutTile& t, int mt, int row0, int col0, MUON_LDS char* buf,
                                        int lane) const {
@@ -347,17 +360,17 @@ struct GradWalk {
   }
   __device__ __forceinline__ Panel q(const OutTile& t) const {
     const int64_t k = (int64_t)t.k0 * kBK;
-    const char* from = kX ? static_cast<const char*>(a.w) + k * a.dim * 2
-                          : static_cast<const char*>(a.xs) + (a.ch.slot0 + k) * a.dim * 2;
-    return Panel{from + t.n0 * 2ll, (uint32_t)a.dim * 2u, a.dim - t.n0, (int32_t)((kX ? a.vocab : live) - k)};
+    const char* from = kX ? static_cast<const char*>(a.w) + k * a.ld * 2
+                          : static_cast<const char*>(a.xs) + (a.ch.slot0 + k) * a.ld * 2;
+    return Panel{from + t.n0 * 2ll, (uint32_t)a.ld * 2u, a.ld - t.n0, (int32_t)((kX ? a.vocab : live) - k)};
   }
   __device__ __forceinline__ int store(Acc& acc, const OutTile& t, int mt, int row0, int col0, MUON_LDS char* buf,
                                        int lane) const {
     const int32_t c0 = t.n0 + col0, m = rows() - t.m0;
     const bool parts = (kX ? a.parts.dx : a.parts.dw) > 1;
     if (parts || (!kX && a.sums)) {   // sums: of a part, or of the chunks so far
-      float* out = parts ? a.sums_of_parts + ((int64_t)t.part * (kX ? a.ch.size : a.vocab) + t.m0) * a.dim
-                         : a.sums + (int64_t)t.m0 * a.dim;
+      float* out = parts ? a.sums_of_parts + ((int64_t)t.part * (kX ? a.ch.size : a.vocab) + t.m0) * a.ld
+                         : a.sums + (int64_t)t.m0 * a.ld;
       bf16_t* dw = static_cast<bf16_t*>(a.dw) + (int64_t)t.m0 * a.dim;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -372,38 +385,40 @@ struct GradWalk {
           for (int u = 0; u < 4; ++u) {
             u32x4 v = get_row(buf, lane, u);
             const int q = row0 + 32 * i + u * 8 + lane / 8, c = c0 + 32 * j + 4 * (lane & 7);
-            if (q >= m || c >= a.dim) continue;
-            const int64_t at = (int64_t)q * a.dim + c;
+            if (q >= m || c >= a.ld) continue;
+            const int64_t at = (int64_t)q * a.ld + c;
             if (!kX && !parts && !a.first) {
               const u32x4 before = *reinterpret_cast<const u32x4*>(out + at);
 #pragma unroll
               for (int x = 0; x < 4; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) + __uint_as_float(before[x]));
             }
-            if (!kX && !parts && a.last)
-              *reinterpret_cast<u32x2*>(dw + at) =
-                  u32x2{pack2(__uint_as_float(v[0]), __uint_as_float(v[1])), pack2(__uint_as_float(v[2]), __uint_as_float(v[3]))};
-            else
+            if (!kX && !parts && a.last) {
+              const float o[4] = {__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]), __uint_as_float(v[3])};
+              store4(dw + (int64_t)q * a.dim + c, a.dim - c, o);
+            } else
               *reinterpret_cast<u32x4*>(out + at) = v;
           }
         }
       }
       return 0;
     }
-    if (!kX)
+    if (!kX && a.chunked)
       return tile_store(acc, mt, buf, static_cast<bf16_t*>(a.dw) + (int64_t)t.m0 * a.dim, row0, m < 256 ? m : 256, c0,
                         a.dim, lane);
     // rows of dx lie where rows[slot] says
     const int32_t* rows = a.ch.rows + a.ch.slot0 + t.m0;
-    bf16_t* dx = static_cast<bf16_t*>(a.dx);
+    bf16_t* to = static_cast<bf16_t*>(kX ? a.dx : a.dw);
+    int64_t row[4][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (i >= mt) break;
-      int32_t to[4];
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int q = row0 + 32 * i + u * 8 + lane / 8;
-        to[u] = q < m ? rows[q] : -1;
+        row[i][u] = i >= mt || q >= m ? -1 : kX ? rows[q] : t.m0 + q;
       }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i >= mt) break;
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -414,7 +429,17 @@ struct GradWalk {
       for (int u = 0; u < 4; ++u) {
         const u32x4 v = get_row(buf, lane, u);
         const int c = c0 + 8 * (lane & 7);
-        if (to[u] >= 0 && c < a.dim) *reinterpret_cast<u32x4*>(dx + (int64_t)to[u] * a.dim + c) = v;
+        if (row[i][u] < 0 || c >= a.dim) continue;
+        bf16_t* p = to + row[i][u] * a.dim + c;
+        if (a.chunked) {
+          *reinterpret_cast<u32x4*>(p) = v;
+        } else if (a.dim - c >= 8) {
+          *reinterpret_cast<u32x4_any*>(p) = v;
+        } else {
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            if (c + x < a.dim) p[x].bits = (uint16_t)(v[x / 2] >> (16 * (x % 2)));
+        }
       }
     }
     return 0;
@@ -442,7 +467,7 @@ __global__ __launch_bounds__(256) void k_add(LossArgs a, int32_t units) {
   const int64_t c = (unit - s * units) * 512 + (threadIdx.x & 63) * 8;
   if (c >= a.dim) return;
   const int cnt = a.dim - c < 8 ? (int)(a.dim - c) : 8, parts = DX ? a.parts.dx : a.parts.dw;
-  const int64_t size = (int64_t)(DX ? a.ch.size : a.vocab) * a.dim, at = s * a.dim + c;
+  const int64_t size = (int64_t)(DX ? a.ch.size : a.vocab) * a.ld, at = s * a.ld + c;
   float sum[8] = {};
   if (!DX && !a.first) load8(a.sums + at, cnt, sum);
 #pragma unroll 4
@@ -453,7 +478,7 @@ __global__ __launch_bounds__(256) void k_add(LossArgs a, int32_t units) {
     for (int i = 0; i < 8; ++i) sum[i] += v[i];
   }
   if (DX) store8(static_cast<T*>(a.dx) + (int64_t)a.ch.rows[a.ch.slot0 + s] * a.dim + c, cnt, sum);
-  else if (a.last) store8(static_cast<T*>(a.dw) + at, cnt, sum);
+  else if (a.last) store8(static_cast<T*>(a.dw) + s * a.dim + c, cnt, sum);
   else store8(a.sums + at, cnt, sum);
 }
 
@@ -482,7 +507,7 @@ template <class T, int PRODUCT>
 int launch_grad(const LossArgs& a, hipStream_t s) {
   const int64_t m = PRODUCT == kDx ? a.ch.size : a.vocab, units = ceil_div(a.dim, 512);
   const int parts = PRODUCT == kDx ? a.parts.dx : a.parts.dw;
-  if (a.xs) {
+  if (a.large) {
     hipLaunchKernelGGL((k_grad<PRODUCT>), dim3(kWalkers), dim3(512), 0, s, a);
   } else {
     const int rc = launch_tile<T, PRODUCT, kStats>(a, m, a.dim, parts, s);
@@ -523,7 +548,7 @@ ProductParts product_parts(int dtype, int64_t tokens, int64_t vocab, int64_t dim
 }
 
 int logits_product(const LossArgs& a, int dtype, Epilogue e, hipStream_t s) {
-  if (a.xs) {
+  if (a.large) {
     if (e == kStats) return launch_logits_large<kStats>(a, s);
     return e == kStatsExp ? launch_logits_large<kStatsExp>(a, s) : launch_logits_large<kGradient>(a, s);
   }
