@@ -132,14 +132,40 @@ __global__ __launch_bounds__(512) void k_few_join(LossArgs a, const I* __restric
     return;
   }
   const T* x = static_cast<const T*>(a.x) + t * a.dim;
+  if constexpr (kTeacher) {   // entries w, w + 8, .. two at a time
 #pragma unroll
-  for (int i = 0; i < (kTeacher ? TeacherRow::N : 1); ++i)
-    for (int j = w; j < 64 && j + 64 * i < k; j += 8) {
-      const int32_t v = __builtin_amdgcn_readlane(r.at[i], j);
-      if (v < 0) continue;
-      const float dot = row_dot(x, static_cast<const T*>(a.w) + (int64_t)v * a.dim, a.dim, lane);
-      if (lane == 0) picked[j + 64 * i] = dot;
-    }
+    for (int i = 0; i < TeacherRow::N; ++i)
+      for (int j = w; j < 64 && j + 64 * i < k; j += 16) {
+        const int32_t v0 = __builtin_amdgcn_readlane(r.at[i], j);
+        const int32_t v1 = __builtin_amdgcn_readlane(r.at[i], j + 8 < 64 ? j + 8 : j);
+        const T* w0 = static_cast<const T*>(a.w) + (int64_t)(v0 < 0 ? 0 : v0) * a.dim;
+        const T* w1 = static_cast<const T*>(a.w) + (int64_t)(v1 < 0 ? 0 : v1) * a.dim;
+        float d0 = 0.f, d1 = 0.f;
+#pragma unroll 2
+        for (int32_t c = lane * 8; c < a.dim; c += 512) {
+          const int cnt = a.dim - c < 8 ? a.dim - c : 8;
+          float p[8], q0[8], q1[8];
+          load8(x + c, cnt, p);
+          load8(w0 + c, cnt, q0);
+          load8(w1 + c, cnt, q1);
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            d0 += p[u] * q0[u];
+            d1 += p[u] * q1[u];
+          }
+        }
+        d0 = wave_sum(d0);
+        d1 = wave_sum(d1);
+        if (lane == 0) {   // an entry that is not there is not read
+          picked[j + 64 * i] = d0;
+          if (j + 8 < 64) picked[j + 8 + 64 * i] = d1;
+        }
+      }
+  } else if (w == 0) {
+    const float d = row_dot(x, static_cast<const T*>(a.w) + (int64_t)__builtin_amdgcn_readfirstlane(r.at[0]) * a.dim,
+                            a.dim, lane);
+    if (lane == 0) picked[0] = d;
+  }
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) merge_sums(n, sum, __shfl_xor(n, o, 64), __shfl_xor(sum, o, 64));
   if (lane == 0) {

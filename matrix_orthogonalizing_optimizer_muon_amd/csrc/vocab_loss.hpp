@@ -162,7 +162,7 @@ struct TeacherRow {
 // off by 1.03 of what one rounding gives, where two to bf16 give 1.4.  A NaN comes
 // out as anything; its row's scale is NaN.
 __device__ __forceinline__ uint32_t pack_exps(float lo, float hi) {
-  return ((__float_as_uint(lo) + 0x2000u) >> 14 & 0xffffu) | ((__float_as_uint(hi) + 0x2000u) << 2 & 0xffff0000u);
+  return __builtin_amdgcn_perm((__float_as_uint(hi) << 2) + 0x8000u, (__float_as_uint(lo) << 2) + 0x8000u, 0x07060302u);
 }
 __device__ __forceinline__ void unpack_exps(uint32_t p, float& lo, float& hi) {
   lo = __uint_as_float((p & 0xffffu) << 14);
