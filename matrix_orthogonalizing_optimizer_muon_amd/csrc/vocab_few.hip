@@ -25,9 +25,9 @@ __host__ __device__ constexpr int64_t few_row_bytes(int64_t dim) {
 // 16 rows of w at a time, which come straight into the MFMA operands (lane l: 16
 // bytes of row l % 16), eight loads in flight; lane l gets row l % 16 of x and rows
 // 4 (l / 16) + 0..3 of w.  Bound by w's way from memory: 32000 x 1024 bf16, 66 MB, one row: 14 us.
-// stats: [block][row] pairs.
-template <class T, int NB>
-__global__ __launch_bounds__(64 * kFewWaves) void k_few_logits(LossArgs a) {
+// stats: [block][row] pairs; the logits of rows' ids go to picked as they come by.
+template <class T, int NB, class I>
+__global__ __launch_bounds__(64 * kFewWaves) void k_few_logits(LossArgs a, const I* __restrict__ ids, int32_t k) {
   constexpr int PER = Few<T>::PER, STEP = 4 * PER, U = 8;
   __shared__ __attribute__((aligned(16))) char lds[kFewLds];
   __shared__ float tops[kFewWaves][16 * NB], sums[kFewWaves][16 * NB];
@@ -73,6 +73,15 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_few_logits(LossArgs a) {
     const int32_t left = a.vocab - r0 - 4 * (lane >> 4);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
+      const int32_t t = 16 * b + (lane & 15);
+      if (t < rows) {
+#pragma unroll 4
+        for (int32_t j = 0; j < k; ++j) {
+          const uint64_t c = (uint64_t)(int64_t)ids[t * k + j] - (uint64_t)(r0 + 4 * (lane >> 4));   // below: huge
+          if (c < 4 && (int32_t)c < left)
+            a.picked[t * k + j] = c < 2 ? (c == 0 ? acc[b][0] : acc[b][1]) : c == 2 ? acc[b][2] : acc[b][3];
+        }
+      }
       float top = -INFINITY, add = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -103,14 +112,14 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_few_logits(LossArgs a) {
   st[1] = all;
 }
 
-// A row's loss from the blocks' sums, by one block: its targets' logits are dot
-// products of its waves.  TT: the teacher's type, or void: targets alone.
+// A row's loss from the blocks' sums, by one block.  TT: the teacher's type, or void:
+// targets alone.
 template <class T, class I, class TT>
 __global__ __launch_bounds__(512) void k_few_join(LossArgs a, const I* __restrict__ ids, const TT* __restrict__ teacher,
                                                   int32_t k, int32_t blocks, float tau, float* __restrict__ loss,
                                                   float* __restrict__ lse) {
   constexpr bool kTeacher = !std::is_same<TT, void>::value;
-  __shared__ float tops[8], sums[8], picked[kMaxTeacher];
+  __shared__ float tops[8], sums[8];
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t t = blockIdx.x;
   float n = -INFINITY, sum = 0.f;
@@ -131,41 +140,6 @@ __global__ __launch_bounds__(512) void k_few_join(LossArgs a, const I* __restric
     if (tid == 0) loss[t] = lse[t] = 0.f;
     return;
   }
-  const T* x = static_cast<const T*>(a.x) + t * a.dim;
-  if constexpr (kTeacher) {   // entries w, w + 8, .. two at a time
-#pragma unroll
-    for (int i = 0; i < TeacherRow::N; ++i)
-      for (int j = w; j < 64 && j + 64 * i < k; j += 16) {
-        const int32_t v0 = __builtin_amdgcn_readlane(r.at[i], j);
-        const int32_t v1 = __builtin_amdgcn_readlane(r.at[i], j + 8 < 64 ? j + 8 : j);
-        const T* w0 = static_cast<const T*>(a.w) + (int64_t)(v0 < 0 ? 0 : v0) * a.dim;
-        const T* w1 = static_cast<const T*>(a.w) + (int64_t)(v1 < 0 ? 0 : v1) * a.dim;
-        float d0 = 0.f, d1 = 0.f;
-#pragma unroll 2
-        for (int32_t c = lane * 8; c < a.dim; c += 512) {
-          const int cnt = a.dim - c < 8 ? a.dim - c : 8;
-          float p[8], q0[8], q1[8];
-          load8(x + c, cnt, p);
-          load8(w0 + c, cnt, q0);
-          load8(w1 + c, cnt, q1);
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            d0 += p[u] * q0[u];
-            d1 += p[u] * q1[u];
-          }
-        }
-        d0 = wave_sum(d0);
-        d1 = wave_sum(d1);
-        if (lane == 0) {   // an entry that is not there is not read
-          picked[j + 64 * i] = d0;
-          if (j + 8 < 64) picked[j + 8 + 64 * i] = d1;
-        }
-      }
-  } else if (w == 0) {
-    const float d = row_dot(x, static_cast<const T*>(a.w) + (int64_t)__builtin_amdgcn_readfirstlane(r.at[0]) * a.dim,
-                            a.dim, lane);
-    if (lane == 0) picked[0] = d;
-  }
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) merge_sums(n, sum, __shfl_xor(n, o, 64), __shfl_xor(sum, o, 64));
   if (lane == 0) {
@@ -182,7 +156,7 @@ __global__ __launch_bounds__(512) void k_few_join(LossArgs a, const I* __restric
   float off = 0.f;
 #pragma unroll
   for (int i = 0; i < (kTeacher ? TeacherRow::N : 1); ++i)
-    if (r.at[i] >= 0) off += r.q[i] * loss_term(a, picked[lane + 64 * i], n, log_sum);
+    if (r.at[i] >= 0) off += r.q[i] * loss_term<T>(a, a.picked[t * k + lane + 64 * i], n, log_sum);
   off = wave_sum(off);
   if (lane) return;
   loss[t] = tau * tau * (r.term + off);
@@ -191,26 +165,25 @@ __global__ __launch_bounds__(512) void k_few_join(LossArgs a, const I* __restric
 
 template <class T>
 int launch(const LossArgs& a, const FewCall& c, hipStream_t s) {
-  const dim3 grid((uint32_t)few_blocks(a.vocab)), block(64 * kFewWaves);
+  const dim3 grid((uint32_t)few_blocks(a.vocab)), block(64 * kFewWaves), rows((uint32_t)a.tokens);
   const int nb = (int)((a.tokens + 15) / 16);
-  if (nb == 1) hipLaunchKernelGGL((k_few_logits<T, 1>), grid, block, 0, s, a);
-  else if (nb == 2) hipLaunchKernelGGL((k_few_logits<T, 2>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((k_few_logits<T, 4>), grid, block, 0, s, a);
-  const dim3 rows((uint32_t)a.tokens);
   const int32_t blocks = (int32_t)grid.x;
-  auto join = [&](auto index, auto* teacher) {
+  auto by_index = [&](auto index) {
     typedef decltype(index) I;
-    typedef typename std::remove_const<typename std::remove_pointer<decltype(teacher)>::type>::type TT;
-    hipLaunchKernelGGL((k_few_join<T, I, TT>), rows, dim3(512), 0, s, a, static_cast<const I*>(c.ids), teacher, c.k,
-                       blocks, c.tau, c.loss, c.lse);
+    const I* ids = static_cast<const I*>(c.ids);
+    if (nb == 1) hipLaunchKernelGGL((k_few_logits<T, 1, I>), grid, block, 0, s, a, ids, c.k);
+    else if (nb == 2) hipLaunchKernelGGL((k_few_logits<T, 2, I>), grid, block, 0, s, a, ids, c.k);
+    else hipLaunchKernelGGL((k_few_logits<T, 4, I>), grid, block, 0, s, a, ids, c.k);
+    auto join = [&](auto* teacher) {
+      typedef typename std::remove_const<typename std::remove_pointer<decltype(teacher)>::type>::type TT;
+      hipLaunchKernelGGL((k_few_join<T, I, TT>), rows, dim3(512), 0, s, a, ids, teacher, c.k, blocks, c.tau, c.loss, c.lse);
+    };
+    if (!c.teacher) join(static_cast<const void*>(nullptr));
+    else if (c.teacher_dtype == MUON_BF16) join(static_cast<const bf16_t*>(c.teacher));
+    else join(static_cast<const float*>(c.teacher));
   };
-  auto by_teacher = [&](auto index) {
-    if (!c.teacher) join(index, static_cast<const void*>(nullptr));
-    else if (c.teacher_dtype == MUON_BF16) join(index, static_cast<const bf16_t*>(c.teacher));
-    else join(index, static_cast<const float*>(c.teacher));
-  };
-  if (c.index_bytes == 8) by_teacher(int64_t(0));
-  else by_teacher(int32_t(0));
+  if (c.index_bytes == 8) by_index(int64_t(0));
+  else by_index(int32_t(0));
   return launch_status("classifier loss launch");
 }
 

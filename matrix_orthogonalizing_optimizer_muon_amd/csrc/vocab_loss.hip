@@ -9,10 +9,9 @@
 //
 // Cross entropy is k = 1, q = 1, tau = 1.  Around the products
 // (vocab_products.hip) the kernels here find the rows that count and their
-// targets, take the targets' logits as dot products of their own in fp32, join
-// the slabs' sums, and put the targets' part into dl: its entries there are
-// written from the fp32 logits, so that exp(..) - q loses nothing to the
-// rounding of dl before the difference.
+// targets, join the slabs' sums, and put the targets' part into dl: its entries
+// there are written from the fp32 logits that the first product picked out, so
+// that exp(..) - q loses nothing to the rounding of dl before the difference.
 //
 // dl is the products' operand and so in the type of x: bf16 rounds an entry by
 // 2^-8 of what it is at the most, as it would a logits gradient in memory (in the
@@ -49,8 +48,8 @@ __global__ __launch_bounds__(256) void k_teacher(const TT* __restrict__ teacher,
 }
 
 // The live rows in their order, in one block: each wave has a segment, counts it,
-// and writes it behind those before.  TEACHER: term tells them; else targets, whose
-// ids are written too.  Rows that do not count get loss and lse 0; slot: -1.
+// and writes it behind those before.  TEACHER: term tells them; else targets, which
+// are written by slot.  Rows that do not count get loss and lse 0; slot: -1.
 constexpr int kLiveThreads = 1024;
 template <class I, bool TEACHER>
 __global__ __launch_bounds__(kLiveThreads) void k_live(const I* __restrict__ targets, const float* __restrict__ term,
@@ -89,8 +88,8 @@ __global__ __launch_bounds__(kLiveThreads) void k_live(const I* __restrict__ tar
     const uint64_t in = __ballot(v >= 0);
     if (t < last) {
       const int32_t to = at + __popcll(in & ((uint64_t(1) << lane) - 1));
-      if (!TEACHER) id[t] = v;
       slot[t] = v >= 0 ? to : -1;
+      if (!TEACHER && v >= 0) id[to] = v;
       if (v >= 0) rows[to] = (int32_t)t;
       else if (loss) loss[t] = lse[t] = 0.f;
     }
@@ -100,8 +99,10 @@ __global__ __launch_bounds__(kLiveThreads) void k_live(const I* __restrict__ tar
 
 struct RowsArgs {
   const int32_t* slot;
-  const int32_t* id;       // tokens: the target of each row, or null: picked by k_picked
-  float* picked;           // tokens x k, the targets' logits
+  const int32_t* teacher_id;   // tokens x k, or null: targets alone, whose ids are there by slot
+  const float* teacher_q;
+  int32_t* id;             // by slot of the call, kp each
+  float* q;
   const float* lse;        // tokens, or null: base, scale and g are k_join's
   const float* dloss;
   float* base;             // by slot of the call
@@ -110,38 +111,39 @@ struct RowsArgs {
   float tau;
 };
 
-// Every row by itself, a wave each: a live one goes to its slot of xs, logit is the dot product with a row of w; another's dx is zeros.
+// Every row by itself, a wave each: a live one, and its teacher's entries, go to its
+// slot; another's dx is zeros.
 template <class T>
 __global__ __launch_bounds__(256) void k_rows(LossArgs a, RowsArgs o, T* __restrict__ xs, T* __restrict__ dx) {
   const int lane = threadIdx.x & 63;
   const int64_t t = block_index() * 4 + (threadIdx.x >> 6);
   if (t >= a.tokens) return;
-  const int32_t s = o.slot[t], v = s >= 0 && o.id ? o.id[t] : -1;
+  const int32_t s = o.slot[t];
   const T* x = static_cast<const T*>(a.x) + t * a.dim;
-  const T* w = static_cast<const T*>(a.w) + (int64_t)(v < 0 ? 0 : v) * a.ld;
   if (s < 0) {
     const float zero[8] = {};
     if (dx)
       for (int32_t c = lane * 8; c < a.dim; c += 512) store8(dx + t * a.dim + c, a.dim - c < 8 ? a.dim - c : 8, zero);
     return;
   }
-  float sum = 0.f;
-  {
-#pragma unroll 4
-    for (int32_t c = lane * 8; c < a.dim; c += 512) {
-      const int cnt = a.dim - c < 8 ? a.dim - c : 8;
-      float p[8], q[8];
-      load8(x + c, cnt, p);
-      load8(w + c, v >= 0 ? cnt : 0, q);
-      store8(xs + (int64_t)s * a.ld + c, a.ld - c < 8 ? a.ld - c : 8, p);   // past dim: zeros
+  for (int32_t c = lane * 8; c < a.dim; c += 2048) {
+    float p[4][8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum += p[i] * q[i];
+    for (int u = 0; u < 4; ++u) {
+      const int32_t at = c + 512 * u, left = a.dim - at;
+      load8(x + at, left < 0 ? 0 : left < 8 ? left : 8, p[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {   // past dim: zeros
+      const int32_t at = c + 512 * u, left = a.ld - at;
+      if (left > 0) store8(xs + (int64_t)s * a.ld + at, left < 8 ? left : 8, p[u]);
     }
   }
-  if (v >= 0) {
-    sum = wave_sum(sum);
-    if (lane == 0) o.picked[t] = sum;
-  }
+  if (o.teacher_id)
+    for (int32_t i = lane; i < a.kp; i += 64) {
+      o.id[(int64_t)s * a.kp + i] = i < a.k ? o.teacher_id[t * a.k + i] : -1;
+      o.q[(int64_t)s * a.kp + i] = i < a.k ? o.teacher_q[t * a.k + i] : 0.f;
+    }
   if (o.lse && lane == 0) {   // exp(-lse) = 2^-base scale, base a whole number
     const float lse = o.lse[t], base = rintf(lse * kLog2e);
     o.base[s] = base;
@@ -164,33 +166,16 @@ __global__ __launch_bounds__(256) void k_pad(const bf16_t* __restrict__ w, int64
 
 // ------------------------------------------------------------------- targets
 
-// The logits of a teacher's entries: a wave has one, picked[t][j] = <x, w_id>.
-template <class T>
-__global__ __launch_bounds__(256) void k_picked(LossArgs a, const int32_t* __restrict__ id, int32_t k,
-                                                float* __restrict__ picked) {
-  const int lane = threadIdx.x & 63;
-  const int64_t unit = block_index() * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t t = unit / k;
-  if (t >= a.tokens) return;
-  const int32_t v = id[unit];
-  if (v < 0) return;
-  const float sum = row_dot(static_cast<const T*>(a.x) + t * a.dim, static_cast<const T*>(a.w) + (int64_t)v * a.ld,
-                            a.dim, lane);
-  if (lane == 0) picked[unit] = sum;
-}
-
 struct JoinArgs {
-  const int32_t* id;       // tokens x k
-  const float* q;          // tokens x k, or null: 1
+  const float* q;          // [chunk][kp], or null: 1
   const float* term;       // tokens, or null: 0
-  const float* picked;     // tokens x k
   const float* dloss;      // tokens, or null
   float* base;             // [chunk], these three: LossArgs; g null without gradients
   float* scale;
   float* g;
   float* loss;             // tokens
   float* lse;              // tokens
-  int32_t k, slabs;
+  int32_t slabs;
   float tau;
 };
 
@@ -198,6 +183,7 @@ struct JoinArgs {
 // of each slab's pairs) and 64 groups that go through the slabs side by side, then
 // a wave for each slot.  8192 rows of 500 slabs (33 MB): 10 us; one row: 5 us.
 constexpr int kJoinRows = 16;
+template <class T>
 __global__ __launch_bounds__(1024) void k_join(LossArgs a, JoinArgs j) {
   __shared__ float tops[16][kJoinRows + 1], sums[16][kJoinRows + 1];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -238,9 +224,9 @@ __global__ __launch_bounds__(1024) void k_join(LossArgs a, JoinArgs j) {
   const int64_t t = a.ch.rows[a.ch.slot0 + s];
   const float log_sum = logf(sum);
   float off = 0.f;
-  for (int32_t i = lane; i < j.k; i += 64)
-    if (j.id[t * j.k + i] >= 0)
-      off += (j.q ? j.q[t * j.k + i] : 1.f) * loss_term(a, j.picked[t * j.k + i], n, log_sum);
+  for (int32_t i = lane; i < a.kp; i += 64)
+    if (a.ids[s * a.kp + i] >= 0)
+      off += (j.q ? j.q[s * a.kp + i] : 1.f) * loss_term<T>(a, a.picked[s * a.kp + i], n, log_sum);
   off = wave_sum(off);
   if (lane) return;
   j.loss[t] = j.tau * j.tau * ((j.term ? j.term[t] : 0.f) + off);
@@ -253,16 +239,17 @@ __global__ __launch_bounds__(1024) void k_join(LossArgs a, JoinArgs j) {
 }
 
 // A target's entry of dl: an id that comes more than once counts with the sum of
-// its weights.  All lanes bring the same row and id.
-__device__ __forceinline__ float weight_of(const JoinArgs& j, int64_t t, int32_t v, int lane) {
+// its weights.  All lanes bring the same slot and id.
+__device__ __forceinline__ float weight_of(const LossArgs& a, const JoinArgs& j, int64_t s, int32_t v, int lane) {
   if (!j.q) return 1.f;   // k is 1
   float q = 0.f;
-  for (int32_t i = lane; i < j.k; i += 64) q += j.id[t * j.k + i] == v ? j.q[t * j.k + i] : 0.f;
+  for (int32_t i = lane; i < a.kp; i += 64) q += a.ids[s * a.kp + i] == v ? j.q[s * a.kp + i] : 0.f;
   return wave_sum(q);
 }
+template <class T>
 __device__ __forceinline__ float target_entry(const LossArgs& a, float picked, float q, float base, float scale,
                                               float g) {
-  return (__builtin_amdgcn_exp2f(exponent(a, picked, base, 0.f)) * scale - q) * g;
+  return (__builtin_amdgcn_exp2f(exponent(a, picked, base, T())) * scale - q) * g;
 }
 
 __device__ __forceinline__ void load_exps(const bf16_t* p, int cnt, float (&v)[8]) {
@@ -289,7 +276,6 @@ __global__ __launch_bounds__(256) void k_rescale(LossArgs a, JoinArgs j, int32_t
   const int64_t s = unit / units;
   if (s >= live_slots(a.ch)) return;
   const int32_t first = (int32_t)(unit - s * units) * kScaleCols;
-  const int64_t t = a.ch.rows[a.ch.slot0 + s];
   const float base = a.base[s], scale = a.scale[s], g = a.g[s];
   T* p = static_cast<T*>(a.dl) + s * a.dl_ld;
   float v[kScaleRuns][8];
@@ -304,15 +290,15 @@ __global__ __launch_bounds__(256) void k_rescale(LossArgs a, JoinArgs j, int32_t
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[u][i] *= by;
   }
-  for (int32_t j0 = 0; j0 < j.k; j0 += 64) {
+  for (int32_t j0 = 0; j0 < a.kp; j0 += 64) {
     const int32_t at = j0 + lane;
-    const int32_t id = at < j.k ? j.id[t * j.k + at] : -1;
+    const int32_t id = at < a.kp ? a.ids[s * a.kp + at] : -1;
     uint64_t hits = __ballot(id >= first && id - first < kScaleCols);
     while (hits) {
       const int h = __ffsll((unsigned long long)hits) - 1;
       hits &= hits - 1;
       const int32_t e = __builtin_amdgcn_readlane(id, h), c = e - first;
-      const float d = target_entry(a, j.picked[t * j.k + j0 + h], weight_of(j, t, e, lane), base, scale, g);
+      const float d = target_entry<T>(a, a.picked[s * a.kp + j0 + h], weight_of(a, j, s, e, lane), base, scale, g);
 #pragma unroll
       for (int u = 0; u < kScaleRuns; ++u)
 #pragma unroll
@@ -329,13 +315,12 @@ __global__ __launch_bounds__(256) void k_targets(LossArgs a, JoinArgs j) {
   const int lane = threadIdx.x & 63;
   const int64_t s = block_index() * 4 + (threadIdx.x >> 6);
   if (s >= live_slots(a.ch)) return;
-  const int64_t t = a.ch.rows[a.ch.slot0 + s];
   const float base = a.base[s], scale = a.scale[s], g = a.g[s];
   T* dl = static_cast<T*>(a.dl) + s * a.dl_ld;
-  for (int32_t i = 0; i < j.k; ++i) {
-    const int32_t v = __builtin_amdgcn_readfirstlane(j.id[t * j.k + i]);
+  for (int32_t i = 0; i < a.k; ++i) {
+    const int32_t v = __builtin_amdgcn_readfirstlane(a.ids[s * a.kp + i]);
     if (v < 0) continue;
-    const float d = target_entry(a, j.picked[t * j.k + i], weight_of(j, t, v, lane), base, scale, g);
+    const float d = target_entry<T>(a, a.picked[s * a.kp + i], weight_of(a, j, s, v, lane), base, scale, g);
     if (lane == 0) store1(dl + v, d);
   }
 }
@@ -375,12 +360,15 @@ int64_t chunk_slots(int dtype, int64_t tokens, int64_t vocab, bool grads, bool s
   return most < 1 ? 1 : most;
 }
 
+// Places of a slot's targets: whole 16-byte fours, or one.
+int32_t places(int32_t k) { return k == 1 ? 1 : (k + 3) / 4 * 4; }
+
 struct LossSpace {
   bool few;
   int64_t chunk, slabs, dl_ld;
   ProductParts parts;
   int32_t ld;
-  uint64_t xs, w, sums_of_parts, id, q, term, rows, slot, count, stats, picked, base, scale, g, dl, sums, bytes;
+  uint64_t xs, w, sums_of_parts, teacher_id, teacher_q, id, q, term, rows, slot, count, stats, picked, base, scale, g, dl, sums, bytes;
 };
 LossSpace loss_space(int dtype, int64_t tokens, int64_t vocab, int64_t dim, int k, bool teacher, bool grads,
                      bool given) {
@@ -389,6 +377,7 @@ LossSpace loss_space(int dtype, int64_t tokens, int64_t vocab, int64_t dim, int 
   if (!grads && few_rows(dtype, tokens, dim)) {
     l.few = true;
     l.stats = p.take((uint64_t)few_blocks(vocab) * tokens * 8);
+    l.picked = p.take((uint64_t)tokens * k * 4);
     l.bytes = p.used;
     return l;
   }
@@ -404,14 +393,16 @@ LossSpace loss_space(int dtype, int64_t tokens, int64_t vocab, int64_t dim, int 
   const uint64_t of_dx = l.parts.dx > 1 ? (uint64_t)l.parts.dx * l.chunk * l.ld * 4 : 0;
   const uint64_t of_dw = l.parts.dw > 1 ? (uint64_t)l.parts.dw * vocab * l.ld * 4 : 0;
   l.sums_of_parts = p.take(of_dx > of_dw ? of_dx : of_dw);   // one after the other
-  l.id = p.take((uint64_t)tokens * k * 4);
-  l.q = p.take(teacher ? (uint64_t)tokens * k * 4 : 0);
+  l.teacher_id = p.take(teacher ? (uint64_t)tokens * k * 4 : 0);
+  l.teacher_q = p.take(teacher ? (uint64_t)tokens * k * 4 : 0);
+  l.id = p.take((uint64_t)tokens * places(k) * 4);
+  l.q = p.take(teacher ? (uint64_t)tokens * places(k) * 4 : 0);
   l.term = p.take(teacher ? (uint64_t)tokens * 4 : 0);
   l.rows = p.take((uint64_t)tokens * 4);
   l.slot = p.take((uint64_t)tokens * 4);
   l.count = p.take(4);
   l.stats = p.take(given ? 0 : (uint64_t)l.slabs * l.chunk * 8);
-  l.picked = p.take((uint64_t)tokens * k * 4);
+  l.picked = p.take((uint64_t)tokens * places(k) * 4);
   l.base = p.take((uint64_t)tokens * 4);
   l.scale = p.take((uint64_t)tokens * 4);
   l.g = p.take((uint64_t)tokens * 4);
@@ -423,8 +414,8 @@ LossSpace loss_space(int dtype, int64_t tokens, int64_t vocab, int64_t dim, int 
 
 template <class I>
 int find_rows(const Call& c, const LossSpace& l, char* ws, hipStream_t s) {
-  int32_t* id = reinterpret_cast<int32_t*>(ws + l.id);
-  float* q = reinterpret_cast<float*>(ws + l.q);
+  int32_t* id = reinterpret_cast<int32_t*>(ws + (c.teacher ? l.teacher_id : l.id));
+  float* q = reinterpret_cast<float*>(ws + l.teacher_q);
   float* term = reinterpret_cast<float*>(ws + l.term);
   int32_t* rows = reinterpret_cast<int32_t*>(ws + l.rows);
   int32_t* slot = reinterpret_cast<int32_t*>(ws + l.slot);
@@ -468,9 +459,12 @@ int run(const Call& c, const LossSpace& l, char* ws, hipStream_t s) {
   a.to_log2 = (float)to_log2;
   a.to_log2_low = (float)(to_log2 - (double)a.to_log2);
   a.stats = given ? nullptr : reinterpret_cast<float*>(ws + l.stats);
+  a.picked = reinterpret_cast<float*>(ws + l.picked);
   if (l.few)
     return few_loss(a, c.dtype, FewCall{c.targets, c.index_bytes, c.teacher, c.teacher_dtype, c.k, c.tau, c.loss, c.lse},
                     s);
+  a.k = c.k;
+  a.kp = places(c.k);
   a.xs = ws + l.xs;
   a.ld = l.ld;
   a.large = large;
@@ -498,23 +492,18 @@ int run(const Call& c, const LossSpace& l, char* ws, hipStream_t s) {
   float* scale = reinterpret_cast<float*>(ws + l.scale);
   float* g = reinterpret_cast<float*>(ws + l.g);
   float* picked = reinterpret_cast<float*>(ws + l.picked);
-  const int32_t* id = reinterpret_cast<int32_t*>(ws + l.id);
-  RowsArgs o = {reinterpret_cast<int32_t*>(ws + l.slot), c.k == 1 ? id : nullptr, picked, c.lse_in, c.dloss, base, scale,
-                g, c.tau};
+  int32_t* id = reinterpret_cast<int32_t*>(ws + l.id);
+  float* q = reinterpret_cast<float*>(ws + l.q);
+  RowsArgs o = {reinterpret_cast<int32_t*>(ws + l.slot),
+                c.teacher ? reinterpret_cast<int32_t*>(ws + l.teacher_id) : nullptr,
+                reinterpret_cast<float*>(ws + l.teacher_q), id, q, c.lse_in, c.dloss, base, scale, g, c.tau};
   hipLaunchKernelGGL((k_rows<T>), grid_of_blocks(ceil_div(c.tokens, 4), 256), dim3(256), 0, s, a, o,
                      reinterpret_cast<T*>(ws + l.xs), grads ? static_cast<T*>(c.dx) : nullptr);
-  if (c.k > 1)
-    hipLaunchKernelGGL((k_picked<T>), grid_of_blocks(ceil_div(c.tokens * c.k, 4), 256), dim3(256), 0, s, a, id, c.k,
-                       picked);
   JoinArgs j = {};
-  j.id = id;
-  j.q = c.teacher ? reinterpret_cast<float*>(ws + l.q) : nullptr;
   j.term = c.teacher ? reinterpret_cast<float*>(ws + l.term) : nullptr;
-  j.picked = picked;
   j.dloss = c.dloss;
   j.loss = c.loss;
   j.lse = c.lse;
-  j.k = c.k;
   j.slabs = (int32_t)l.slabs;
   j.tau = c.tau;
   const int64_t chunks = ceil_div(c.tokens, l.chunk), slots = l.chunk;
@@ -526,8 +515,11 @@ int run(const Call& c, const LossSpace& l, char* ws, hipStream_t s) {
     a.scale = j.scale = scale + a.ch.slot0;
     a.g = g + a.ch.slot0;
     j.g = grads ? g + a.ch.slot0 : nullptr;
+    a.ids = id + a.ch.slot0 * a.kp;
+    a.picked = picked + a.ch.slot0 * a.kp;
+    j.q = c.teacher ? q + a.ch.slot0 * a.kp : nullptr;
     if ((rc = logits_product(a, c.dtype, given ? kGradient : grads ? kStatsExp : kStats, s))) return rc;
-    if (!given) hipLaunchKernelGGL(k_join, dim3((uint32_t)ceil_div(slots, kJoinRows)), dim3(1024), 0, s, a, j);
+    if (!given) hipLaunchKernelGGL((k_join<T>), dim3((uint32_t)ceil_div(slots, kJoinRows)), dim3(1024), 0, s, a, j);
     if (!grads) continue;
     if (given) {
       hipLaunchKernelGGL((k_targets<T>), grid_of_blocks(ceil_div(slots, 4), 256), dim3(256), 0, s, a, j);

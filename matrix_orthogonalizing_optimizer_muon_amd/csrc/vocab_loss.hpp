@@ -44,6 +44,12 @@ struct LossArgs {
   // logits: exponents of two come as a whole number n and a sum of 2^(l to_log2 - n), so that differences of
   // exponents are exact and nothing is rounded at a logit's size
   float* stats;            // [slab][chunk] pairs (n, the smallest at or above the largest exponent; sum), or null
+  // the targets of a slot of the chunk, kp places each (k, in whole fours where more than one; -1: none), and their
+  // logits, which the logits' product writes as it has them in its sums: a loss near zero, or a probability near
+  // one, is a difference of the two
+  const int32_t* ids;
+  float* picked;
+  int32_t k, kp;
   // by slot of the chunk: probabilities are 2^(l to_log2 - base) scale; g is dloss times temperature
   const float* base;
   const float* scale;
@@ -67,7 +73,8 @@ __device__ __forceinline__ int32_t live_slots(const Chunk& c) {
   return left < 0 ? 0 : left < c.size ? (int32_t)left : c.size;
 }
 
-// The exponent of two of a logit, less n.  In fp32 with both parts of the factor.
+// The exponent of two of a logit, less n.  In fp32 with both parts of the factor; a
+// target's has to be what its sum was made with.
 __device__ __forceinline__ float exponent(const LossArgs& a, float l, float n, float) {
   return fmaf(l, a.to_log2_low, fmaf(l, a.to_log2, -n));
 }
@@ -87,24 +94,9 @@ __device__ __forceinline__ void merge_sums(float& n, float& sum, float n2, float
 }
 // The log of sum 2^n, from that of sum; and lse - l / tau of a logit.
 __device__ __forceinline__ float log_of(float n, float log_sum) { return fmaf(n, kLn2, fmaf(n, kLn2Low, log_sum)); }
-__device__ __forceinline__ float loss_term(const LossArgs& a, float l, float n, float log_sum) {
-  return log_sum - exponent(a, l, n, 0.f) * kLn2;
-}
-
-// <x, w> of two rows, by a wave.
 template <class T>
-__device__ __forceinline__ float row_dot(const T* x, const T* w, int32_t dim, int lane) {
-  float sum = 0.f;
-#pragma unroll 4
-  for (int32_t c = lane * 8; c < dim; c += 512) {
-    const int cnt = dim - c < 8 ? dim - c : 8;
-    float p[8], q[8];
-    load8(x + c, cnt, p);
-    load8(w + c, cnt, q);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sum += p[i] * q[i];
-  }
-  return wave_sum(sum);
+__device__ __forceinline__ float loss_term(const LossArgs& a, float l, float n, float log_sum) {
+  return log_sum - exponent(a, l, n, T()) * kLn2;
 }
 
 // A teacher's entries of a row, lane l those of l + 64 i: ids, -1 where there is

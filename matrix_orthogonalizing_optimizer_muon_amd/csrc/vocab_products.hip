@@ -39,6 +39,47 @@ __device__ __forceinline__ void store_exps(bf16_t* p, int cnt, const float* v) {
 }
 __device__ __forceinline__ void store_exps(float* p, int cnt, const float* v) { store4(p, cnt, v); }
 
+// Writes the targets' logits that a wave has: lane l those of row l % 32 (slot s, or
+// -1: none) in columns first + 32 (v / 16) + 8 (v % 16 / 4) + 4 (l / 32) + v % 4 for v < N,
+// of value(v).  `id`: the only target of each row, where k is one.
+template <int N, class Value>
+__device__ __forceinline__ void pick(const LossArgs& a, int32_t first, int64_t s, int32_t id, int lane, Value value) {
+  const int half = lane >> 5;
+  if (a.kp == 1) {
+    const int32_t c = id - first;
+    const bool hit = id >= first && c < 2 * N && ((c >> 2) & 1) == half;
+    if (!__any(hit)) return;
+    const int32_t at = (c >> 5) * 16 + ((c >> 3) & 3) * 4 + (c & 3);
+    float x = 0.f;
+#pragma unroll
+    for (int v = 0; v < N; ++v) x = at == v ? value(v) : x;
+    if (hit) a.picked[s] = x;
+    return;
+  }
+  // the two lanes of a row look at fours of its places in turn; a hit goes to the lane that has its column
+  const int32_t* ids = a.ids + (s < 0 ? 0 : s) * a.kp;
+  for (int32_t j0 = 0; j0 < a.kp; j0 += 8) {
+    const int32_t j = j0 + 4 * half;
+    u32x4 four = {~0u, ~0u, ~0u, ~0u};
+    if (s >= 0 && j < a.kp) four = *reinterpret_cast<const u32x4*>(ids + j);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int32_t mine = (int32_t)four[u];
+      uint64_t hits = __ballot(mine >= first && mine - first < 2 * N);
+      while (hits) {
+        const int h = __ffsll((unsigned long long)hits) - 1;
+        hits &= hits - 1;
+        const int32_t c = __builtin_amdgcn_readlane(mine, h) - first;
+        const int32_t at = (c >> 5) * 16 + ((c >> 3) & 3) * 4 + (c & 3);
+        float x = 0.f;
+#pragma unroll
+        for (int v = 0; v < N; ++v) x = at == v ? value(v) : x;
+        if (lane == (h & 31) + 32 * ((c >> 2) & 1)) a.picked[s * a.kp + j0 + 4 * (h >> 5) + u] = x;
+      }
+    }
+  }
+}
+
 // One output tile per block of 4 waves (2 x 2) and two LDS stages, as
 // k_product's of the expert layer.  fp32: a k-tile's sum (32 products) is added to
 // the total by itself, so that no value is rounded K / 2 times in a row (errors of
@@ -151,6 +192,8 @@ __global__ __launch_bounds__(256) void k_tile(LossArgs a, int32_t tiles_n) {
     const int32_t c0 = n0 + wx * W + 4 * (lane >> 5);
     if constexpr (PRODUCT == kLogits) {
       if (n0 + wx * W >= a.vocab) continue;   // uniform over the wave
+      pick<16 * NT>(a, n0 + wx * W, exists ? r : -1, exists && a.kp == 1 ? a.ids[r] : -1, lane,
+                    [&](int v) { return acc[i][v / 16][v % 16]; });
       float e[NT][16];
 #pragma unroll
       for (int j = 0; j < NT; ++j)
@@ -257,6 +300,12 @@ struct LogitsWalk {
     const int32_t left = a.vocab - first;   // columns of the slab that exist, where less than 64
     const int c = 4 * (lane >> 5);
     const auto rs = nt::make_rsrc(static_cast<char*>(a.dl) + ((int64_t)t.m0 * a.dl_ld + first) * 2, kRange);
+    int32_t ids[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int32_t r = t.m0 + row0 + 32 * i + (lane & 31);
+      ids[i] = a.kp == 1 && i < mt && r < live ? a.ids[r] : -1;
+    }
     float bases[4], scales[4];
     if constexpr (EPI == kGradient) {   // all rows' at once
 #pragma unroll
@@ -322,6 +371,12 @@ struct LogitsWalk {
           __builtin_amdgcn_raw_buffer_store_b128(v, rs, at, 0, 0);
         }
       }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i >= mt) break;
+      const int32_t r = t.m0 + row0 + 32 * i + (lane & 31);
+      pick<32>(a, first, r < live ? r : -1, ids[i], lane, [&](int v) { return acc[i][v / 16][v % 16]; });
     }
     return 0;
   }

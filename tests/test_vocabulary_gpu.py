@@ -334,6 +334,28 @@ def test_large_and_equal_logits():
     close(loss, torch.full((3,), math.log(512)).double(), want.abs() * 12 * ULP + (512 + 8) * ULP, "loss")
 
 
+@pytest.mark.parametrize("dtype", [F, B], ids=str)
+@pytest.mark.parametrize("tokens,vocab,dim", [(5, 1000, 64), (150, 700, 128), (150, 701, 65)])
+def test_losses_near_zero(tokens, vocab, dim, dtype):
+    """A loss is log(1 + sum over the others of exp(l_v - l_y)): the target's logit in its sum and the one taken off
+    are the same number, whatever it was rounded by.  So the loss is off by the others' part of it, their differences
+    to the target's off by 2 dz and two roundings of each, and by a few roundings at the size of 1."""
+    g = gen(tokens + dim)
+    w = (torch.randn(vocab, dim, generator=g) / math.sqrt(dim)).to(dtype)
+    y = torch.randint(0, vocab, (tokens,), generator=g)
+    x = (torch.randn(tokens, dim, generator=g) * 0.5 + torch.linspace(14, 40, tokens)[:, None] * w[y].float()).to(dtype)
+    loss, _ = M.classifier_loss(x.cuda(), w.cuda(), y.cuda())
+    both = M.classifier_loss_grads(torch.ones(tokens).cuda(), x.cuda(), w.cuda(), y.cuda())[0]
+    z = x.double() @ w.double().t()
+    others = torch.where(torch.arange(vocab) == y[:, None], -inf, z - z.gather(1, y[:, None]))
+    want = torch.log1p(others.exp().sum(1))
+    assert float(want.min()) < 1e-3
+    dz = (x.double().abs() @ w.double().abs().t()).max(1).values * dim * ULP
+    bound = want * 2 * (2 * dz + 8 * ULP * z.abs().max(1).values + (vocab + 8) * ULP) + 4 * ULP
+    close(loss, want, bound, "loss")
+    close(both, want, bound, "loss with gradients")
+
+
 def test_overflow_of_a_logit_is_nan_in_its_row_alone():
     x, w, dloss, ids, _ = inputs(66, 140, 32, F, 0, 4, absent=0.0)
     x[7] = 3e38
