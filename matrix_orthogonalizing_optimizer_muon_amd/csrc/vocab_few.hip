@@ -70,18 +70,26 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_few_logits(LossArgs a, const
       for (int b = 0; b < NB; ++b)
         acc[b] = multiply16(f, *reinterpret_cast<const u32x4*>(xp + b * 16 * ld + s * 64), acc[b], T());
     }
+    // the rows' ids a wave's width at a time: few are among these 16
+    for (int32_t i0 = 0; i0 < rows * k; i0 += 64) {
+      const uint64_t id = i0 + lane < rows * k ? (uint64_t)(int64_t)ids[i0 + lane] : ~uint64_t(0);
+      const uint64_t off = id - (uint64_t)r0;   // below: huge
+      uint64_t hits = __ballot(off < 16 && id < (uint64_t)a.vocab);
+      while (hits) {
+        const int h = __ffsll((unsigned long long)hits) - 1;
+        hits &= hits - 1;
+        const int c = __builtin_amdgcn_readlane((int32_t)off, h), t = (i0 + h) / k;
+        float x = 0.f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x = t >> 4 == b && (c & 3) == i ? acc[b][i] : x;
+        if (lane == (t & 15) + 16 * (c >> 2)) a.picked[i0 + h] = x;
+      }
+    }
     const int32_t left = a.vocab - r0 - 4 * (lane >> 4);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      const int32_t t = 16 * b + (lane & 15);
-      if (t < rows) {
-#pragma unroll 4
-        for (int32_t j = 0; j < k; ++j) {
-          const uint64_t c = (uint64_t)(int64_t)ids[t * k + j] - (uint64_t)(r0 + 4 * (lane >> 4));   // below: huge
-          if (c < 4 && (int32_t)c < left)
-            a.picked[t * k + j] = c < 2 ? (c == 0 ? acc[b][0] : acc[b][1]) : c == 2 ? acc[b][2] : acc[b][3];
-        }
-      }
       float top = -INFINITY, add = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i)

@@ -39,46 +39,77 @@ __device__ __forceinline__ void store_exps(bf16_t* p, int cnt, const float* v) {
 }
 __device__ __forceinline__ void store_exps(float* p, int cnt, const float* v) { store4(p, cnt, v); }
 
-// Writes the targets' logits that a wave has: lane l those of row l % 32 (slot s, or
-// -1: none) in columns first + 32 (v / 16) + 8 (v % 16 / 4) + 4 (l / 32) + v % 4 for v < N,
-// of value(v).  `id`: the only target of each row, where k is one.
+// The targets' logits that a wave has go to picked: lane l has those of row l % 32
+// (slot s, or -1: none) in columns first + 32 (v / 16) + 8 (v % 16 / 4) + 4 (l / 32) + v % 4
+// for v < N, of value(v).
+__device__ __forceinline__ int32_t value_at(int32_t c) { return (c >> 5) * 16 + ((c >> 3) & 3) * 4 + (c & 3); }
+
+// `id`: the only target of the lane's row.
 template <int N, class Value>
-__device__ __forceinline__ void pick(const LossArgs& a, int32_t first, int64_t s, int32_t id, int lane, Value value) {
-  const int half = lane >> 5;
-  if (a.kp == 1) {
-    const int32_t c = id - first;
-    const bool hit = id >= first && c < 2 * N && ((c >> 2) & 1) == half;
-    if (!__any(hit)) return;
-    const int32_t at = (c >> 5) * 16 + ((c >> 3) & 3) * 4 + (c & 3);
-    float x = 0.f;
+__device__ __forceinline__ void pick_one(const LossArgs& a, int32_t first, int64_t s, int32_t id, int lane,
+                                         Value value) {
+  const int32_t c = id - first;
+  const bool hit = id >= first && c < 2 * N && ((c >> 2) & 1) == lane >> 5;
+  if (!__any(hit)) return;
+  const int32_t at = value_at(c);
+  float x = 0.f;
 #pragma unroll
-    for (int v = 0; v < N; ++v) x = at == v ? value(v) : x;
-    if (hit) a.picked[s] = x;
-    return;
+  for (int v = 0; v < N; ++v) x = at == v ? value(v) : x;
+  if (hit) a.picked[s] = x;
+}
+
+// 32 places of a row, 16 in each of its lanes: places j0 + 8 n + 4 (l / 32) + 0..3.
+struct Places {
+  u32x4 id[4];
+  __device__ __forceinline__ void load(const LossArgs& a, int64_t s, int32_t j0, int lane) {
+    const int32_t* p = a.ids + (s < 0 ? 0 : s) * a.kp;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const int32_t j = j0 + 8 * n + 4 * (lane >> 5);
+      id[n] = u32x4{~0u, ~0u, ~0u, ~0u};
+      if (s >= 0 && j < a.kp) id[n] = *reinterpret_cast<const u32x4*>(p + j);
+    }
   }
-  // the two lanes of a row look at fours of its places in turn; a hit goes to the lane that has its column
-  const int32_t* ids = a.ids + (s < 0 ? 0 : s) * a.kp;
-  for (int32_t j0 = 0; j0 < a.kp; j0 += 8) {
-    const int32_t j = j0 + 4 * half;
-    u32x4 four = {~0u, ~0u, ~0u, ~0u};
-    if (s >= 0 && j < a.kp) four = *reinterpret_cast<const u32x4*>(ids + j);
+  // A hit goes to the lane that has its column.  A lane notes one of its hits, as is
+  // mostly all there is: k / (vocab / 64) for a row.
+  template <int N, class Value>
+  __device__ __forceinline__ void pick(const LossArgs& a, int32_t first, int64_t s, int32_t j0, int lane,
+                                       Value value) const {
+    uint32_t note = 0, count = 0;   // place of the lane's 16, column
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int32_t mine = (int32_t)four[u];
-      uint64_t hits = __ballot(mine >= first && mine - first < 2 * N);
+    for (int e = 0; e < 16; ++e) {
+      const uint32_t c = id[e / 4][e % 4] - (uint32_t)first;   // -1: far above
+      note = c < 2 * N ? c + 256 * e : note;
+      count += c < 2 * N;
+    }
+    uint64_t hits = __ballot(count == 1);
+    while (hits) {
+      const int h = __ffsll((unsigned long long)hits) - 1;
+      hits &= hits - 1;
+      const uint32_t n = __builtin_amdgcn_readlane(note, h);
+      give<N>(a, s, j0, h, n >> 8, n & 255, lane, value);
+    }
+    if (!__any(count > 1)) return;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      hits = __ballot(count > 1 && id[e / 4][e % 4] - (uint32_t)first < 2 * N);
       while (hits) {
         const int h = __ffsll((unsigned long long)hits) - 1;
         hits &= hits - 1;
-        const int32_t c = __builtin_amdgcn_readlane(mine, h) - first;
-        const int32_t at = (c >> 5) * 16 + ((c >> 3) & 3) * 4 + (c & 3);
-        float x = 0.f;
-#pragma unroll
-        for (int v = 0; v < N; ++v) x = at == v ? value(v) : x;
-        if (lane == (h & 31) + 32 * ((c >> 2) & 1)) a.picked[s * a.kp + j0 + 4 * (h >> 5) + u] = x;
+        give<N>(a, s, j0, h, e, __builtin_amdgcn_readlane(id[e / 4][e % 4], h) - (uint32_t)first, lane, value);
       }
     }
   }
-}
+  template <int N, class Value>
+  static __device__ __forceinline__ void give(const LossArgs& a, int64_t s, int32_t j0, int h, uint32_t e, uint32_t c,
+                                              int lane, Value value) {
+    const int32_t at = value_at((int32_t)c);
+    float x = 0.f;
+#pragma unroll
+    for (int v = 0; v < N; ++v) x = at == v ? value(v) : x;
+    if (lane == (h & 31) + 32 * (int)((c >> 2) & 1)) a.picked[s * a.kp + j0 + 8 * (e >> 2) + 4 * (h >> 5) + (e & 3)] = x;
+  }
+};
 
 // One output tile per block of 4 waves (2 x 2) and two LDS stages, as
 // k_product's of the expert layer.  fp32: a k-tile's sum (32 products) is added to
@@ -192,8 +223,17 @@ __global__ __launch_bounds__(256) void k_tile(LossArgs a, int32_t tiles_n) {
     const int32_t c0 = n0 + wx * W + 4 * (lane >> 5);
     if constexpr (PRODUCT == kLogits) {
       if (n0 + wx * W >= a.vocab) continue;   // uniform over the wave
-      pick<16 * NT>(a, n0 + wx * W, exists ? r : -1, exists && a.kp == 1 ? a.ids[r] : -1, lane,
-                    [&](int v) { return acc[i][v / 16][v % 16]; });
+      const int64_t slot = exists ? r : -1;
+      auto value = [&](int v) { return acc[i][v / 16][v % 16]; };
+      if (a.kp == 1) {
+        pick_one<16 * NT>(a, n0 + wx * W, slot, exists ? a.ids[r] : -1, lane, value);
+      } else {
+        for (int32_t j0 = 0; j0 < a.kp; j0 += 32) {
+          Places p;
+          p.load(a, slot, j0, lane);
+          p.template pick<16 * NT>(a, n0 + wx * W, slot, j0, lane, value);
+        }
+      }
       float e[NT][16];
 #pragma unroll
       for (int j = 0; j < NT; ++j)
@@ -300,11 +340,31 @@ struct LogitsWalk {
     const int32_t left = a.vocab - first;   // columns of the slab that exist, where less than 64
     const int c = 4 * (lane >> 5);
     const auto rs = nt::make_rsrc(static_cast<char*>(a.dl) + ((int64_t)t.m0 * a.dl_ld + first) * 2, kRange);
-    int32_t ids[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    auto slot = [&](int i) {
       const int32_t r = t.m0 + row0 + 32 * i + (lane & 31);
-      ids[i] = a.kp == 1 && i < mt && r < live ? a.ids[r] : -1;
+      return i < mt && r < live ? r : -1;
+    };
+    // targets first: behind the stores of results their ids would wait for these
+    if (a.kp == 1) {
+      int32_t ids[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ids[i] = slot(i) >= 0 ? a.ids[slot(i)] : -1;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < mt) pick_one<32>(a, first, slot(i), ids[i], lane, [&](int v) { return acc[i][v / 16][v % 16]; });
+    } else {
+      Places now, then;   // the next places on their way while these are looked at
+      now.load(a, slot(0), 0, lane);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i >= mt) break;
+        for (int32_t j0 = 0; j0 < a.kp; j0 += 32) {
+          if (j0 + 32 < a.kp) then.load(a, slot(i), j0 + 32, lane);
+          else then.load(a, i < 3 ? slot(i + 1) : -1, 0, lane);
+          now.template pick<32>(a, first, slot(i), j0, lane, [&](int v) { return acc[i][v / 16][v % 16]; });
+          now = then;
+        }
+      }
     }
     float bases[4], scales[4];
     if constexpr (EPI == kGradient) {   // all rows' at once
@@ -371,12 +431,6 @@ struct LogitsWalk {
           __builtin_amdgcn_raw_buffer_store_b128(v, rs, at, 0, 0);
         }
       }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (i >= mt) break;
-      const int32_t r = t.m0 + row0 + 32 * i + (lane & 31);
-      pick<32>(a, first, r < live ? r : -1, ids[i], lane, [&](int v) { return acc[i][v / 16][v % 16]; });
     }
     return 0;
   }
