@@ -477,3 +477,103 @@ def test_a_tensor_that_requires_grad_is_refused():
         M.classifier_loss(x, w, targets)
     with torch.no_grad():
         M.classifier_loss(x, w, targets)
+
+
+# ------------------------------------------------------------------ entry points
+
+def test_outputs_off_16_bytes():
+    """The entry point writes dx and dw at any alignment of their type, and nothing beside them."""
+    import ctypes
+    from matrix_orthogonalizing_optimizer_muon_amd import _lib as L
+    for tokens, vocab, dim in ((300, 520, 72), (70, 33, 8)):
+        x, w, dloss, ids, _ = (None if t is None else t.cuda() for t in inputs(tokens, vocab, dim, B, 0, 31))
+        want = M.classifier_loss_grads(dloss, x, w, ids)
+        need = ctypes.c_uint64()
+        assert L.lib().muon_classifier_loss_workspace(1, tokens, vocab, dim, 1, ctypes.byref(need)) == 0
+        ws = torch.empty(need.value, dtype=torch.uint8, device="cuda")
+        loss, lse = torch.empty(tokens, device="cuda"), torch.empty(tokens, device="cuda")
+        dx, dw = (torch.full((t.numel() + 16,), 7.0, dtype=B, device="cuda") for t in (x, w))
+        assert L.lib().muon_classifier_loss_grads(
+            dloss.data_ptr(), x.data_ptr(), w.data_ptr(), ids.data_ptr(), 8, 1, tokens, vocab, dim, loss.data_ptr(),
+            lse.data_ptr(), dx.data_ptr() + 2, dw.data_ptr() + 2, ws.data_ptr(), need.value,
+            torch.cuda.current_stream().cuda_stream) == 0
+        torch.cuda.synchronize()
+        for got, t in ((dx, want[2]), (dw, want[3])):
+            assert torch.equal(got[1:1 + t.numel()].view(t.shape), t)
+            assert bool((got[0] == 7).all() and (got[1 + t.numel():] == 7).all())
+        assert torch.equal(loss, want[0]) and torch.equal(lse, want[1])
+
+
+def test_given_lse_is_taken_as_it_is():
+    """The backward pass goes by the lse that it is given, a shifted one too."""
+    x, w, dloss, ids, _ = inputs(90, 200, 40, F, 0, 41, absent=0.0)
+    at, q = O.target_weights(ids, 200)
+    lse = O.loss(x, w, at, q)[1].float() + 0.25
+    dx, dw = M.classifier_loss_backward(dloss.cuda(), x.cuda(), w.cuda(), ids.cuda(), lse.cuda())
+    want = O.grads(dloss, x, w, at, q, 1.0, lse)
+    b = bounds_of(x, w, dloss, at, q, torch.zeros(90, dtype=torch.float64), 1.0, 1)
+    close(dx, want[0], b[2] + HALF[F] * (want[0].abs() + b[2]), "dx")
+    close(dw, want[1], b[3] + HALF[F] * (want[1].abs() + b[3]), "dw")
+
+
+@pytest.mark.parametrize("dtype", [F, B], ids=str)
+def test_gradients_against_differences(dtype):
+    """The loss's own differences: moving x and w along a direction by h moves the loss by <gradient, direction> h, up
+    to h^2 / 2 times the curvature along it and twice the loss's rounding over h."""
+    x, w, dloss, ids, teacher = inputs(40, 120, 32, F, 3, 17, absent=0.1)
+    x, w = x.to(dtype).float(), w.to(dtype).float()
+    g = gen(18)
+    vx, vw = torch.randn(x.shape, generator=g), torch.randn(w.shape, generator=g) / 32 ** 0.5
+    dloss = dloss.abs()
+
+    def total(a, b):
+        loss, _ = M.distill_loss(a.cuda(), b.cuda(), teacher.cuda(), ids.cuda(), temperature=2.0)
+        return float((loss.double().cpu() * dloss).sum())
+    dx, dw = M.distill_loss_grads(dloss.cuda(), x.to(dtype).cuda(), w.to(dtype).cuda(), teacher.cuda(), ids.cuda(),
+                                  temperature=2.0)[2:]
+    slope = float((dx.cpu().double() * vx).sum() + (dw.cpu().double() * vw).sum())
+    h = 2.0 ** -7
+    got = (total(x + h * vx, w + h * vw) - total(x - h * vx, w - h * vw)) / (2 * h)
+    # third derivatives along the direction: those of the same sum in 64 bits, by its own differences
+    def exact(s):
+        at, q = O.teacher_weights(teacher, ids, 120, 2.0)
+        return float((O.loss((x + s * vx).double(), (w + s * vw).double(), at, q, 2.0)[0] * dloss).sum())
+    third = abs(exact(2 * h) - 2 * exact(h) + 2 * exact(-h) - exact(-2 * h)) / (2 * h ** 3)
+    size = float((dx.cpu().double() * vx).abs().sum() + (dw.cpu().double() * vw).abs().sum())
+    rounding = float(dloss.sum()) * 64 * 32 * ULP / h      # of 32-term logits of size 64 at the most
+    assert abs(got - slope) <= third * h * h + rounding + 3 * HALF[dtype] * size, (got, slope)
+
+
+@pytest.mark.parametrize("teacher", [False, True])
+def test_example_runs_and_its_gradients_are_the_losses(teacher):
+    """The model's gradients against differences of its loss along each tensor's gradient: the loss is piecewise smooth
+    in the classifier, the last tensor of the chain, and in the table, the first."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "language_model.py")
+    spec = importlib.util.spec_from_file_location("language_model", path)
+    lm = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(lm)
+    losses, model = lm.train(steps=3, vocab=500, tokens=256, width=64, hidden=64, experts=4)
+    assert all(math.isfinite(v) for v in losses)
+    if teacher:
+        losses, model = lm.train(steps=3, vocab=500, tokens=256, width=64, hidden=64, experts=4, teacher=model, seed=3)
+        assert all(math.isfinite(v) for v in losses)
+    t, y = lm.text(500, 256, 3)
+    top = model.top(t, 16) if teacher else None
+    if top is not None:    # another distribution than the model's own, whose gradient is none
+        top = (top[0].roll(1, dims=1).contiguous(), top[1])
+    _, grads = model.loss_and_grads(t, y, top)
+    for tensor, grad in ((model.classifier, grads[0]), (model.table, grads[1])):
+        keep = tensor.clone()
+        # steps of whole bf16 roundings are lost in weights of size 1/8, so a step is taken of the size of the weights
+        way = grad.float() / grad.float().norm() * keep.float().norm() * 0.05
+        sides = []
+        for s in (1, -1):
+            tensor.copy_((keep.float() + s * way).to(B))
+            sides.append((float(model.loss_and_grads(t, y, top)[0]), tensor.float() - keep.float()))
+            tensor.copy_(keep)
+        moved = float(((sides[0][1] - sides[1][1]) * grad.float()).sum())
+        assert moved > 0 and sides[0][0] > sides[1][0]
+        # half a bf16 step in each of the layer's tensors, and the curvature over a step of a twentieth
+        assert abs((sides[0][0] - sides[1][0]) / moved - 1) < 0.15
