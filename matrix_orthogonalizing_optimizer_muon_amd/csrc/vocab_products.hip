@@ -111,11 +111,66 @@ struct Places {
   }
 };
 
+// An fp32 operand's way from memory to its tile (Stager's layout) where 31 bits
+// address a tile's rows: loads through a descriptor and without a branch, so that a
+// wait for one k-tile's leaves the next one's in flight (389 x 4099 x 515, dw: 31 ->
+// 26 us).  Rows that do not exist lie past the descriptor's range or get no address.
+// Of columns that do not, those of a k-contiguous operand are set to zero; of a
+// k-major one they reach only outputs that do not exist.
+template <bool KM>
+struct Stager32 {
+  using G = Tile<float>;
+  static constexpr int CPR = KM ? G::B / G::PER : G::BK / G::PER, ROWS = KM ? G::BK : G::B, NC = ROWS * CPR / 256;
+  const float* base;
+  int64_t ld;
+  int32_t rows, k;      // rows from base on (k-major: of k); k of a k-contiguous operand
+  int32_t cols;         // of a k-major operand, from base on
+  uint32_t voff[NC];
+  u32x4 v[NC];
+
+  // base: row 0 of the tile (k-major: k = 0, its first column); extent: rows, or columns, from there on
+  __device__ __forceinline__ void init(const float* b, int64_t ld_, int32_t extent, int32_t k_) {
+    base = b;
+    ld = ld_;
+    rows = KM ? k_ : extent;
+    k = k_;
+    cols = extent;
+#pragma unroll
+    for (int u = 0; u < NC; ++u) {
+      const int id = u * 256 + (int)threadIdx.x, r = id / CPR, c = id % CPR;
+      const bool ok = KM ? c * G::PER < extent : r < extent;
+      voff[u] = ok ? ((uint32_t)r * (uint32_t)ld + c * G::PER) * 4u : kNone;
+    }
+  }
+  __device__ __forceinline__ void fetch(int64_t k0) {
+    // to the end of the last row's columns: nothing behind the operand is read
+    const int64_t left = (KM ? (rows - k0 - 1) * ld + cols : rows * ld - k0) * 4;
+    const auto rs = nt::make_rsrc(base + (KM ? k0 * ld : k0), left <= 0 ? 0u : left < kRange ? (uint32_t)left : kRange);
+#pragma unroll
+    for (int u = 0; u < NC; ++u) {
+      const int c = (u * 256 + (int)threadIdx.x) % CPR;
+      v[u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, voff[u], 0, 0));
+      if constexpr (!KM) {
+        const int64_t at = k0 + c * G::PER;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[u][i] = at + i < k ? v[u][i] : 0u;
+      }
+    }
+  }
+  __device__ __forceinline__ void commit(char* lds) const {
+#pragma unroll
+    for (int u = 0; u < NC; ++u) {
+      const int id = u * 256 + (int)threadIdx.x, r = id / CPR, c = id % CPR;
+      *reinterpret_cast<u32x4*>(lds + (KM ? G::at_t(r, c) : G::at(r, c))) = v[u];
+    }
+  }
+};
+
 // One output tile per block of 4 waves (2 x 2) and two LDS stages, as
 // k_product's of the expert layer.  fp32: a k-tile's sum (32 products) is added to
 // the total by itself, so that no value is rounded K / 2 times in a row (errors of
 // the gradients of 389 x 4099 x 515: 4.0e-6 -> 1.2e-6 of their norm).
-template <class T, int PRODUCT, int EPI>
+template <class T, int PRODUCT, int EPI, bool SHORT>
 __global__ __launch_bounds__(256) void k_tile(LossArgs a, int32_t tiles_n) {
   using G = Tile<T>;
   constexpr bool PT = PRODUCT == kDw, QT = PRODUCT != kLogits;
@@ -133,15 +188,23 @@ __global__ __launch_bounds__(256) void k_tile(LossArgs a, int32_t tiles_n) {
   const T* xs = static_cast<const T*>(a.xs) + a.ch.slot0 * a.ld;
   int64_t m_left;
   int32_t K;
-  Stager<T, PT> sp;
-  Stager<T, QT> sq;
+  typename std::conditional<SHORT, Stager32<PT>, Stager<T, PT>>::type sp;
+  typename std::conditional<SHORT, Stager32<QT>, Stager<T, QT>>::type sq;
+  typedef decltype(sp) PStager;
+  typedef decltype(sq) QStager;
+  const T* wmat = static_cast<const T*>(a.w);
   if constexpr (PRODUCT == kLogits) {
     m_left = live - m0;
     if (m_left <= 0) return;
     K = a.dim;
-    sp.init(xs, nullptr, m0, m_left, 0, 0, a.dim);
-    sq.init(a.w, nullptr, n0, a.vocab - n0, 0, 0, a.dim);
-    sp.ld = sq.ld = a.ld;
+    if constexpr (SHORT) {
+      sp.init(xs + m0 * a.ld, a.ld, (int32_t)m_left, K);
+      sq.init(wmat + (int64_t)n0 * a.ld, a.ld, a.vocab - n0, K);
+    } else {
+      sp.init(xs, nullptr, m0, m_left, 0, 0, a.dim);
+      sq.init(wmat, nullptr, n0, a.vocab - n0, 0, 0, a.dim);
+      sp.ld = sq.ld = a.ld;
+    }
   } else {
     m_left = (PRODUCT == kDx ? live : a.vocab) - m0;
     if (m_left <= 0) return;
@@ -149,15 +212,26 @@ __global__ __launch_bounds__(256) void k_tile(LossArgs a, int32_t tiles_n) {
     const int32_t all = PRODUCT == kDx ? a.vocab : live, parts = PRODUCT == kDx ? a.parts.dx : a.parts.dw;
     const int64_t part = ((int64_t)all + parts * G::BK - 1) / (parts * G::BK) * G::BK, k0 = part * blockIdx.z;
     K = (int32_t)(all - k0 < 0 ? 0 : all - k0 < part ? all - k0 : part);
-    if constexpr (PRODUCT == kDx) {
-      sp.init(static_cast<const T*>(a.dl) + k0, nullptr, m0, m_left, 0, 0, K);
-      sq.init(a.w, nullptr, k0, K, 0, n0, a.dim);
+    const T* dl = static_cast<const T*>(a.dl);
+    if constexpr (SHORT) {
+      if constexpr (PRODUCT == kDx) {
+        sp.init(dl + m0 * a.dl_ld + k0, a.dl_ld, (int32_t)m_left, K);
+        sq.init(wmat + k0 * a.ld + n0, a.ld, a.dim - n0, K);
+      } else {
+        sp.init(dl + k0 * a.dl_ld + m0, a.dl_ld, (int32_t)m_left, K);
+        sq.init(xs + k0 * a.ld + n0, a.ld, a.dim - n0, K);
+      }
     } else {
-      sp.init(a.dl, nullptr, k0, K, 0, (int32_t)m0, a.vocab);
-      sq.init(xs, nullptr, k0, K, 0, n0, a.dim);
+      if constexpr (PRODUCT == kDx) {
+        sp.init(dl + k0, nullptr, m0, m_left, 0, 0, K);
+        sq.init(wmat, nullptr, k0, K, 0, n0, a.dim);
+      } else {
+        sp.init(dl, nullptr, k0, K, 0, (int32_t)m0, a.vocab);
+        sq.init(xs, nullptr, k0, K, 0, n0, a.dim);
+      }
+      sp.ld = a.dl_ld;
+      sq.ld = a.ld;
     }
-    sp.ld = a.dl_ld;
-    sq.ld = a.ld;
   }
   f32x16_t acc[NT][NT];
 #pragma unroll
@@ -168,8 +242,8 @@ __global__ __launch_bounds__(256) void k_tile(LossArgs a, int32_t tiles_n) {
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
   const int nk = (int)(((uint32_t)K + G::BK - 1) / G::BK);
   // the k-tile after next comes into one pair of stagers while the next one waits in the other
-  Stager<T, PT> sp1 = sp;
-  Stager<T, QT> sq1 = sq;
+  PStager sp1 = sp;
+  QStager sq1 = sq;
   if (nk) {
     sp.fetch(0);
     sq.fetch(0);
@@ -180,7 +254,7 @@ __global__ __launch_bounds__(256) void k_tile(LossArgs a, int32_t tiles_n) {
     sp1.fetch(G::BK);
     sq1.fetch(G::BK);
   }
-  auto step = [&](int kt, Stager<T, PT>& p2, Stager<T, QT>& q2, const Stager<T, PT>& p1, const Stager<T, QT>& q1) {
+  auto step = [&](int kt, PStager& p2, QStager& q2, const PStager& p1, const QStager& q1) {
     __syncthreads();
     const char* st = lds + (kt & 1) * (PB + QB);
     char* next = lds + (~kt & 1) * (PB + QB);
@@ -600,8 +674,10 @@ int launch_logits_large(const LossArgs& a, hipStream_t s) {
 template <class T, int PRODUCT, int EPI>
 int launch_tile(const LossArgs& a, int64_t m, int64_t n, int parts, hipStream_t s) {
   const int64_t tiles_n = ceil_div(n, Tile<T>::B), blocks = ceil_div(m, Tile<T>::B) * tiles_n;
-  hipLaunchKernelGGL((k_tile<T, PRODUCT, EPI>), grid_of_blocks(blocks, 256, (uint32_t)parts), dim3(256), 0, s, a,
-                     (int32_t)tiles_n);
+  auto* kernel = &k_tile<T, PRODUCT, EPI, false>;
+  if constexpr (sizeof(T) == 4)
+    if (a.vocab < (1 << 21) && a.dim < (1 << 21)) kernel = &k_tile<T, PRODUCT, EPI, true>;
+  hipLaunchKernelGGL(kernel, grid_of_blocks(blocks, 256, (uint32_t)parts), dim3(256), 0, s, a, (int32_t)tiles_n);
   return launch_status("classifier product launch");
 }
 
