@@ -255,6 +255,16 @@ def test_distill_loss(tokens, vocab, dim, dtype, k, tau):
     check_losses(x, w, dloss, ids.int(), teacher.bfloat16(), tau, guarded, "off alignment")
 
 
+@pytest.mark.parametrize("dtype", [F, B], ids=str)
+@pytest.mark.parametrize("tokens", [1023, 8193, 16384, 16385, 40007])
+def test_many_rows(tokens, dtype):
+    """Rows' places are counted by one block or by all of them, in their order either way."""
+    x, w, dloss, ids, _ = inputs(tokens, 40, 8, dtype, 0, tokens, absent=0.5)
+    check_losses(x, w, dloss, ids, None, 1.0, on_gpu, "targets")
+    x, w, dloss, ids, teacher = inputs(tokens, 40, 8, dtype, 3, tokens + 1, absent=0.5)
+    check_losses(x, w, dloss, ids.int(), teacher, 1.5, on_gpu, "teacher")
+
+
 def test_rows_that_do_not_count_are_not_read():
     """NaN and infinities in rows without a target reach nothing, in dw neither."""
     x, w, dloss, ids, _ = inputs(70, 150, 48, F, 0, 3)
