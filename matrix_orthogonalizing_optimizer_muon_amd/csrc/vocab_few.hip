@@ -1,5 +1,5 @@
-// The classifier's losses of few rows without gradients (scoring token by token):
-// what counts is how fast w comes from memory, once for all rows.
+// The classifier's losses of few rows (scoring token by token), and their logits for
+// the gradients: what counts is how fast w comes from memory, once for all rows.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -13,6 +13,9 @@ namespace {
 
 constexpr int kFewWaves = 8, kFewLds = 140 * 1024;
 
+// Whether a block has 16 entries of the vocabulary.
+bool narrow(int64_t vocab) { return vocab <= 16 * 256; }
+
 // LDS of one row of x: its columns in whole steps of k, and 16 bytes so that 16
 // rows read at one chunk lie on different banks.
 template <class T>
@@ -21,23 +24,73 @@ __host__ __device__ constexpr int64_t few_row_bytes(int64_t dim) {
   return (dim + STEP - 1) / STEP * STEP * (int64_t)sizeof(T) + 16;
 }
 
+// What a wave does with the logits of 16 entries of the vocabulary from r0 on and NB
+// times 16 rows from 16 b0 on: lane l has those of row l % 16 and of entries
+// 4 (l / 16) + 0..3.  The logits of rows' ids (k a row) go to picked as they come by.
+template <class T, int NB, class I, bool GRADS>
+__device__ __forceinline__ void take_logits(const LossArgs& a, const I* ids, int32_t k, int rows, int32_t r0, int b0,
+                                            int lane, const Acc16 (&acc)[NB], float (&n)[NB], float (&sum)[NB]) {
+  // the rows' ids a wave's width at a time: few are among these 16
+  for (int32_t i0 = 0; i0 < rows * k; i0 += 64) {
+    const uint64_t id = i0 + lane < rows * k ? (uint64_t)(int64_t)ids[i0 + lane] : ~uint64_t(0);
+    const uint64_t off = id - (uint64_t)r0;   // below: huge
+    uint64_t hits = __ballot(off < 16 && id < (uint64_t)a.vocab);
+    while (hits) {
+      const int h = __ffsll((unsigned long long)hits) - 1;
+      hits &= hits - 1;
+      const int c = __builtin_amdgcn_readlane((int32_t)off, h), t = (i0 + h) / k;
+      float x = 0.f;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x = t >> 4 == b0 + b && (c & 3) == i ? acc[b][i] : x;
+      if (t >> 4 >= b0 && t >> 4 < b0 + NB && lane == (t & 15) + 16 * (c >> 2)) a.picked[i0 + h] = x;
+    }
+  }
+  const int32_t left = a.vocab - r0 - 4 * (lane >> 4);
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    const int t = 16 * (b0 + b) + (lane & 15);
+    if (GRADS && t < rows) *reinterpret_cast<Acc16*>(a.z + t * a.dl_ld + r0 + 4 * (lane >> 4)) = acc[b];
+    float top = -INFINITY, add = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < left) top = fmaxf(top, acc[b][i]);
+    const float m = whole_exponent(a, top);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < left) add += __builtin_amdgcn_exp2f(exponent(a, acc[b][i], m, T()));
+    merge_sums(n[b], sum[b], m, add);
+  }
+}
+
 // The exponents' sums of up to 16 NB rows (of x, whole in LDS) over w: a wave has
 // 16 rows of w at a time, which come straight into the MFMA operands (lane l: 16
 // bytes of row l % 16), eight loads in flight; lane l gets row l % 16 of x and rows
 // 4 (l / 16) + 0..3 of w.  Bound by w's way from memory: 32000 x 1024 bf16, 66 MB, one row: 14 us.
-// stats: [block][row] pairs; the logits of rows' ids go to picked as they come by.
-template <class T, int NB, class I>
+// stats: [block][row] pairs.
+// GRADS: rows are slots, and their logits are kept.
+template <class T, int NB, class I, bool GRADS>
 __global__ __launch_bounds__(64 * kFewWaves) void k_few_logits(LossArgs a, const I* __restrict__ ids, int32_t k) {
   constexpr int PER = Few<T>::PER, STEP = 4 * PER, U = 8;
   __shared__ __attribute__((aligned(16))) char lds[kFewLds];
   __shared__ float tops[kFewWaves][16 * NB], sums[kFewWaves][16 * NB];
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int ld = (int)few_row_bytes<T>(a.dim), chunks = ld / 16 - 1, rows = (int)a.tokens;
-  for (int i = tid; i < 16 * NB * chunks; i += 64 * kFewWaves) {
-    const int r = i / chunks, c = i - r * chunks, left = a.dim - c * PER;
-    u32x4 v = {0u, 0u, 0u, 0u};
-    if (r < rows && left > 0) v = load16(static_cast<const T*>(a.x) + (int64_t)r * a.dim + c * PER, left);
-    *reinterpret_cast<u32x4*>(lds + r * ld + c * 16) = v;
+  const int ld = (int)few_row_bytes<T>(a.dim), chunks = ld / 16 - 1, rows = GRADS ? live_slots(a.ch) : (int)a.tokens;
+  const T* x = static_cast<const T*>(GRADS ? a.xs : a.x);
+  for (int i0 = tid; i0 < 16 * NB * chunks; i0 += 64 * kFewWaves * U) {
+    u32x4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + 64 * kFewWaves * u, r = i / chunks, c = i - r * chunks, left = a.dim - c * PER;
+      v[u] = u32x4{0u, 0u, 0u, 0u};
+      if (r < rows && left > 0) v[u] = load16(x + (int64_t)r * a.ld + c * PER, left);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + 64 * kFewWaves * u, r = i / chunks;
+      if (r < 16 * NB) *reinterpret_cast<u32x4*>(lds + r * ld + (i - r * chunks) * 16) = v[u];
+    }
   }
   __syncthreads();
   const char* xp = lds + (lane & 15) * ld + (lane >> 4) * 16;
@@ -50,7 +103,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_few_logits(LossArgs a, const
   }
   for (int32_t grp = blockIdx.x * kFewWaves + w; grp < groups; grp += gridDim.x * kFewWaves) {
     const int32_t r0 = grp * 16, r = r0 + (lane & 15);
-    const T* wp = static_cast<const T*>(a.w) + (int64_t)(r < a.vocab ? r : a.vocab - 1) * a.dim + at;
+    const T* wp = static_cast<const T*>(a.w) + (int64_t)(r < a.vocab ? r : a.vocab - 1) * a.ld + at;
     Acc16 acc[NB] = {};
     int s = 0;
     for (; s + U <= steps; s += U) {
@@ -70,36 +123,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_few_logits(LossArgs a, const
       for (int b = 0; b < NB; ++b)
         acc[b] = multiply16(f, *reinterpret_cast<const u32x4*>(xp + b * 16 * ld + s * 64), acc[b], T());
     }
-    // the rows' ids a wave's width at a time: few are among these 16
-    for (int32_t i0 = 0; i0 < rows * k; i0 += 64) {
-      const uint64_t id = i0 + lane < rows * k ? (uint64_t)(int64_t)ids[i0 + lane] : ~uint64_t(0);
-      const uint64_t off = id - (uint64_t)r0;   // below: huge
-      uint64_t hits = __ballot(off < 16 && id < (uint64_t)a.vocab);
-      while (hits) {
-        const int h = __ffsll((unsigned long long)hits) - 1;
-        hits &= hits - 1;
-        const int c = __builtin_amdgcn_readlane((int32_t)off, h), t = (i0 + h) / k;
-        float x = 0.f;
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x = t >> 4 == b && (c & 3) == i ? acc[b][i] : x;
-        if (lane == (t & 15) + 16 * (c >> 2)) a.picked[i0 + h] = x;
-      }
-    }
-    const int32_t left = a.vocab - r0 - 4 * (lane >> 4);
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      float top = -INFINITY, add = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < left) top = fmaxf(top, acc[b][i]);
-      const float m = whole_exponent(a, top);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < left) add += __builtin_amdgcn_exp2f(exponent(a, acc[b][i], m, T()));
-      merge_sums(n[b], sum[b], m, add);
-    }
+    take_logits<T, NB, I, GRADS>(a, ids, k, rows, r0, 0, lane, acc, n, sum);
   }
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
@@ -111,13 +135,74 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_few_logits(LossArgs a, const
     }
   }
   __syncthreads();
-  if (tid >= rows) return;   // rows <= 16 NB <= 64
+  if (tid >= rows || !a.stats) return;   // rows <= 16 NB <= 64
   float top = tops[0][tid], all = sums[0][tid];
 #pragma unroll
   for (int i = 1; i < kFewWaves; ++i) merge_sums(top, all, tops[i][tid], sums[i][tid]);
-  float* st = a.stats + 2 * ((int64_t)blockIdx.x * rows + tid);
+  float* st = a.stats + 2 * ((int64_t)blockIdx.x * (GRADS ? a.ch.size : rows) + tid);
   st[0] = top;
   st[1] = all;
+}
+
+// The same for vocabularies of up to 256 groups of 16, a block each: its waves have a
+// piece of the columns each, of w and of x straight from memory, and the results are
+// added up in LDS, 16 rows by a wave.  24 rows, 500 x 2048 bf16: 8.5 us, by waves
+// with all columns 20.
+template <class T, int NB, class I, bool GRADS>
+__global__ __launch_bounds__(64 * kFewWaves) void k_few_narrow(LossArgs a, const I* __restrict__ ids, int32_t k) {
+  constexpr int PER = Few<T>::PER, STEP = 4 * PER, U = NB == 4 ? 4 : 8;
+  __shared__ Acc16 pieces[kFewWaves][NB][64];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int rows = GRADS ? live_slots(a.ch) : (int)a.tokens;
+  if (rows == 0) return;
+  const int32_t r0 = blockIdx.x * 16, r = r0 + (lane & 15), at = PER * (lane >> 4);
+  const T* wp = static_cast<const T*>(a.w) + (int64_t)(r < a.vocab ? r : a.vocab - 1) * a.ld + at;
+  const T* xp[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {   // rows past the last: its results are not kept
+    const int t = 16 * b + (lane & 15);
+    xp[b] = static_cast<const T*>(GRADS ? a.xs : a.x) + (int64_t)(t < rows ? t : rows - 1) * a.ld + at;
+  }
+  const int32_t steps = (a.dim + STEP - 1) / STEP, per = (steps + kFewWaves - 1) / kFewWaves;
+  const int32_t end = (w + 1) * per < steps ? (w + 1) * per : steps, full = end < a.dim / STEP ? end : a.dim / STEP;
+  Acc16 acc[NB] = {};
+  int32_t s = w * per;
+  for (; s + U <= full; s += U) {
+    u32x4 f[U], g[U][NB];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      f[u] = *reinterpret_cast<const u32x4_any*>(wp + (s + u) * STEP);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) g[u][b] = *reinterpret_cast<const u32x4_any*>(xp[b] + (s + u) * STEP);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) acc[b] = multiply16(f[u], g[u][b], acc[b], T());
+  }
+  for (; s < end; ++s) {
+    const int left = a.dim - at - s * STEP;
+    const u32x4 zero = {0u, 0u, 0u, 0u};
+    const u32x4 f = left > 0 ? load16(wp + s * STEP, left) : zero;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) acc[b] = multiply16(f, left > 0 ? load16(xp[b] + s * STEP, left) : zero, acc[b], T());
+  }
+#pragma unroll
+  for (int b = 0; b < NB; ++b) pieces[w][b][lane] = acc[b];
+  __syncthreads();
+  if (w >= NB || 16 * w >= rows) return;
+  Acc16 all[1] = {pieces[0][w][lane]};
+#pragma unroll
+  for (int i = 1; i < kFewWaves; ++i) all[0] += pieces[i][w][lane];
+  float n[1] = {-INFINITY}, sum[1] = {0.f};
+  take_logits<T, 1, I, GRADS>(a, ids, k, rows, r0, w, lane, all, n, sum);
+#pragma unroll
+  for (int o = 16; o < 64; o <<= 1) merge_sums(n[0], sum[0], __shfl_xor(n[0], o, 64), __shfl_xor(sum[0], o, 64));
+  const int t = 16 * w + lane;
+  if (lane >= 16 || t >= rows || !a.stats) return;
+  float* st = a.stats + 2 * ((int64_t)blockIdx.x * (GRADS ? a.ch.size : rows) + t);
+  st[0] = n[0];
+  st[1] = sum[0];
 }
 
 // A row's loss from the blocks' sums, by one block.  TT: the teacher's type, or void:
@@ -171,17 +256,26 @@ __global__ __launch_bounds__(512) void k_few_join(LossArgs a, const I* __restric
   lse[t] = log_of(n, log_sum);
 }
 
+template <class T, class I, bool GRADS>
+void launch_logits(const LossArgs& a, const I* ids, int32_t k, hipStream_t s) {
+  const dim3 grid((uint32_t)few_blocks(a.vocab)), block(64 * kFewWaves);
+  const int nb = (int)((a.tokens + 15) / 16);
+  auto* kernel = nb == 1 ? &k_few_logits<T, 1, I, GRADS> : nb == 2 ? &k_few_logits<T, 2, I, GRADS>
+                                                                  : &k_few_logits<T, 4, I, GRADS>;
+  if (narrow(a.vocab))
+    kernel = nb == 1 ? &k_few_narrow<T, 1, I, GRADS> : nb == 2 ? &k_few_narrow<T, 2, I, GRADS>
+                                                               : &k_few_narrow<T, 4, I, GRADS>;
+  hipLaunchKernelGGL(kernel, grid, block, 0, s, a, ids, k);
+}
+
 template <class T>
 int launch(const LossArgs& a, const FewCall& c, hipStream_t s) {
-  const dim3 grid((uint32_t)few_blocks(a.vocab)), block(64 * kFewWaves), rows((uint32_t)a.tokens);
-  const int nb = (int)((a.tokens + 15) / 16);
+  const dim3 grid((uint32_t)few_blocks(a.vocab)), rows((uint32_t)a.tokens);
   const int32_t blocks = (int32_t)grid.x;
   auto by_index = [&](auto index) {
     typedef decltype(index) I;
     const I* ids = static_cast<const I*>(c.ids);
-    if (nb == 1) hipLaunchKernelGGL((k_few_logits<T, 1, I>), grid, block, 0, s, a, ids, c.k);
-    else if (nb == 2) hipLaunchKernelGGL((k_few_logits<T, 2, I>), grid, block, 0, s, a, ids, c.k);
-    else hipLaunchKernelGGL((k_few_logits<T, 4, I>), grid, block, 0, s, a, ids, c.k);
+    launch_logits<T, I, false>(a, ids, c.k, s);
     auto join = [&](auto* teacher) {
       typedef typename std::remove_const<typename std::remove_pointer<decltype(teacher)>::type>::type TT;
       hipLaunchKernelGGL((k_few_join<T, I, TT>), rows, dim3(512), 0, s, a, ids, teacher, c.k, blocks, c.tau, c.loss, c.lse);
@@ -199,14 +293,22 @@ int launch(const LossArgs& a, const FewCall& c, hipStream_t s) {
 
 // 256 blocks of one CU each go through w; fewer where there is not a wave's work for each.
 int64_t few_blocks(int64_t vocab) {
+  if (narrow(vocab)) return ceil_div(vocab, 16);
   const int64_t blocks = ceil_div(vocab, 16 * kFewWaves);
   return blocks < 256 ? blocks : 256;
 }
 
-bool few_rows(int dtype, int64_t tokens, int64_t dim) {
+bool few_rows(int dtype, int64_t tokens, int64_t vocab, int64_t dim) {
   if (tokens < 1 || tokens > 64) return false;
+  if (narrow(vocab)) return dim < (1 << 30);
   const int64_t row = dtype == MUON_BF16 ? few_row_bytes<bf16_t>(dim) : few_row_bytes<float>(dim);
   return (tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64) * row <= kFewLds;
+}
+
+int few_logits(const LossArgs& a, int dtype, hipStream_t s) {
+  if (dtype == MUON_BF16) launch_logits<bf16_t, int32_t, true>(a, a.ids, a.kp, s);
+  else launch_logits<float, int32_t, true>(a, a.ids, a.kp, s);
+  return launch_status("classifier product launch");
 }
 
 int few_loss(const LossArgs& a, int dtype, const FewCall& c, hipStream_t s) {

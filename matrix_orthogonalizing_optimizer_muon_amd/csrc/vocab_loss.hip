@@ -126,7 +126,7 @@ constexpr int kRowsWaves = 16;
 constexpr int64_t kCountRows = 16384;
 template <class T, class I, bool TEACHER, bool COUNT>
 __global__ __launch_bounds__(64 * kRowsWaves) void k_rows(LossArgs a, RowsArgs o, const I* __restrict__ targets,
-                                                          T* __restrict__ xs, T* __restrict__ dx) {
+                                                          T* __restrict__ xs, T* __restrict__ xd, T* __restrict__ dx) {
   __shared__ int32_t counts[kRowsWaves];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t0 = block_index() * kRowsWaves, t = t0 + w;
@@ -134,15 +134,16 @@ __global__ __launch_bounds__(64 * kRowsWaves) void k_rows(LossArgs a, RowsArgs o
   if constexpr (COUNT) {
     auto marked = [&](int64_t i) { return TEACHER ? o.term[i] <= INFINITY : read_index(targets, i, a.vocab) >= 0; };
     int32_t mine = 0;
-    for (int64_t i = threadIdx.x; i - threadIdx.x < t0; i += 64 * kRowsWaves * 8) {
+    const int64_t others = t0 < a.tokens ? t0 : a.tokens;
+    for (int64_t i = threadIdx.x; i - threadIdx.x < others; i += 64 * kRowsWaves * 8) {
       bool in[8];   // loads without conditions, so that they are in flight together
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         const int64_t at = i + 64 * kRowsWaves * u;
-        in[u] = marked(at < t0 ? at : t0 - 1);
+        in[u] = marked(at < others ? at : others - 1);
       }
 #pragma unroll
-      for (int u = 0; u < 8; ++u) mine += __popcll(__ballot(in[u] && i + 64 * kRowsWaves * u < t0));
+      for (int u = 0; u < 8; ++u) mine += __popcll(__ballot(in[u] && i + 64 * kRowsWaves * u < others));
     }
     const int64_t own = t0 + (lane & (kRowsWaves - 1));
     const uint64_t here = __ballot(lane < kRowsWaves && own < a.tokens && marked(own < a.tokens ? own : a.tokens - 1));
@@ -151,9 +152,18 @@ __global__ __launch_bounds__(64 * kRowsWaves) void k_rows(LossArgs a, RowsArgs o
     int32_t before = 0;
 #pragma unroll
     for (int i = 0; i < kRowsWaves; ++i) before += counts[i];
-    if (t0 + kRowsWaves >= a.tokens && threadIdx.x == 0) *o.count = before + __popcll(here);
+    if (t0 < a.tokens && t0 + kRowsWaves >= a.tokens && threadIdx.x == 0) *o.count = before + __popcll(here);
+    before += __popcll(here & ((uint64_t(1) << w) - 1));
+    s = here >> w & 1 ? before : -1;
+    if (a.twice && s < 0 && t < whole_slots((int32_t)a.tokens)) {   // a slot behind the live ones
+      const float zero[8] = {};
+      T* row = xd + twice_row(t < a.tokens ? a.tokens - 1 - (t - before) : t) * a.ld;
+      for (int32_t c = lane * 8; c < a.ld; c += 512) {
+        store8(row + c, 8, zero);
+        store8(row + 32 * a.ld + c, 8, zero);
+      }
+    }
     if (t >= a.tokens) return;
-    s = here >> w & 1 ? before + __popcll(here & ((uint64_t(1) << w) - 1)) : -1;
     if (lane == 0) {
       if (s >= 0) {
         o.rows[s] = (int32_t)t;
@@ -184,6 +194,11 @@ __global__ __launch_bounds__(64 * kRowsWaves) void k_rows(LossArgs a, RowsArgs o
     for (int u = 0; u < 4; ++u) {   // past dim: zeros
       const int32_t at = c + 512 * u, left = a.ld - at;
       if (left > 0) store8(xs + (int64_t)s * a.ld + at, left < 8 ? left : 8, p[u]);
+      if (left > 0 && COUNT && a.twice) {
+        T* row = xd + twice_row(s) * a.ld + at;
+        store8(row, 8, p[u]);
+        store8(row + 32 * a.ld, 8, p[u]);
+      }
     }
   }
   if (TEACHER)
@@ -313,29 +328,49 @@ __device__ __forceinline__ void load_exps(const bf16_t* p, int cnt, float (&v)[8
 }
 __device__ __forceinline__ void load_exps(const float* p, int cnt, float (&v)[8]) { load8(p, cnt, v); }
 
-// 2^(exponent - n of its slab) into gradients, in place, and the targets' entries:
-// a wave has 1024 columns of a slot.  8192 x 32000 bf16, 1.05 GB: 174 us.
+// Gradients from 2^(exponent - n of its slab), in place where a slot has one row, or
+// from logits (Z), and the targets' entries: a wave has 1024 columns of a slot, zeros
+// past the vocabulary.
+// 8192 x 32000 bf16, 1.05 GB: 174 us.
 constexpr int kScaleRuns = 2, kScaleCols = 512 * kScaleRuns;
-template <class T>
-__global__ __launch_bounds__(256) void k_rescale(LossArgs a, JoinArgs j, int32_t units) {
+template <class T, bool Z>
+__global__ __launch_bounds__(256) void k_rescale(LossArgs a, JoinArgs j, const T* exps, int32_t units) {
   const int lane = threadIdx.x & 63;
   const int64_t unit = block_index() * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t s = unit / units;
-  if (s >= live_slots(a.ch)) return;
   const int32_t first = (int32_t)(unit - s * units) * kScaleCols;
+  T* p = static_cast<T*>(a.dl) + (a.twice ? twice_row(s) : s) * a.dl_ld;
+  auto store = [&](T* to, const float (&v)[kScaleRuns][8]) {
+#pragma unroll
+    for (int u = 0; u < kScaleRuns; ++u) {
+      const int32_t c = first + 512 * u + lane * 8;
+      if (c < a.dl_ld) store8(to + c, 8, v[u]);
+    }
+  };
+  float v[kScaleRuns][8] = {};
+  if (s >= live_slots(a.ch)) {
+    if (a.twice && s < whole_slots(a.ch.size)) {
+      store(p, v);
+      store(p + 32 * a.dl_ld, v);
+    }
+    return;
+  }
   const float base = a.base[s], scale = a.scale[s], g = a.g[s];
-  T* p = static_cast<T*>(a.dl) + s * a.dl_ld;
-  float v[kScaleRuns][8];
-  int cnt[kScaleRuns];
 #pragma unroll
   for (int u = 0; u < kScaleRuns; ++u) {
-    const int32_t c = first + 512 * u + lane * 8, left = a.vocab - c;
-    cnt[u] = left <= 0 ? 0 : left < 8 ? left : 8;
-    load_exps(p + c, cnt[u], v[u]);
-    const float n = cnt[u] ? a.stats[2 * ((int64_t)(c / Slab<T>::kCols) * a.ch.size + s)] : 0.f;
-    const float by = __builtin_amdgcn_exp2f(n - base) * (scale * g);
+    const int32_t c = first + 512 * u + lane * 8, left = a.vocab - c, cnt = left <= 0 ? 0 : left < 8 ? left : 8;
+    if constexpr (Z) {
+      load8(a.z + s * a.dl_ld + c, cnt, v[u]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[u][i] *= by;
+      for (int i = 0; i < 8; ++i)
+        v[u][i] = i < cnt ? __builtin_amdgcn_exp2f(exponent(a, v[u][i], base, T())) * scale * g : 0.f;
+    } else {
+      load_exps(exps + s * a.dl_ld + c, cnt, v[u]);
+      const float n = cnt ? a.stats[2 * ((int64_t)(c / Slab<T>::kCols) * a.ch.size + s)] : 0.f;
+      const float by = __builtin_amdgcn_exp2f(n - base) * (scale * g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[u][i] = i < cnt ? v[u][i] * by : 0.f;
+    }
   }
   for (int32_t j0 = 0; j0 < a.kp; j0 += 64) {
     const int32_t at = j0 + lane;
@@ -352,8 +387,20 @@ __global__ __launch_bounds__(256) void k_rescale(LossArgs a, JoinArgs j, int32_t
         for (int i = 0; i < 8; ++i) v[u][i] = c == 512 * u + lane * 8 + i ? d : v[u][i];
     }
   }
+  store(p, v);
+  if constexpr (sizeof(T) == 2) {
+    if (a.twice) {
 #pragma unroll
-  for (int u = 0; u < kScaleRuns; ++u) store8(p + first + 512 * u + lane * 8, cnt[u], v[u]);
+      for (int u = 0; u < kScaleRuns; ++u)
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          const uint32_t first_row = pack2(v[u][i], v[u][i + 1]);
+          v[u][i] -= __uint_as_float(first_row << 16);
+          v[u][i + 1] -= __uint_as_float(first_row & 0xffff0000u);
+        }
+      store(p + 32 * a.dl_ld, v);
+    }
+  }
 }
 
 // The targets' entries of dl where the logits' gradients are there, a wave a slot.
@@ -411,18 +458,18 @@ int64_t chunk_slots(int dtype, int64_t tokens, int64_t vocab, bool grads, bool s
 int32_t places(int32_t k) { return k == 1 ? 1 : (k + 3) / 4 * 4; }
 
 struct LossSpace {
-  bool few;
+  bool few, twice;
   int64_t chunk, slabs, dl_ld;
   ProductParts parts;
   int32_t ld;
-  uint64_t xs, w, sums_of_parts, teacher_id, teacher_q, id, q, term, rows, slot, count, stats, picked, base, scale, g, dl, sums, bytes;
+  uint64_t xs, xd, w, sums_of_parts, teacher_id, teacher_q, id, q, term, rows, slot, count, stats, picked, base, scale, g, dl, z, sums, bytes;
 };
 LossSpace loss_space(int dtype, int64_t tokens, int64_t vocab, int64_t dim, int k, bool teacher, bool grads,
                      bool given) {
   Pieces p;
   LossSpace l = {};
-  if (!grads && few_rows(dtype, tokens, dim)) {
-    l.few = true;
+  l.few = few_rows(dtype, tokens, vocab, dim);
+  if (l.few && !grads) {
     l.stats = p.take((uint64_t)few_blocks(vocab) * tokens * 8);
     l.picked = p.take((uint64_t)tokens * k * 4);
     l.bytes = p.used;
@@ -430,12 +477,15 @@ LossSpace loss_space(int dtype, int64_t tokens, int64_t vocab, int64_t dim, int 
   }
   const int64_t es = dtype == MUON_BF16 ? 2 : 4;
   l.chunk = chunk_slots(dtype, tokens, vocab, grads, !given);
-  l.slabs = ceil_div(vocab, slab_cols(dtype));
+  l.slabs = l.few ? few_blocks(vocab) : ceil_div(vocab, slab_cols(dtype));
   l.dl_ld = ceil_div(vocab, 64) * 64;
   const bool large = large_sizes(dtype, tokens, vocab, dim);
-  l.parts = grads ? product_parts(dtype, l.chunk, vocab, dim, large) : ProductParts{1, 1};
+  l.twice = grads && large && l.chunk == tokens && tokens <= kTwiceRows;
+  const int64_t rows = l.twice ? 2 * whole_slots((int32_t)l.chunk) : l.chunk;   // of dl
+  l.parts = grads ? product_parts(dtype, rows, vocab, dim, large) : ProductParts{1, 1};
   l.ld = (int32_t)(large ? ceil_div(dim, 8) * 8 : dim);
   l.xs = p.take((uint64_t)tokens * l.ld * es);
+  l.xd = p.take(l.twice ? (uint64_t)rows * l.ld * es : 0);
   l.w = p.take(l.ld != dim ? (uint64_t)vocab * l.ld * 2 : 0);
   const uint64_t of_dx = l.parts.dx > 1 ? (uint64_t)l.parts.dx * l.chunk * l.ld * 4 : 0;
   const uint64_t of_dw = l.parts.dw > 1 ? (uint64_t)l.parts.dw * vocab * l.ld * 4 : 0;
@@ -448,12 +498,13 @@ LossSpace loss_space(int dtype, int64_t tokens, int64_t vocab, int64_t dim, int 
   l.rows = p.take((uint64_t)tokens * 4);
   l.slot = p.take((uint64_t)tokens * 4);
   l.count = p.take(4);
-  l.stats = p.take(given ? 0 : (uint64_t)l.slabs * l.chunk * 8);
+  l.stats = p.take(given && (l.few || !l.twice) ? 0 : (uint64_t)l.slabs * l.chunk * 8);
   l.picked = p.take((uint64_t)tokens * places(k) * 4);
   l.base = p.take((uint64_t)tokens * 4);
   l.scale = p.take((uint64_t)tokens * 4);
   l.g = p.take((uint64_t)tokens * 4);
-  l.dl = p.take(grads ? (uint64_t)l.chunk * l.dl_ld * es : 0);
+  l.dl = p.take(grads ? (uint64_t)rows * l.dl_ld * es : 0);
+  l.z = p.take(l.few || l.twice ? (uint64_t)l.chunk * l.dl_ld * (l.few ? 4 : es) : 0);   // or exponentials
   l.sums = p.take(grads && l.chunk < tokens ? (uint64_t)vocab * l.ld * 4 : 0);
   l.bytes = p.used;
   return l;
@@ -499,8 +550,9 @@ void launch_rows(const Call& c, const LossSpace& l, const LossArgs& a, char* ws,
                        (int32_t)c.vocab, o.id, o.rows, slot, o.count, c.loss, c.lse);
   if (!c.tokens) return;
   auto* kernel = count ? &k_rows<T, I, TEACHER, true> : &k_rows<T, I, TEACHER, false>;
-  hipLaunchKernelGGL(kernel, grid_of_blocks(ceil_div(c.tokens, kRowsWaves), 64 * kRowsWaves), dim3(64 * kRowsWaves), 0, s,
-                     a, o, ids, reinterpret_cast<T*>(ws + l.xs), c.dw ? static_cast<T*>(c.dx) : nullptr);
+  const int64_t rows = a.twice ? whole_slots((int32_t)c.tokens) : c.tokens;
+  hipLaunchKernelGGL(kernel, grid_of_blocks(ceil_div(rows, kRowsWaves), 64 * kRowsWaves), dim3(64 * kRowsWaves), 0, s,
+                     a, o, ids, reinterpret_cast<T*>(ws + l.xs), reinterpret_cast<T*>(ws + l.xd), c.dw ? static_cast<T*>(c.dx) : nullptr);
 }
 
 template <class T>
@@ -535,15 +587,18 @@ int run(const Call& c, const LossSpace& l, char* ws, hipStream_t s) {
   const double to_log2 = 1.4426950408889634 / (double)c.tau;
   a.to_log2 = (float)to_log2;
   a.to_log2_low = (float)(to_log2 - (double)a.to_log2);
-  a.stats = given ? nullptr : reinterpret_cast<float*>(ws + l.stats);
+  a.twice = l.twice && large;
+  a.stats = given && (l.few || !a.twice) ? nullptr : reinterpret_cast<float*>(ws + l.stats);
   a.picked = reinterpret_cast<float*>(ws + l.picked);
-  if (l.few)
+  a.ld = l.few && !grads ? a.dim : l.ld;
+  if (l.few && !grads)
     return few_loss(a, c.dtype, FewCall{c.targets, c.index_bytes, c.teacher, c.teacher_dtype, c.k, c.tau, c.loss, c.lse},
                     s);
   a.k = c.k;
   a.kp = places(c.k);
   a.xs = ws + l.xs;
-  a.ld = l.ld;
+  a.xd = ws + l.xd;
+  a.z = l.few ? reinterpret_cast<float*>(ws + l.z) : nullptr;
   a.large = large;
   a.chunked = l.ld == c.dim && aligned16(c.dx) && aligned16(c.dw);
   if (l.ld != c.dim) {
@@ -590,14 +645,21 @@ int run(const Call& c, const LossSpace& l, char* ws, hipStream_t s) {
     a.ids = id + a.ch.slot0 * a.kp;
     a.picked = picked + a.ch.slot0 * a.kp;
     j.q = c.teacher ? q + a.ch.slot0 * a.kp : nullptr;
-    if ((rc = logits_product(a, c.dtype, given ? kGradient : grads ? kStatsExp : kStats, s))) return rc;
+    const bool at_once = given && !l.few && !a.twice;   // dl from the logits' product
+    const Epilogue e = at_once ? kGradient : grads ? kStatsExp : kStats;
+    void* const dl = a.dl;
+    if (a.twice) a.dl = ws + l.z;   // the exponentials
+    if ((rc = l.few ? few_logits(a, c.dtype, s) : logits_product(a, c.dtype, e, s))) return rc;
+    const T* exps = static_cast<const T*>(a.dl);
+    a.dl = dl;
     if (!given) hipLaunchKernelGGL((k_join<T>), dim3((uint32_t)ceil_div(slots, kJoinRows)), dim3(1024), 0, s, a, j);
     if (!grads) continue;
-    if (given) {
+    if (at_once) {
       hipLaunchKernelGGL((k_targets<T>), grid_of_blocks(ceil_div(slots, 4), 256), dim3(256), 0, s, a, j);
     } else {
-      const int64_t units = ceil_div(c.vocab, kScaleCols);
-      hipLaunchKernelGGL((k_rescale<T>), grid_of_blocks(ceil_div(slots * units, 4), 256), dim3(256), 0, s, a, j,
+      const int64_t units = ceil_div(c.vocab, kScaleCols), rows = a.twice ? whole_slots((int32_t)slots) : slots;
+      auto* kernel = l.few ? &k_rescale<T, true> : &k_rescale<T, false>;
+      hipLaunchKernelGGL(kernel, grid_of_blocks(ceil_div(rows * units, 4), 256), dim3(256), 0, s, a, j, exps,
                          (int32_t)units);
     }
     if ((rc = launch_status("classifier loss launch"))) return rc;

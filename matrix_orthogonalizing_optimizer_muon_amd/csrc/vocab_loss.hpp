@@ -55,6 +55,11 @@ struct LossArgs {
   const float* scale;
   const float* g;
   void* dl;                // [chunk][dl_ld], or null
+  float* z;                // [chunk][dl_ld] logits of few rows, which dl is made from, or null: from 2^(exponent - n) there
+  // Whether a slot has two rows of dl, twice_row(slot) and, 32 behind it, what rounding to bf16 left of the first;
+  // xd has its x in both.  Rows between the live slots and whole 32 are zeros.
+  bool twice;
+  const void* xd;
   // gradients
   void* dx;                // tokens x dim
   void* dw;                // vocab x dim
@@ -63,6 +68,10 @@ struct LossArgs {
   float* sums;             // vocab x ld: of the chunks so far, or null where there is one
   bool first, last;        // chunk
 };
+
+// Rows of dl that are kept twice: a slot's two are in the registers of one lane.
+__host__ __device__ __forceinline__ int64_t twice_row(int64_t slot) { return slot + slot / 32 * 32; }
+__host__ __device__ __forceinline__ int32_t whole_slots(int32_t slots) { return (slots + 31) / 32 * 32; }
 
 // log2(e) and ln 2, each in two parts
 constexpr float kLog2e = 1.4426950408889634f, kLog2eLow = (float)(1.4426950408889634 - (double)kLog2e);
@@ -181,7 +190,14 @@ inline bool large_sizes(int dtype, int64_t tokens, int64_t vocab, int64_t dim) {
 }
 ProductParts product_parts(int dtype, int64_t tokens, int64_t vocab, int64_t dim, bool large);
 
-// Losses of few rows without gradients: whether vocab_few.hip takes them, and its
+// Up to so many rows of bf16 dl are kept twice (LossArgs::twice).  The gradients of
+// a few rows are sums of few large entries of dl, whose rounding to bf16 does not
+// average out: off by up to 2^-8, over the 2^-9 or so that rounding the result gives.
+// Both rows fit one tile's 256, so that the products pass over w and dw once either way,
+// and dx is added up in the tile.
+constexpr int64_t kTwiceRows = 128;
+
+// Logits of few rows: whether vocab_few.hip takes them, and its
 // blocks, each of which has a pair for every row in stats.
 struct FewCall {
   const void* ids;
@@ -193,8 +209,9 @@ struct FewCall {
   float* loss;
   float* lse;
 };
-bool few_rows(int dtype, int64_t tokens, int64_t dim);
+bool few_rows(int dtype, int64_t tokens, int64_t vocab, int64_t dim);
 int64_t few_blocks(int64_t vocab);
+int few_logits(const LossArgs& a, int dtype, hipStream_t s);
 int few_loss(const LossArgs& a, int dtype, const FewCall& c, hipStream_t s);
 
 // The products, of one chunk.

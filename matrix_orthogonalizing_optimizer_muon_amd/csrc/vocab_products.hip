@@ -529,7 +529,7 @@ struct GradWalk {
   typedef ColPanel QC;
   const LossArgs& a;
   Walk walk;
-  int32_t live;
+  int32_t live, slots;   // rows of dl, and slots
   __device__ __forceinline__ bool next(OutTile& t) { return walk.next(t); }
   __device__ __forceinline__ int32_t rows() const { return kX ? live : a.vocab; }
   __device__ __forceinline__ int64_t m_left(const OutTile& t) const { return rows() - t.m0; }
@@ -544,15 +544,26 @@ struct GradWalk {
   __device__ __forceinline__ Panel q(const OutTile& t) const {
     const int64_t k = (int64_t)t.k0 * kBK;
     const char* from = kX ? static_cast<const char*>(a.w) + k * a.ld * 2
-                          : static_cast<const char*>(a.xs) + (a.ch.slot0 + k) * a.ld * 2;
+                          : a.twice ? static_cast<const char*>(a.xd) + k * a.ld * 2
+                                    : static_cast<const char*>(a.xs) + (a.ch.slot0 + k) * a.ld * 2;
     return Panel{from + t.n0 * 2ll, (uint32_t)a.ld * 2u, a.ld - t.n0, (int32_t)((kX ? a.vocab : live) - k)};
   }
   __device__ __forceinline__ int store(Acc& acc, const OutTile& t, int mt, int row0, int col0, MUON_LDS char* buf,
                                        int lane) const {
-    const int32_t c0 = t.n0 + col0, m = rows() - t.m0;
+    int32_t m0 = t.m0;
+    if (kX && a.twice) {   // a slot's two rows are a lane's
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = acc[2 * i][j] + acc[2 * i + 1][j];
+      mt /= 2;
+      row0 /= 2;
+      m0 /= 2;
+    }
+    const int32_t c0 = t.n0 + col0, m = (kX ? slots : a.vocab) - m0;
     const bool parts = (kX ? a.parts.dx : a.parts.dw) > 1;
     if (parts || (!kX && a.sums)) {   // sums: of a part, or of the chunks so far
-      float* out = parts ? a.sums_of_parts + ((int64_t)t.part * (kX ? a.ch.size : a.vocab) + t.m0) * a.ld
+      float* out = parts ? a.sums_of_parts + ((int64_t)t.part * (kX ? a.ch.size : a.vocab) + m0) * a.ld
                          : a.sums + (int64_t)t.m0 * a.ld;
       bf16_t* dw = static_cast<bf16_t*>(a.dw) + (int64_t)t.m0 * a.dim;
 #pragma unroll
@@ -589,7 +600,7 @@ struct GradWalk {
       return tile_store(acc, mt, buf, static_cast<bf16_t*>(a.dw) + (int64_t)t.m0 * a.dim, row0, m < 256 ? m : 256, c0,
                         a.dim, lane);
     // rows of dx lie where rows[slot] says
-    const int32_t* rows = a.ch.rows + a.ch.slot0 + t.m0;
+    const int32_t* rows = a.ch.rows + a.ch.slot0 + m0;
     bf16_t* to = static_cast<bf16_t*>(kX ? a.dx : a.dw);
     int64_t row[4][4];
 #pragma unroll
@@ -633,32 +644,50 @@ template <int PRODUCT>
 __global__ __launch_bounds__(512, 2) void k_grad(LossArgs a) {
   __shared__ __attribute__((aligned(16))) char lds[GradWalk<PRODUCT>::Sh::LDS];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  GradWalk<PRODUCT> o{a, {}, __builtin_amdgcn_readfirstlane(live_slots(a.ch))};
+  const int32_t slots = __builtin_amdgcn_readfirstlane(live_slots(a.ch));
+  GradWalk<PRODUCT> o{a, {}, a.twice ? 2 * whole_slots(slots) : slots, slots};
   if (PRODUCT == kDx) o.walk.init(o.live, a.dim, a.vocab, (uint32_t)a.parts.dx);
   else o.walk.init(a.vocab, a.dim, o.live, (uint32_t)a.parts.dw);
   walk_tiles(lds, lane, w, o);
 }
 
-// The parts' sums, in their order: a wave has 512 columns of a slot of dx, which
-// goes to its row, or of a row of dw, which goes on from the chunks before.
-template <class T, int PRODUCT>
+// The parts' sums, in their order: 512 columns of a slot of dx, which go to its row,
+// or of a row of dw, which go on from the chunks before, are a wave's, or, where there
+// are kManyParts and more, a block's, whose waves have a quarter of the parts each (64
+// parts of one row: 5 us, by one wave 9.6).
+constexpr int kManyParts = 12;
+template <class T, int PRODUCT, bool MANY>
 __global__ __launch_bounds__(256) void k_add(LossArgs a, int32_t units) {
   constexpr bool DX = PRODUCT == kDx;
-  const int64_t unit = block_index() * 4 + (threadIdx.x >> 6);
+  __shared__ float quarters[MANY ? 4 : 1][64][9];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t unit = MANY ? block_index() : block_index() * 4 + w;
   const int64_t s = unit / units;
-  if (s >= (DX ? live_slots(a.ch) : a.vocab)) return;
-  const int64_t c = (unit - s * units) * 512 + (threadIdx.x & 63) * 8;
-  if (c >= a.dim) return;
-  const int cnt = a.dim - c < 8 ? (int)(a.dim - c) : 8, parts = DX ? a.parts.dx : a.parts.dw;
+  if (s >= (DX ? live_slots(a.ch) : a.vocab)) return;   // MANY: the whole block
+  const int64_t c = (unit - s * units) * 512 + lane * 8;
+  const int cnt = a.dim - c < 0 ? 0 : a.dim - c < 8 ? (int)(a.dim - c) : 8, parts = DX ? a.parts.dx : a.parts.dw;
   const int64_t size = (int64_t)(DX ? a.ch.size : a.vocab) * a.ld, at = s * a.ld + c;
   float sum[8] = {};
-  if (!DX && !a.first) load8(a.sums + at, cnt, sum);
-#pragma unroll 4
-  for (int32_t p = 0; p < parts; ++p) {
+  if (!DX && !a.first && (!MANY || w == 0)) load8(a.sums + at, cnt, sum);
+  const int32_t per = MANY ? (parts + 3) / 4 : parts, from = MANY ? w * per : 0, to = from + per < parts ? from + per : parts;
+#pragma unroll 8
+  for (int32_t p = from; p < to; ++p) {
     float v[8];
     load8(a.sums_of_parts + p * size + at, cnt, v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum[i] += v[i];
+  }
+  if constexpr (MANY) {
+    if (w) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) quarters[w][lane][i] = sum[i];
+    }
+    __syncthreads();
+    if (w) return;
+#pragma unroll
+    for (int q = 1; q < 4; ++q)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] += quarters[q][lane][i];
   }
   if (DX) store8(static_cast<T*>(a.dx) + (int64_t)a.ch.rows[a.ch.slot0 + s] * a.dim + c, cnt, sum);
   else if (a.last) store8(static_cast<T*>(a.dw) + s * a.dim + c, cnt, sum);
@@ -698,8 +727,10 @@ int launch_grad(const LossArgs& a, hipStream_t s) {
     const int rc = launch_tile<T, PRODUCT, kStats>(a, m, a.dim, parts, s);
     if (rc) return rc;
   }
-  if (parts > 1)
-    hipLaunchKernelGGL((k_add<T, PRODUCT>), grid_of_blocks(ceil_div(m * units, 4), 256), dim3(256), 0, s, a,
+  if (parts >= kManyParts)
+    hipLaunchKernelGGL((k_add<T, PRODUCT, true>), grid_of_blocks(m * units, 256), dim3(256), 0, s, a, (int32_t)units);
+  else if (parts > 1)
+    hipLaunchKernelGGL((k_add<T, PRODUCT, false>), grid_of_blocks(ceil_div(m * units, 4), 256), dim3(256), 0, s, a,
                        (int32_t)units);
   return launch_status("classifier product launch");
 }
