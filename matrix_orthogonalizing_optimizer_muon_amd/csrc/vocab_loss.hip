@@ -226,6 +226,30 @@ __global__ __launch_bounds__(256) void k_pad(const bf16_t* __restrict__ w, int64
   store8(out + r * ld + c, 8, v);
 }
 
+// The unit of dl; one where the largest g is zero, far from one or not a number.
+__global__ __launch_bounds__(1024) void k_unit(LossArgs a, const float* __restrict__ dloss, float tau,
+                                               float* __restrict__ unit) {
+  __shared__ float tops[16];
+  const int32_t live = __builtin_amdgcn_readfirstlane(*a.ch.count);
+  float top = 0.f;
+  for (int32_t i = threadIdx.x; i < live; i += 4096) {
+    float g[4];   // loads without conditions, so that they are in flight together
+#pragma unroll
+    for (int u = 0; u < 4; ++u) g[u] = dloss[a.ch.rows[i + 1024 * u < live ? i + 1024 * u : live - 1]];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) top = fmaxf(top, fabsf(g[u] * tau));
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
+  __syncthreads();
+  if (threadIdx.x) return;
+  for (int i = 1; i < 16; ++i) top = fmaxf(top, tops[i]);
+  if (!(top > 0x1p-100f && top < 0x1p100f)) top = 1.f;
+  unit[0] = 1.f / top;
+  unit[1] = top;
+}
+
 // ------------------------------------------------------------------- targets
 
 struct JoinArgs {
@@ -355,7 +379,7 @@ __global__ __launch_bounds__(256) void k_rescale(LossArgs a, JoinArgs j, const T
     }
     return;
   }
-  const float base = a.base[s], scale = a.scale[s], g = a.g[s];
+  const float base = a.base[s], scale = a.scale[s], g = in_units(a, a.g[s]);
 #pragma unroll
   for (int u = 0; u < kScaleRuns; ++u) {
     const int32_t c = first + 512 * u + lane * 8, left = a.vocab - c, cnt = left <= 0 ? 0 : left < 8 ? left : 8;
@@ -409,7 +433,7 @@ __global__ __launch_bounds__(256) void k_targets(LossArgs a, JoinArgs j) {
   const int lane = threadIdx.x & 63;
   const int64_t s = block_index() * 4 + (threadIdx.x >> 6);
   if (s >= live_slots(a.ch)) return;
-  const float base = a.base[s], scale = a.scale[s], g = a.g[s];
+  const float base = a.base[s], scale = a.scale[s], g = in_units(a, a.g[s]);
   T* dl = static_cast<T*>(a.dl) + s * a.dl_ld;
   for (int32_t i = 0; i < a.k; ++i) {
     const int32_t v = __builtin_amdgcn_readfirstlane(a.ids[s * a.kp + i]);
@@ -462,7 +486,7 @@ struct LossSpace {
   int64_t chunk, slabs, dl_ld;
   ProductParts parts;
   int32_t ld;
-  uint64_t xs, xd, w, sums_of_parts, teacher_id, teacher_q, id, q, term, rows, slot, count, stats, picked, base, scale, g, dl, z, sums, bytes;
+  uint64_t xs, xd, w, sums_of_parts, teacher_id, teacher_q, id, q, term, rows, slot, count, unit, stats, picked, base, scale, g, dl, z, sums, bytes;
 };
 LossSpace loss_space(int dtype, int64_t tokens, int64_t vocab, int64_t dim, int k, bool teacher, bool grads,
                      bool given) {
@@ -498,6 +522,7 @@ LossSpace loss_space(int dtype, int64_t tokens, int64_t vocab, int64_t dim, int 
   l.rows = p.take((uint64_t)tokens * 4);
   l.slot = p.take((uint64_t)tokens * 4);
   l.count = p.take(4);
+  l.unit = p.take(8);
   l.stats = p.take(given && (l.few || !l.twice) ? 0 : (uint64_t)l.slabs * l.chunk * 8);
   l.picked = p.take((uint64_t)tokens * places(k) * 4);
   l.base = p.take((uint64_t)tokens * 4);
@@ -619,6 +644,11 @@ int run(const Call& c, const LossSpace& l, char* ws, hipStream_t s) {
   if (!c.tokens) {   // no rows: dw is zeros
     a.first = a.last = true;
     return grads ? dw_product(a, c.dtype, s) : MUON_OK;
+  }
+  if (grads && large && !a.twice) {
+    float* unit = reinterpret_cast<float*>(ws + l.unit);
+    hipLaunchKernelGGL(k_unit, dim3(1), dim3(1024), 0, s, a, c.dloss, c.tau, unit);
+    a.unit = unit;
   }
   float* base = reinterpret_cast<float*>(ws + l.base);
   float* scale = reinterpret_cast<float*>(ws + l.scale);

@@ -54,6 +54,9 @@ struct LossArgs {
   const float* base;
   const float* scale;
   const float* g;
+  // (1 / u, u), or null: dl is in units of u, the largest |g| of a live row.  Losses that are averaged have one g, whose
+  // rounding to bf16 would be in all of the gradients; in units of itself it is one
+  const float* unit;
   void* dl;                // [chunk][dl_ld], or null
   float* z;                // [chunk][dl_ld] logits of few rows, which dl is made from, or null: from 2^(exponent - n) there
   // Whether a slot has two rows of dl, twice_row(slot) and, 32 behind it, what rounding to bf16 left of the first;
@@ -72,6 +75,8 @@ struct LossArgs {
 // Rows of dl that are kept twice: a slot's two are in the registers of one lane.
 __host__ __device__ __forceinline__ int64_t twice_row(int64_t slot) { return slot + slot / 32 * 32; }
 __host__ __device__ __forceinline__ int32_t whole_slots(int32_t slots) { return (slots + 31) / 32 * 32; }
+
+__device__ __forceinline__ float in_units(const LossArgs& a, float g) { return a.unit ? g * a.unit[0] : g; }
 
 // log2(e) and ln 2, each in two parts
 constexpr float kLog2e = 1.4426950408889634f, kLog2eLow = (float)(1.4426950408889634 - (double)kLog2e);

@@ -447,7 +447,7 @@ struct LogitsWalk {
         const int32_t r = t.m0 + row0 + 32 * i + (lane & 31);
         const bool exists = i < mt && r < live;
         bases[i] = exists ? a.base[r] : 0.f;
-        scales[i] = exists ? a.scale[r] * a.g[r] : 0.f;
+        scales[i] = exists ? a.scale[r] * in_units(a, a.g[r]) : 0.f;
       }
     }
 #pragma unroll
@@ -550,6 +550,15 @@ struct GradWalk {
   }
   __device__ __forceinline__ int store(Acc& acc, const OutTile& t, int mt, int row0, int col0, MUON_LDS char* buf,
                                        int lane) const {
+    if (a.unit) {
+      const float u = a.unit[1];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i >= mt) break;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] *= u;
+      }
+    }
     int32_t m0 = t.m0;
     if (kX && a.twice) {   // a slot's two rows are a lane's
 #pragma unroll

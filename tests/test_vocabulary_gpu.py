@@ -370,6 +370,27 @@ def test_losses_near_zero(tokens, vocab, dim, dtype):
     close(both, want, bound, "loss with gradients")
 
 
+@pytest.mark.parametrize("form", ["both", "backward"])
+def test_equal_dloss_is_not_rounded(form):
+    """Averaged losses have one dloss, whose rounding to bf16 (here by 0.0036) would be in every
+    gradient.  All logits are 0 and targets different: a target's entry of dl, dloss (2^-10 - 1),
+    may be off by 2^-10, others, dloss 2^-10, by nothing; the result by half a step."""
+    T, V, d, g = 300, 1024, 40, 1.0036 / 256
+    x, w = torch.randn(T, d, generator=gen(1)).bfloat16(), torch.zeros(V, d).bfloat16()
+    targets, dloss = torch.randperm(V, generator=gen(2))[:T], torch.full((T,), g)
+    if form == "both":
+        dw = M.classifier_loss_grads(dloss.cuda(), x.cuda(), w.cuda(), targets.cuda())[3]
+    else:
+        lse = torch.full((T,), math.log(V))
+        dw = M.classifier_loss_backward(dloss.cuda(), x.cuda(), w.cuda(), targets.cuda(), lse.cuda())[1]
+    at, q = O.target_weights(targets, V)
+    want = O.grads(dloss, x, w, at, q, 1.0)[1]
+    own = torch.zeros(V, d, dtype=torch.float64).index_add_(0, targets, x.double().abs() * g)
+    # sums of T products; exp(-lse) by a logarithm of half a step off
+    slack = 2.0 ** -10 * own + (T + 16) * ULP * (own + x.double().abs().sum(0) * g / V)
+    close(dw, want, slack + HALF[B] * (want.abs() + slack), "dw")
+
+
 def test_overflow_of_a_logit_is_nan_in_its_row_alone():
     x, w, dloss, ids, _ = inputs(66, 140, 32, F, 0, 4, absent=0.0)
     x[7] = 3e38
