@@ -611,7 +611,7 @@ int muon_embed_backward(const void* dout, const void* tokens, int index_bytes, i
                         uint64_t workspace_bytes, void* stream);
 
 /*
- * Cross entropy of the logits l = x w^T, which are never in memory whole:
+ * Cross entropy of the logits l = x w^T, which are in memory for up to 128 rows alone:
  *   lse[t] = log sum_v exp(l_tv),  loss[t] = lse[t] - l_t,targets[t]
  * A target that names nothing takes its row out: loss and lse 0, its gradient
  * zeros, and its x reaches nothing.  Work goes with the rows that are left.
@@ -619,7 +619,8 @@ int muon_embed_backward(const void* dout, const void* tokens, int index_bytes, i
  *   muon_classifier_loss_grads     these and, for the loss's gradient dloss (fp32,
  *                                  tokens), dx (tokens x dim) and dw (vocab x dim):
  *                                  dl_tv = dloss[t] (exp(l_tv - lse[t]) - [v = targets[t]]),
- *                                  dx = dl w, dw = dl^T x, with dl rounded to dtype
+ *                                  dx = dl w, dw = dl^T x, with dl rounded to dtype (bf16: up to
+ *                                  128 rows to 16 digits, beyond in units of the largest dloss)
  *   muon_classifier_loss_backward  dx and dw from the lse that a loss call gave
  *                                  (computes the logits again)
  * muon_classifier_loss_workspace: bytes that a call needs; gradients 0: the loss

@@ -13,15 +13,28 @@ namespace {
 
 constexpr int kFewWaves = 8, kFewLds = 140 * 1024;
 
-// Whether a block has 16 entries of the vocabulary.
-bool narrow(int64_t vocab) { return vocab <= 16 * 256; }
-
 // LDS of one row of x: its columns in whole steps of k, and 16 bytes so that 16
 // rows read at one chunk lie on different banks.
 template <class T>
 __host__ __device__ constexpr int64_t few_row_bytes(int64_t dim) {
   constexpr int64_t STEP = 4 * Few<T>::PER;
   return (dim + STEP - 1) / STEP * STEP * (int64_t)sizeof(T) + 16;
+}
+
+int row_blocks(int64_t tokens) { return tokens <= 16 ? 1 : tokens <= 32 ? 2 : tokens <= 64 ? 4 : 8; }
+
+bool fits(int dtype, int64_t tokens, int64_t dim) {
+  const int64_t row = dtype == MUON_BF16 ? few_row_bytes<bf16_t>(dim) : few_row_bytes<float>(dim);
+  return tokens <= 64 && 16 * row_blocks(tokens) * row <= kFewLds;
+}
+
+// Whether a block has 16 entries of the vocabulary and reads x for them from L2: up to
+// one for each CU, and where x is larger than LDS as long as that is less than the
+// large tiles take for few rows (k-tiles of 0.9 us on few CUs).  Losses, us, so and by
+// those: 24 rows of 4551 x 2624 19, 46; 64 of 8192 x 4096 42, 65; 32 of 16384 x 2560
+// 34, 48; 100 of 4000 x 2048 22, 40; 50 of 8000 x 1536 in fp32 31, 67.
+bool narrow(int dtype, int64_t tokens, int64_t vocab, int64_t dim) {
+  return vocab <= 16 * 256 || (!fits(dtype, tokens, dim) && vocab * row_blocks(tokens) <= (1 << 15));
 }
 
 // What a wave does with the logits of 16 entries of the vocabulary from r0 on and NB
@@ -144,13 +157,13 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_few_logits(LossArgs a, const
   st[1] = all;
 }
 
-// The same for vocabularies of up to 256 groups of 16, a block each: its waves have a
+// The same with a block for 16 entries of the vocabulary (narrow): its waves have a
 // piece of the columns each, of w and of x straight from memory, and the results are
 // added up in LDS, 16 rows by a wave.  24 rows, 500 x 2048 bf16: 8.5 us, by waves
 // with all columns 20.
 template <class T, int NB, class I, bool GRADS>
 __global__ __launch_bounds__(64 * kFewWaves) void k_few_narrow(LossArgs a, const I* __restrict__ ids, int32_t k) {
-  constexpr int PER = Few<T>::PER, STEP = 4 * PER, U = NB == 4 ? 4 : 8;
+  constexpr int PER = Few<T>::PER, STEP = 4 * PER, U = NB == 8 ? 2 : NB == 4 ? 4 : 8;
   __shared__ Acc16 pieces[kFewWaves][NB][64];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int rows = GRADS ? live_slots(a.ch) : (int)a.tokens;
@@ -258,20 +271,23 @@ __global__ __launch_bounds__(512) void k_few_join(LossArgs a, const I* __restric
 
 template <class T, class I, bool GRADS>
 void launch_logits(const LossArgs& a, const I* ids, int32_t k, hipStream_t s) {
-  const dim3 grid((uint32_t)few_blocks(a.vocab)), block(64 * kFewWaves);
-  const int nb = (int)((a.tokens + 15) / 16);
+  constexpr int kType = sizeof(T) == 2 ? MUON_BF16 : MUON_F32;
+  const dim3 grid((uint32_t)few_blocks(kType, a.tokens, a.vocab, a.dim)), block(64 * kFewWaves);
+  const int nb = row_blocks(a.tokens);
   auto* kernel = nb == 1 ? &k_few_logits<T, 1, I, GRADS> : nb == 2 ? &k_few_logits<T, 2, I, GRADS>
                                                                   : &k_few_logits<T, 4, I, GRADS>;
-  if (narrow(a.vocab))
-    kernel = nb == 1 ? &k_few_narrow<T, 1, I, GRADS> : nb == 2 ? &k_few_narrow<T, 2, I, GRADS>
-                                                               : &k_few_narrow<T, 4, I, GRADS>;
+  if (narrow(kType, a.tokens, a.vocab, a.dim))
+    kernel = nb == 1   ? &k_few_narrow<T, 1, I, GRADS>
+             : nb == 2 ? &k_few_narrow<T, 2, I, GRADS>
+             : nb == 4 ? &k_few_narrow<T, 4, I, GRADS>
+                       : &k_few_narrow<T, 8, I, GRADS>;
   hipLaunchKernelGGL(kernel, grid, block, 0, s, a, ids, k);
 }
 
 template <class T>
 int launch(const LossArgs& a, const FewCall& c, hipStream_t s) {
-  const dim3 grid((uint32_t)few_blocks(a.vocab)), rows((uint32_t)a.tokens);
-  const int32_t blocks = (int32_t)grid.x;
+  const dim3 rows((uint32_t)a.tokens);
+  const int32_t blocks = (int32_t)few_blocks(sizeof(T) == 2 ? MUON_BF16 : MUON_F32, a.tokens, a.vocab, a.dim);
   auto by_index = [&](auto index) {
     typedef decltype(index) I;
     const I* ids = static_cast<const I*>(c.ids);
@@ -292,17 +308,15 @@ int launch(const LossArgs& a, const FewCall& c, hipStream_t s) {
 }  // namespace
 
 // 256 blocks of one CU each go through w; fewer where there is not a wave's work for each.
-int64_t few_blocks(int64_t vocab) {
-  if (narrow(vocab)) return ceil_div(vocab, 16);
+int64_t few_blocks(int dtype, int64_t tokens, int64_t vocab, int64_t dim) {
+  if (narrow(dtype, tokens, vocab, dim)) return ceil_div(vocab, 16);
   const int64_t blocks = ceil_div(vocab, 16 * kFewWaves);
   return blocks < 256 ? blocks : 256;
 }
 
 bool few_rows(int dtype, int64_t tokens, int64_t vocab, int64_t dim) {
-  if (tokens < 1 || tokens > 64) return false;
-  if (narrow(vocab)) return dim < (1 << 30);
-  const int64_t row = dtype == MUON_BF16 ? few_row_bytes<bf16_t>(dim) : few_row_bytes<float>(dim);
-  return (tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64) * row <= kFewLds;
+  if (tokens < 1 || tokens > 128) return false;
+  return fits(dtype, tokens, dim) || narrow(dtype, tokens, vocab, dim);
 }
 
 int few_logits(const LossArgs& a, int dtype, hipStream_t s) {

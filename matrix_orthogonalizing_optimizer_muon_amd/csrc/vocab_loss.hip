@@ -494,14 +494,14 @@ LossSpace loss_space(int dtype, int64_t tokens, int64_t vocab, int64_t dim, int 
   LossSpace l = {};
   l.few = few_rows(dtype, tokens, vocab, dim);
   if (l.few && !grads) {
-    l.stats = p.take((uint64_t)few_blocks(vocab) * tokens * 8);
+    l.stats = p.take((uint64_t)few_blocks(dtype, tokens, vocab, dim) * tokens * 8);
     l.picked = p.take((uint64_t)tokens * k * 4);
     l.bytes = p.used;
     return l;
   }
   const int64_t es = dtype == MUON_BF16 ? 2 : 4;
   l.chunk = chunk_slots(dtype, tokens, vocab, grads, !given);
-  l.slabs = l.few ? few_blocks(vocab) : ceil_div(vocab, slab_cols(dtype));
+  l.slabs = l.few ? few_blocks(dtype, tokens, vocab, dim) : ceil_div(vocab, slab_cols(dtype));
   l.dl_ld = ceil_div(vocab, 64) * 64;
   const bool large = large_sizes(dtype, tokens, vocab, dim);
   l.twice = grads && large && l.chunk == tokens && tokens <= kTwiceRows;

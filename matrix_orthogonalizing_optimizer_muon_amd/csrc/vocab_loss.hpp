@@ -215,7 +215,7 @@ struct FewCall {
   float* lse;
 };
 bool few_rows(int dtype, int64_t tokens, int64_t vocab, int64_t dim);
-int64_t few_blocks(int64_t vocab);
+int64_t few_blocks(int dtype, int64_t tokens, int64_t vocab, int64_t dim);
 int few_logits(const LossArgs& a, int dtype, hipStream_t s);
 int few_loss(const LossArgs& a, int dtype, const FewCall& c, hipStream_t s);
 

@@ -4,7 +4,7 @@
 //   dx      dx[rows[s]][i] = sum_v dl[s][v] w[v][i]      w k-major
 //   dw      dw[v][i]  = sum_s dl[s][v] x[rows[s]][i]     both k-major
 //
-// Logits are never stored: what leaves the first product is, for each slab of
+// Logits are not stored (but for those of few rows, vocab_few.hip): what leaves the first product is, for each slab of
 // columns, a row's largest exponent of two, rounded up, and the sum of 2^ the rest
 // (kStats), these and 2^ the rest in as many bits as x has (kStatsExp, which k_rescale makes
 // gradients of once the row's sum is known), or the logits' gradient without

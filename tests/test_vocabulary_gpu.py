@@ -138,7 +138,8 @@ def test_embed_passes_values_on():
 SIZES = [(1, 1, 1), (1, 16, 16), (1, 1000, 64), (5, 33, 7), (17, 129, 200), (64, 128, 64), (130, 300, 72),
          (257, 515, 129), (300, 1024, 256), (513, 70, 520), (700, 1111, 264), (520, 2050, 128), (385, 6007, 136),
          (129, 129, 8), (2100, 40, 16), (16, 5003, 136), (33, 40000, 72), (64, 777, 1096), (65, 777, 1096),
-         (48, 4096, 333), (64, 4097, 72), (31, 515, 2100), (128, 300, 72), (127, 515, 136), (97, 2050, 264)]
+         (48, 4096, 333), (64, 4097, 72), (31, 515, 2100), (128, 300, 72), (127, 515, 136), (97, 2050, 264),
+         (100, 5003, 72), (64, 8192, 1144), (20, 16383, 2264)]
 
 
 def inputs(tokens, vocab, dim, dtype, k, seed, absent=0.2, index=J):
