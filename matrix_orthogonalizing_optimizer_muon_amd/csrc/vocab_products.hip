@@ -4,11 +4,12 @@
 //   dx      dx[rows[s]][i] = sum_v dl[s][v] w[v][i]      w k-major
 //   dw      dw[v][i]  = sum_s dl[s][v] x[rows[s]][i]     both k-major
 //
-// Logits are not stored (but for those of few rows, vocab_few.hip): what leaves the first product is, for each slab of
-// columns, a row's largest exponent of two, rounded up, and the sum of 2^ the rest
-// (kStats), these and 2^ the rest in as many bits as x has (kStatsExp, which k_rescale makes
-// gradients of once the row's sum is known), or the logits' gradient without
-// the targets' part (kGradient, where the sum is known before).
+// Logits are not stored (but for those of few rows, vocab_few.hip): what leaves the
+// first product is, for each slab of columns, a row's largest exponent of two, rounded
+// up, and the sum of 2^ the rest (kStats), these and 2^ the rest in as many bits as x
+// has (kStatsExp, which k_rescale makes gradients of once the row's sum is known), or
+// the logits' gradient without the targets' part (kGradient, where the sum is known
+// before).
 #include <hip/hip_runtime.h>
 
 #include <math.h>
@@ -171,7 +172,7 @@ struct Stager32 {
 // the total by itself, so that no value is rounded K / 2 times in a row (errors of
 // the gradients of 389 x 4099 x 515: 4.0e-6 -> 1.2e-6 of their norm).
 template <class T, int PRODUCT, int EPI, bool SHORT>
-__global__ __launch_bounds__(256) void k_tile(LossArgs a, int32_t tiles_n) {
+__global__ __launch_bounds__(256) void k_tile(LossArgs a, int32_t tiles_m, int32_t tiles_n) {
   using G = Tile<T>;
   constexpr bool PT = PRODUCT == kDw, QT = PRODUCT != kLogits;
   constexpr int PB = PT ? G::BYTES_T : G::BYTES, QB = QT ? G::BYTES_T : G::BYTES;
@@ -179,10 +180,14 @@ __global__ __launch_bounds__(256) void k_tile(LossArgs a, int32_t tiles_n) {
   static_assert(W == Slab<T>::kCols, "a wave's columns are a slab");
   __shared__ __attribute__((aligned(16))) char lds[2 * (PB + QB)];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, wy = w >> 1, wx = w & 1;
-  const int64_t t = block_index();
-  const int64_t tm = t / tiles_n;
-  const int32_t n0 = (int32_t)(t - tm * tiles_n) * G::B;
-  const int64_t m0 = tm * G::B;
+  // an XCD (blocks go to them in turn) has one piece of a list that goes down 8 rows of tiles at a time, and w
+  // or dl from memory once (logits of 103 x 100414 x 2048: 594 -> 551 us; 1000 x 32000 x 1024: 650 -> 631)
+  const int64_t all = (int64_t)tiles_m * tiles_n, b = block_index(), t = (b & 7) * ((all + 7) / 8) + (b >> 3);
+  if (b >> 3 >= (all + 7) / 8 || t >= all) return;
+  const int64_t group = t / (8 * (int64_t)tiles_n), off = t - group * 8 * tiles_n;
+  const int64_t wide = tiles_m - group * 8 < 8 ? tiles_m - group * 8 : 8;
+  const int32_t n0 = (int32_t)(off / wide) * G::B;
+  const int64_t m0 = (group * 8 + off % wide) * G::B;
   const int32_t live = live_slots(a.ch);
   const int32_t* rows = a.ch.rows + a.ch.slot0;
   const T* xs = static_cast<const T*>(a.xs) + a.ch.slot0 * a.ld;
@@ -711,11 +716,12 @@ int launch_logits_large(const LossArgs& a, hipStream_t s) {
 
 template <class T, int PRODUCT, int EPI>
 int launch_tile(const LossArgs& a, int64_t m, int64_t n, int parts, hipStream_t s) {
-  const int64_t tiles_n = ceil_div(n, Tile<T>::B), blocks = ceil_div(m, Tile<T>::B) * tiles_n;
+  const int64_t tiles_n = ceil_div(n, Tile<T>::B), tiles_m = ceil_div(m, Tile<T>::B);
+  const int64_t blocks = ceil_div(tiles_m * tiles_n, 8) * 8;
   auto* kernel = &k_tile<T, PRODUCT, EPI, false>;
   if constexpr (sizeof(T) == 4)
     if (a.vocab < (1 << 21) && a.dim < (1 << 21)) kernel = &k_tile<T, PRODUCT, EPI, true>;
-  hipLaunchKernelGGL(kernel, grid_of_blocks(blocks, 256, (uint32_t)parts), dim3(256), 0, s, a, (int32_t)tiles_n);
+  hipLaunchKernelGGL(kernel, grid_of_blocks(blocks, 256, (uint32_t)parts), dim3(256), 0, s, a, (int32_t)tiles_m, (int32_t)tiles_n);
   return launch_status("classifier product launch");
 }
 
@@ -767,7 +773,7 @@ int parts_of(int64_t m, int64_t n, int64_t k, int64_t b, int64_t k_tile, int at_
 ProductParts product_parts(int dtype, int64_t tokens, int64_t vocab, int64_t dim, bool large) {
   const bool bf16 = dtype == MUON_BF16;
   const int64_t b = large ? 256 : bf16 ? Tile<bf16_t>::B : Tile<float>::B, k = bf16 ? kBK : Tile<float>::BK;
-  const int at_once = large ? kWalkers : 2 * kWalkers;
+  const int at_once = (large ? 1 : bf16 ? 2 : 4) * kWalkers;   // by LDS
   const double us = large ? 1.7 : 2;
   return ProductParts{parts_of(tokens, dim, vocab, b, k, at_once, us), parts_of(vocab, dim, tokens, b, k, at_once, us)};
 }
