@@ -32,39 +32,40 @@ bool fits(int dtype, int64_t tokens, int64_t dim) {
 // one for each CU, and where x is larger than LDS as long as that is less than the
 // large tiles take for few rows (k-tiles of 0.9 us on few CUs).  Losses, us, so and by
 // those: 24 rows of 4551 x 2624 19, 46; 64 of 8192 x 4096 42, 65; 32 of 16384 x 2560
-// 34, 48; 100 of 4000 x 2048 22, 40; 50 of 8000 x 1536 in fp32 31, 67.
+// 34, 48; 100 of 4000 x 2048 22, 40; 420 of 20 x 3200 31, 58;
+// 50 of 8000 x 1536 in fp32 31, 67; 4000 of 100 x 2048 in fp32 53, 93.
 bool narrow(int dtype, int64_t tokens, int64_t vocab, int64_t dim) {
-  return vocab <= 16 * 256 || (!fits(dtype, tokens, dim) && vocab * row_blocks(tokens) <= (1 << 15));
+  return fits(dtype, tokens, dim) ? vocab <= 16 * 256 : vocab * (ceil_div(tokens, 16) * 16) <= (1 << 19);
 }
 
 // What a wave does with the logits of 16 entries of the vocabulary from r0 on and NB
 // times 16 rows from 16 b0 on: lane l has those of row l % 16 and of entries
-// 4 (l / 16) + 0..3.  The logits of rows' ids (k a row) go to picked as they come by.
-template <class T, int NB, class I, bool GRADS>
-__device__ __forceinline__ void take_logits(const LossArgs& a, const I* ids, int32_t k, int rows, int32_t r0, int b0,
+// 4 (l / 16) + 0..3.  They are kept in z, or, where that is null, those of the up to 64
+// rows' targets go to picked as they come by.
+template <class T, int NB, class I>
+__device__ __forceinline__ void take_logits(const LossArgs& a, const I* targets, int rows, int32_t r0, int b0,
                                             int lane, const Acc16 (&acc)[NB], float (&n)[NB], float (&sum)[NB]) {
-  // the rows' ids a wave's width at a time: few are among these 16
-  for (int32_t i0 = 0; i0 < rows * k; i0 += 64) {
-    const uint64_t id = i0 + lane < rows * k ? (uint64_t)(int64_t)ids[i0 + lane] : ~uint64_t(0);
+  if (!a.z) {
+    const uint64_t id = lane < rows ? (uint64_t)(int64_t)targets[lane] : ~uint64_t(0);
     const uint64_t off = id - (uint64_t)r0;   // below: huge
     uint64_t hits = __ballot(off < 16 && id < (uint64_t)a.vocab);
     while (hits) {
-      const int h = __ffsll((unsigned long long)hits) - 1;
+      const int t = __ffsll((unsigned long long)hits) - 1;
       hits &= hits - 1;
-      const int c = __builtin_amdgcn_readlane((int32_t)off, h), t = (i0 + h) / k;
+      const int c = __builtin_amdgcn_readlane((int32_t)off, t);
       float x = 0.f;
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int i = 0; i < 4; ++i) x = t >> 4 == b0 + b && (c & 3) == i ? acc[b][i] : x;
-      if (t >> 4 >= b0 && t >> 4 < b0 + NB && lane == (t & 15) + 16 * (c >> 2)) a.picked[i0 + h] = x;
+      if (lane == (t & 15) + 16 * (c >> 2)) a.picked[t] = x;
     }
   }
   const int32_t left = a.vocab - r0 - 4 * (lane >> 4);
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     const int t = 16 * (b0 + b) + (lane & 15);
-    if (GRADS && t < rows) *reinterpret_cast<Acc16*>(a.z + t * a.dl_ld + r0 + 4 * (lane >> 4)) = acc[b];
+    if (a.z && t < rows) *reinterpret_cast<Acc16*>(a.z + t * a.dl_ld + r0 + 4 * (lane >> 4)) = acc[b];
     float top = -INFINITY, add = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -82,9 +83,9 @@ __device__ __forceinline__ void take_logits(const LossArgs& a, const I* ids, int
 // bytes of row l % 16), eight loads in flight; lane l gets row l % 16 of x and rows
 // 4 (l / 16) + 0..3 of w.  Bound by w's way from memory: 32000 x 1024 bf16, 66 MB, one row: 14 us.
 // stats: [block][row] pairs.
-// GRADS: rows are slots, and their logits are kept.
+// GRADS: rows are slots.
 template <class T, int NB, class I, bool GRADS>
-__global__ __launch_bounds__(64 * kFewWaves) void k_few_logits(LossArgs a, const I* __restrict__ ids, int32_t k) {
+__global__ __launch_bounds__(64 * kFewWaves) void k_few_logits(LossArgs a, const I* __restrict__ targets) {
   constexpr int PER = Few<T>::PER, STEP = 4 * PER, U = 8;
   __shared__ __attribute__((aligned(16))) char lds[kFewLds];
   __shared__ float tops[kFewWaves][16 * NB], sums[kFewWaves][16 * NB];
@@ -136,7 +137,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_few_logits(LossArgs a, const
       for (int b = 0; b < NB; ++b)
         acc[b] = multiply16(f, *reinterpret_cast<const u32x4*>(xp + b * 16 * ld + s * 64), acc[b], T());
     }
-    take_logits<T, NB, I, GRADS>(a, ids, k, rows, r0, 0, lane, acc, n, sum);
+    take_logits<T, NB, I>(a, targets, rows, r0, 0, lane, acc, n, sum);
   }
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
@@ -161,19 +162,19 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_few_logits(LossArgs a, const
 // piece of the columns each, of w and of x straight from memory, and the results are
 // added up in LDS, 16 rows by a wave.  24 rows, 500 x 2048 bf16: 8.5 us, by waves
 // with all columns 20.
-template <class T, int NB, class I, bool GRADS>
-__global__ __launch_bounds__(64 * kFewWaves) void k_few_narrow(LossArgs a, const I* __restrict__ ids, int32_t k) {
+template <class T, int NB, bool GRADS>
+__global__ __launch_bounds__(64 * kFewWaves) void k_few_narrow(LossArgs a) {
   constexpr int PER = Few<T>::PER, STEP = 4 * PER, U = NB == 8 ? 2 : NB == 4 ? 4 : 8;
   __shared__ Acc16 pieces[kFewWaves][NB][64];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int rows = GRADS ? live_slots(a.ch) : (int)a.tokens;
-  if (rows == 0) return;
+  const int row0 = blockIdx.y * 128, rows = GRADS ? live_slots(a.ch) : (int)a.tokens;
+  if (rows <= row0) return;
   const int32_t r0 = blockIdx.x * 16, r = r0 + (lane & 15), at = PER * (lane >> 4);
   const T* wp = static_cast<const T*>(a.w) + (int64_t)(r < a.vocab ? r : a.vocab - 1) * a.ld + at;
   const T* xp[NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b) {   // rows past the last: its results are not kept
-    const int t = 16 * b + (lane & 15);
+    const int t = row0 + 16 * b + (lane & 15);
     xp[b] = static_cast<const T*>(GRADS ? a.xs : a.x) + (int64_t)(t < rows ? t : rows - 1) * a.ld + at;
   }
   const int32_t steps = (a.dim + STEP - 1) / STEP, per = (steps + kFewWaves - 1) / kFewWaves;
@@ -203,15 +204,15 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_few_narrow(LossArgs a, const
 #pragma unroll
   for (int b = 0; b < NB; ++b) pieces[w][b][lane] = acc[b];
   __syncthreads();
-  if (w >= NB || 16 * w >= rows) return;
+  if (w >= NB || row0 + 16 * w >= rows) return;
   Acc16 all[1] = {pieces[0][w][lane]};
 #pragma unroll
   for (int i = 1; i < kFewWaves; ++i) all[0] += pieces[i][w][lane];
   float n[1] = {-INFINITY}, sum[1] = {0.f};
-  take_logits<T, 1, I, GRADS>(a, ids, k, rows, r0, w, lane, all, n, sum);
+  take_logits<T, 1, int32_t>(a, nullptr, rows, r0, row0 / 16 + w, lane, all, n, sum);
 #pragma unroll
   for (int o = 16; o < 64; o <<= 1) merge_sums(n[0], sum[0], __shfl_xor(n[0], o, 64), __shfl_xor(sum[0], o, 64));
-  const int t = 16 * w + lane;
+  const int t = row0 + 16 * w + lane;
   if (lane >= 16 || t >= rows || !a.stats) return;
   float* st = a.stats + 2 * ((int64_t)blockIdx.x * (GRADS ? a.ch.size : rows) + t);
   st[0] = n[0];
@@ -262,7 +263,7 @@ __global__ __launch_bounds__(512) void k_few_join(LossArgs a, const I* __restric
   float off = 0.f;
 #pragma unroll
   for (int i = 0; i < (kTeacher ? TeacherRow::N : 1); ++i)
-    if (r.at[i] >= 0) off += r.q[i] * loss_term<T>(a, a.picked[t * k + lane + 64 * i], n, log_sum);
+    if (r.at[i] >= 0) off += r.q[i] * loss_term<T>(a, a.z ? a.z[t * a.dl_ld + r.at[i]] : a.picked[t], n, log_sum);
   off = wave_sum(off);
   if (lane) return;
   loss[t] = tau * tau * (r.term + off);
@@ -270,18 +271,22 @@ __global__ __launch_bounds__(512) void k_few_join(LossArgs a, const I* __restric
 }
 
 template <class T, class I, bool GRADS>
-void launch_logits(const LossArgs& a, const I* ids, int32_t k, hipStream_t s) {
+void launch_logits(const LossArgs& a, const I* targets, hipStream_t s) {
   constexpr int kType = sizeof(T) == 2 ? MUON_BF16 : MUON_F32;
-  const dim3 grid((uint32_t)few_blocks(kType, a.tokens, a.vocab, a.dim)), block(64 * kFewWaves);
+  const dim3 block(64 * kFewWaves);
+  const uint32_t blocks = (uint32_t)few_blocks(kType, a.tokens, a.vocab, a.dim);
   const int nb = row_blocks(a.tokens);
+  if (narrow(kType, a.tokens, a.vocab, a.dim)) {
+    auto* kernel = nb == 1   ? &k_few_narrow<T, 1, GRADS>
+                   : nb == 2 ? &k_few_narrow<T, 2, GRADS>
+                   : nb == 4 ? &k_few_narrow<T, 4, GRADS>
+                             : &k_few_narrow<T, 8, GRADS>;
+    hipLaunchKernelGGL(kernel, dim3(blocks, (uint32_t)ceil_div(a.tokens, 128)), block, 0, s, a);
+    return;
+  }
   auto* kernel = nb == 1 ? &k_few_logits<T, 1, I, GRADS> : nb == 2 ? &k_few_logits<T, 2, I, GRADS>
                                                                   : &k_few_logits<T, 4, I, GRADS>;
-  if (narrow(kType, a.tokens, a.vocab, a.dim))
-    kernel = nb == 1   ? &k_few_narrow<T, 1, I, GRADS>
-             : nb == 2 ? &k_few_narrow<T, 2, I, GRADS>
-             : nb == 4 ? &k_few_narrow<T, 4, I, GRADS>
-                       : &k_few_narrow<T, 8, I, GRADS>;
-  hipLaunchKernelGGL(kernel, grid, block, 0, s, a, ids, k);
+  hipLaunchKernelGGL(kernel, dim3(blocks), block, 0, s, a, targets);
 }
 
 template <class T>
@@ -291,7 +296,7 @@ int launch(const LossArgs& a, const FewCall& c, hipStream_t s) {
   auto by_index = [&](auto index) {
     typedef decltype(index) I;
     const I* ids = static_cast<const I*>(c.ids);
-    launch_logits<T, I, false>(a, ids, c.k, s);
+    launch_logits<T, I, false>(a, ids, s);
     auto join = [&](auto* teacher) {
       typedef typename std::remove_const<typename std::remove_pointer<decltype(teacher)>::type>::type TT;
       hipLaunchKernelGGL((k_few_join<T, I, TT>), rows, dim3(512), 0, s, a, ids, teacher, c.k, blocks, c.tau, c.loss, c.lse);
@@ -315,14 +320,19 @@ int64_t few_blocks(int dtype, int64_t tokens, int64_t vocab, int64_t dim) {
 }
 
 bool few_rows(int dtype, int64_t tokens, int64_t vocab, int64_t dim) {
-  if (tokens < 1 || tokens > 128) return false;
+  if (tokens < 1) return false;
   return fits(dtype, tokens, dim) || narrow(dtype, tokens, vocab, dim);
 }
 
 int few_logits(const LossArgs& a, int dtype, hipStream_t s) {
-  if (dtype == MUON_BF16) launch_logits<bf16_t, int32_t, true>(a, a.ids, a.kp, s);
-  else launch_logits<float, int32_t, true>(a, a.ids, a.kp, s);
+  if (dtype == MUON_BF16) launch_logits<bf16_t, int32_t, true>(a, nullptr, s);
+  else launch_logits<float, int32_t, true>(a, nullptr, s);
   return launch_status("classifier product launch");
+}
+
+// k 1: the targets' logits are picked as they come by, unless blocks' waves share columns.
+bool few_keeps(int dtype, int64_t tokens, int64_t vocab, int64_t dim, int k) {
+  return k > 1 || narrow(dtype, tokens, vocab, dim);
 }
 
 int few_loss(const LossArgs& a, int dtype, const FewCall& c, hipStream_t s) {

@@ -312,7 +312,8 @@ __global__ __launch_bounds__(1024) void k_join(LossArgs a, JoinArgs j) {
   float off = 0.f;
   for (int32_t i = lane; i < a.kp; i += 64)
     if (a.ids[s * a.kp + i] >= 0)
-      off += (j.q ? j.q[s * a.kp + i] : 1.f) * loss_term<T>(a, a.picked[s * a.kp + i], n, log_sum);
+      off += (j.q ? j.q[s * a.kp + i] : 1.f) *
+             loss_term<T>(a, a.z ? a.z[s * a.dl_ld + a.ids[s * a.kp + i]] : a.picked[s * a.kp + i], n, log_sum);
   off = wave_sum(off);
   if (lane) return;
   j.loss[t] = j.tau * j.tau * ((j.term ? j.term[t] : 0.f) + off);
@@ -404,7 +405,8 @@ __global__ __launch_bounds__(256) void k_rescale(LossArgs a, JoinArgs j, const T
       const int h = __ffsll((unsigned long long)hits) - 1;
       hits &= hits - 1;
       const int32_t e = __builtin_amdgcn_readlane(id, h), c = e - first;
-      const float d = target_entry<T>(a, a.picked[s * a.kp + j0 + h], weight_of(a, j, s, e, lane), base, scale, g);
+      const float l = Z ? a.z[s * a.dl_ld + e] : a.picked[s * a.kp + j0 + h];
+      const float d = target_entry<T>(a, l, weight_of(a, j, s, e, lane), base, scale, g);
 #pragma unroll
       for (int u = 0; u < kScaleRuns; ++u)
 #pragma unroll
@@ -482,7 +484,7 @@ int64_t chunk_slots(int dtype, int64_t tokens, int64_t vocab, bool grads, bool s
 int32_t places(int32_t k) { return k == 1 ? 1 : (k + 3) / 4 * 4; }
 
 struct LossSpace {
-  bool few, twice;
+  bool few, twice, keeps;   // keeps: z, of few rows
   int64_t chunk, slabs, dl_ld;
   ProductParts parts;
   int32_t ld;
@@ -495,7 +497,11 @@ LossSpace loss_space(int dtype, int64_t tokens, int64_t vocab, int64_t dim, int 
   l.few = few_rows(dtype, tokens, vocab, dim);
   if (l.few && !grads) {
     l.stats = p.take((uint64_t)few_blocks(dtype, tokens, vocab, dim) * tokens * 8);
-    l.picked = p.take((uint64_t)tokens * k * 4);
+    const bool z = few_keeps(dtype, tokens, vocab, dim, k);
+    l.dl_ld = ceil_div(vocab, 64) * 64;
+    l.picked = p.take(z ? 0 : (uint64_t)tokens * 4);
+    l.z = p.take(z ? (uint64_t)tokens * l.dl_ld * 4 : 0);
+    l.keeps = z;
     l.bytes = p.used;
     return l;
   }
@@ -529,6 +535,7 @@ LossSpace loss_space(int dtype, int64_t tokens, int64_t vocab, int64_t dim, int 
   l.scale = p.take((uint64_t)tokens * 4);
   l.g = p.take((uint64_t)tokens * 4);
   l.dl = p.take(grads ? (uint64_t)rows * l.dl_ld * es : 0);
+  l.keeps = l.few;
   l.z = p.take(l.few || l.twice ? (uint64_t)l.chunk * l.dl_ld * (l.few ? 4 : es) : 0);   // or exponentials
   l.sums = p.take(grads && l.chunk < tokens ? (uint64_t)vocab * l.ld * 4 : 0);
   l.bytes = p.used;
@@ -616,6 +623,8 @@ int run(const Call& c, const LossSpace& l, char* ws, hipStream_t s) {
   a.stats = given && (l.few || !a.twice) ? nullptr : reinterpret_cast<float*>(ws + l.stats);
   a.picked = reinterpret_cast<float*>(ws + l.picked);
   a.ld = l.few && !grads ? a.dim : l.ld;
+  a.dl_ld = l.dl_ld;
+  a.z = l.keeps ? reinterpret_cast<float*>(ws + l.z) : nullptr;
   if (l.few && !grads)
     return few_loss(a, c.dtype, FewCall{c.targets, c.index_bytes, c.teacher, c.teacher_dtype, c.k, c.tau, c.loss, c.lse},
                     s);
@@ -623,7 +632,6 @@ int run(const Call& c, const LossSpace& l, char* ws, hipStream_t s) {
   a.kp = places(c.k);
   a.xs = ws + l.xs;
   a.xd = ws + l.xd;
-  a.z = l.few ? reinterpret_cast<float*>(ws + l.z) : nullptr;
   a.large = large;
   a.chunked = l.ld == c.dim && aligned16(c.dx) && aligned16(c.dw);
   if (l.ld != c.dim) {
@@ -633,7 +641,6 @@ int run(const Call& c, const LossSpace& l, char* ws, hipStream_t s) {
                        reinterpret_cast<bf16_t*>(ws + l.w));
     a.w = ws + l.w;
   }
-  a.dl_ld = l.dl_ld;
   a.sums_of_parts = reinterpret_cast<float*>(ws + l.sums_of_parts);
   a.parts = l.parts;
   a.dl = grads ? ws + l.dl : nullptr;

@@ -58,7 +58,7 @@ struct LossArgs {
   // rounding to bf16 would be in all of the gradients; in units of itself it is one
   const float* unit;
   void* dl;                // [chunk][dl_ld], or null
-  float* z;                // [chunk][dl_ld] logits of few rows, which dl is made from, or null: from 2^(exponent - n) there
+  float* z;                // [chunk][dl_ld] logits of few rows, which dl is made from and targets read; else null
   // Whether a slot has two rows of dl, twice_row(slot) and, 32 behind it, what rounding to bf16 left of the first;
   // xd has its x in both.  Rows between the live slots and whole 32 are zeros.
   bool twice;
@@ -217,6 +217,7 @@ struct FewCall {
 bool few_rows(int dtype, int64_t tokens, int64_t vocab, int64_t dim);
 int64_t few_blocks(int dtype, int64_t tokens, int64_t vocab, int64_t dim);
 int few_logits(const LossArgs& a, int dtype, hipStream_t s);
+bool few_keeps(int dtype, int64_t tokens, int64_t vocab, int64_t dim, int k);   // z, without gradients
 int few_loss(const LossArgs& a, int dtype, const FewCall& c, hipStream_t s);
 
 // The products, of one chunk.

@@ -72,10 +72,12 @@ struct Places {
     }
   }
   // A hit goes to the lane that has its column.  A lane notes one of its hits, as is
-  // mostly all there is: k / (vocab / 64) for a row.
+  // mostly all there is: k / (vocab / 64) for a row.  Where a lane has more, the wave's
+  // 32 rows go through LDS (buf, 4 KB), from where lanes take theirs (gradients of 4000
+  // rows of 500 x 1024, k = 64: 164 us, one by one 789).
   template <int N, class Value>
   __device__ __forceinline__ void pick(const LossArgs& a, int32_t first, int64_t s, int32_t j0, int lane,
-                                       Value value) const {
+                                       MUON_LDS char* buf, Value value) const {
     uint32_t note = 0, count = 0;   // place of the lane's 16, column
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
@@ -83,22 +85,32 @@ struct Places {
       note = c < 2 * N ? c + 256 * e : note;
       count += c < 2 * N;
     }
+    if (__any(count > 1)) {
+      const int r = lane & 31;
+#pragma unroll
+      for (int j = 0; j < N / 16; ++j) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          put_row(buf, lane, g, u32x4{__float_as_uint(value(16 * j + 4 * g)), __float_as_uint(value(16 * j + 4 * g + 1)),
+                                      __float_as_uint(value(16 * j + 4 * g + 2)), __float_as_uint(value(16 * j + 4 * g + 3))});
+        asm volatile("" ::: "memory");   // reads of other lanes' writes, in the wave's order
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const uint32_t c = id[e / 4][e % 4] - (uint32_t)(first + 32 * j);
+          if (c < 32)
+            a.picked[s * a.kp + j0 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3)] =
+                *(const MUON_LDS float*)(buf + r * 128 + (((c >> 2) ^ nt::swz<128>(r)) << 4) + (c & 3) * 4);
+        }
+        asm volatile("" ::: "memory");
+      }
+      return;
+    }
     uint64_t hits = __ballot(count == 1);
     while (hits) {
       const int h = __ffsll((unsigned long long)hits) - 1;
       hits &= hits - 1;
       const uint32_t n = __builtin_amdgcn_readlane(note, h);
       give<N>(a, s, j0, h, n >> 8, n & 255, lane, value);
-    }
-    if (!__any(count > 1)) return;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      hits = __ballot(count > 1 && id[e / 4][e % 4] - (uint32_t)first < 2 * N);
-      while (hits) {
-        const int h = __ffsll((unsigned long long)hits) - 1;
-        hits &= hits - 1;
-        give<N>(a, s, j0, h, e, __builtin_amdgcn_readlane(id[e / 4][e % 4], h) - (uint32_t)first, lane, value);
-      }
     }
   }
   template <int N, class Value>
@@ -294,6 +306,8 @@ __global__ __launch_bounds__(256) void k_tile(LossArgs a, int32_t tiles_m, int32
     step(kt, sp, sq, sp1, sq1);
     if (kt + 1 < nk) step(kt + 1, sp1, sq1, sp, sq);
   }
+  static_assert(sizeof(lds) >= 4 * 4096, "the waves' rows");
+  if (PRODUCT == kLogits && a.kp > 1) __syncthreads();   // other waves' reads of the last k-tile
   // lane l has row l % 32 of a 32 x 32 tile, registers 4 g + 0..3 columns 8 g + 4 (l / 32) + 0..3
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
@@ -310,7 +324,7 @@ __global__ __launch_bounds__(256) void k_tile(LossArgs a, int32_t tiles_m, int32
         for (int32_t j0 = 0; j0 < a.kp; j0 += 32) {
           Places p;
           p.load(a, slot, j0, lane);
-          p.template pick<16 * NT>(a, n0 + wx * W, slot, j0, lane, value);
+          p.template pick<16 * NT>(a, n0 + wx * W, slot, j0, lane, (MUON_LDS char*)(lds + w * 4096), value);
         }
       }
       float e[NT][16];
@@ -440,7 +454,7 @@ struct LogitsWalk {
         for (int32_t j0 = 0; j0 < a.kp; j0 += 32) {
           if (j0 + 32 < a.kp) then.load(a, slot(i), j0 + 32, lane);
           else then.load(a, i < 3 ? slot(i + 1) : -1, 0, lane);
-          now.template pick<32>(a, first, slot(i), j0, lane, [&](int v) { return acc[i][v / 16][v % 16]; });
+          now.template pick<32>(a, first, slot(i), j0, lane, buf, [&](int v) { return acc[i][v / 16][v % 16]; });
           now = then;
         }
       }

@@ -253,7 +253,7 @@ def test_classifier_loss(tokens, vocab, dim, dtype):
 @pytest.mark.parametrize("k,tau", [(1, 1.0), (5, 2.0), (64, 0.7), (65, 1.0), (256, 3.0)])
 @pytest.mark.parametrize("dtype", [F, B], ids=str)
 @pytest.mark.parametrize("tokens,vocab,dim", [(1, 16, 16), (5, 33, 7), (40, 2050, 264), (130, 300, 72), (257, 515, 129),
-                                              (64, 5000, 40), (100, 700, 72)])
+                                              (64, 5000, 40), (100, 700, 72), (700, 1000, 72)])
 def test_distill_loss(tokens, vocab, dim, dtype, k, tau):
     x, w, dloss, ids, teacher = inputs(tokens, vocab, dim, dtype, k, tokens + k)
     check_losses(x, w, dloss, ids, teacher, tau, on_gpu, "aligned")
