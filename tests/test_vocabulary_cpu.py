@@ -137,10 +137,12 @@ def test_workspaces():
     loss, grads, given = (bytes_of("muon_classifier_loss_workspace", 1, tokens, vocab, dim, g) for g in (0, 1, 2))
     assert loss < tokens * vocab          # far from the logits' 2 or 4 bytes each
     assert loss < given <= grads
-    # a million rows: dl within 2 GiB, the slabs' sums within 256 MiB, dw's sums, and what goes with rows
+    # a million rows: dl within 2 GiB, the slabs' sums within 256 MiB, dw's sums, and what goes with
+    # rows, a copy of x's live ones among it
+    rows = (1 << 20) * (dim * 2 + 64)
     most = bytes_of("muon_classifier_loss_workspace", 1, 1 << 20, 131072, dim, 1)
-    assert most < (1 << 31) + (1 << 28) + 131072 * dim * 4 + (1 << 20) * 64
-    assert bytes_of("muon_classifier_loss_workspace", 1, 1 << 20, 131072, dim, 0) < (1 << 28) + (1 << 20) * 64
+    assert most < (1 << 31) + (1 << 28) + 131072 * dim * 4 + rows
+    assert bytes_of("muon_classifier_loss_workspace", 1, 1 << 20, 131072, dim, 0) < (1 << 28) + rows
 
 
 # ---------------------------------------------------------------------- oracle
