@@ -32,8 +32,8 @@ bool fits(int dtype, int64_t tokens, int64_t dim) {
 // one for each CU, and where x is larger than LDS as long as that is less than the
 // large tiles take for few rows (k-tiles of 0.9 us on few CUs).  Losses, us, so and by
 // those: 24 rows of 4551 x 2624 19, 46; 64 of 8192 x 4096 42, 65; 32 of 16384 x 2560
-// 34, 48; 100 of 4000 x 2048 22, 40; 420 of 20 x 3200 31, 58;
-// 50 of 8000 x 1536 in fp32 31, 67; 4000 of 100 x 2048 in fp32 53, 93.
+// 34, 48; 100 of 4000 x 2048 22, 40; 420 of 20 x 3200 31, 58; 50 of 8000 x 1536 in
+// fp32 31, 67; 4000 of 100 x 2048 in fp32 53, 93.
 bool narrow(int dtype, int64_t tokens, int64_t vocab, int64_t dim) {
   return fits(dtype, tokens, dim) ? vocab <= 16 * 256 : vocab * (ceil_div(tokens, 16) * 16) <= (1 << 19);
 }
@@ -82,8 +82,7 @@ __device__ __forceinline__ void take_logits(const LossArgs& a, const I* targets,
 // 16 rows of w at a time, which come straight into the MFMA operands (lane l: 16
 // bytes of row l % 16), eight loads in flight; lane l gets row l % 16 of x and rows
 // 4 (l / 16) + 0..3 of w.  Bound by w's way from memory: 32000 x 1024 bf16, 66 MB, one row: 14 us.
-// stats: [block][row] pairs.
-// GRADS: rows are slots.
+// stats: [block][row] pairs.  GRADS: rows are slots.
 template <class T, int NB, class I, bool GRADS>
 __global__ __launch_bounds__(64 * kFewWaves) void k_few_logits(LossArgs a, const I* __restrict__ targets) {
   constexpr int PER = Few<T>::PER, STEP = 4 * PER, U = 8;
