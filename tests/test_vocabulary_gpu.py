@@ -253,7 +253,7 @@ def test_classifier_loss(tokens, vocab, dim, dtype):
 @pytest.mark.parametrize("k,tau", [(1, 1.0), (5, 2.0), (64, 0.7), (65, 1.0), (256, 3.0)])
 @pytest.mark.parametrize("dtype", [F, B], ids=str)
 @pytest.mark.parametrize("tokens,vocab,dim", [(1, 16, 16), (5, 33, 7), (40, 2050, 264), (130, 300, 72), (257, 515, 129),
-                                              (64, 5000, 40), (100, 700, 72), (700, 1000, 72)])
+                                              (64, 5000, 40), (100, 700, 72), (700, 1000, 72), (300, 2050, 136)])
 def test_distill_loss(tokens, vocab, dim, dtype, k, tau):
     x, w, dloss, ids, teacher = inputs(tokens, vocab, dim, dtype, k, tokens + k)
     check_losses(x, w, dloss, ids, teacher, tau, on_gpu, "aligned")
@@ -270,11 +270,12 @@ def test_many_rows(tokens, dtype):
     check_losses(x, w, dloss, ids.int(), teacher, 1.5, on_gpu, "teacher")
 
 
-def test_rows_that_do_not_count_are_not_read():
+@pytest.mark.parametrize("tokens,vocab", [(70, 150), (600, 1000), (60, 5000)])
+def test_rows_that_do_not_count_are_not_read(tokens, vocab):
     """NaN and infinities in rows without a target reach nothing, in dw neither."""
-    x, w, dloss, ids, _ = inputs(70, 150, 48, F, 0, 3)
-    ids[:5] = torch.tensor([3, -1, 150, 7, -1])
-    dead = O.named(ids, 150) < 0
+    x, w, dloss, ids, _ = inputs(tokens, vocab, 48, F, 0, 3)
+    ids[:5] = torch.tensor([3, -1, vocab, 7, -1])
+    dead = O.named(ids, vocab) < 0
     x[dead] = torch.tensor([nan, inf, -inf])[torch.arange(int(dead.sum())) % 3][:, None]
     dloss[dead] = nan
     for dtype in (F, B):
@@ -283,10 +284,11 @@ def test_rows_that_do_not_count_are_not_read():
         assert all(bool(t.isfinite().all()) for t in got)
 
 
-def test_no_row_counts():
+@pytest.mark.parametrize("tokens,vocab", [(40, 90), (700, 1000), (40, 5000)])
+def test_no_row_counts(tokens, vocab):
     for dtype in (F, B):
-        x, w, dloss, ids, teacher = inputs(40, 90, 24, dtype, 4, 8)
-        none = torch.full((40,), -1).cuda()
+        x, w, dloss, ids, teacher = inputs(tokens, vocab, 24, dtype, 4, 8)
+        none = torch.full((tokens,), -1).cuda()
         x, w, dloss, ids, teacher = (t.cuda() for t in (x, w, dloss, ids, teacher))
         for got in (M.classifier_loss_grads(dloss, x, w, none),
                     M.classifier_loss(x, w, none),
@@ -311,9 +313,10 @@ def test_no_rows():
         assert not M.embed_backward(x, none, 90).any() and M.embed(none, w).shape == (0, 24)
 
 
-def test_teacher_entries_that_are_not_there():
+@pytest.mark.parametrize("tokens,vocab", [(60, 100), (700, 1000), (60, 5000)])
+def test_teacher_entries_that_are_not_there(tokens, vocab):
     """-inf, NaN, +inf and ids of nothing in a teacher's rows, ids that come twice."""
-    x, w, dloss, ids, teacher = inputs(60, 100, 32, F, 6, 11)
+    x, w, dloss, ids, teacher = inputs(tokens, vocab, 32, F, 6, 11)
     teacher[0, :3] = torch.tensor([-inf, nan, -inf])
     teacher[1] = -inf
     teacher[2, 1] = 3e38
@@ -322,14 +325,14 @@ def test_teacher_entries_that_are_not_there():
     ids[5] = 7
     ids[6] = torch.tensor([4, 4, 9, 4, 9, -1])
     ids[7] = -1
-    ids[8, 0] = 100
+    ids[8, 0] = vocab
     for i in (0, 2, 3, 4):
         ids[i] = torch.arange(6) + i
     # the differences of 6e38 over tau overflow to weight 0, as the definition's do
-    at, q = O.teacher_weights(teacher, ids, 100, 1.0)
+    at, q = O.teacher_weights(teacher, ids, vocab, 1.0)
     got = M.distill_loss_grads(dloss.cuda(), x.cuda(), w.cuda(), teacher.cuda(), ids.cuda())
-    arg = torch.full((60,), 40.0, dtype=torch.float64)
-    b = bounds_of(x, w, dloss, at, q, arg, 1.0, 2)
+    arg = torch.full((tokens,), 40.0, dtype=torch.float64)
+    b = bounds_of(x, w, dloss, at, q, arg, 1.0, 2 * HALF[F])
     want = (*O.loss(x, w, at, q), *O.grads(dloss, x, w, at, q))
     for g, v, e, name in zip(got, want, b, ("loss", "lse", "dx", "dw")):
         close(g, v, e + HALF[F] * (v.abs() + e), name)
@@ -350,7 +353,7 @@ def test_large_and_equal_logits():
 
 
 @pytest.mark.parametrize("dtype", [F, B], ids=str)
-@pytest.mark.parametrize("tokens,vocab,dim", [(5, 1000, 64), (150, 700, 128), (150, 701, 65)])
+@pytest.mark.parametrize("tokens,vocab,dim", [(5, 1000, 64), (150, 700, 128), (150, 701, 65), (150, 4003, 128)])
 def test_losses_near_zero(tokens, vocab, dim, dtype):
     """A loss is log(1 + sum over the others of exp(l_v - l_y)): the target's logit in its sum and the one taken off
     are the same number, whatever it was rounded by.  So the loss is off by the others' part of it, their differences
@@ -414,7 +417,7 @@ def test_chunks(dtype):
     at, q = O.target_weights(ids, vocab)
     arg = torch.zeros(tokens, dtype=torch.float64, device="cuda")
     want_loss, want_lse = O.loss(x, w, at, q)
-    b_loss, b_lse, b_dx, b_dw = bounds_of(x, w, dloss, at, q, arg, 1.0, 2)
+    b_loss, b_lse, b_dx, b_dw = bounds_of(x, w, dloss, at, q, arg, 1.0, 2 * HALF[dtype] * (1 + HALF[dtype]))
     close(loss, want_loss, b_loss, "loss")
     close(lse, want_lse, b_lse, "lse")
     half = HALF[dtype]
@@ -424,9 +427,10 @@ def test_chunks(dtype):
         close(got[1], want[1], 2 * b_dw + half * (want[1].abs() + b_dw) + TINY[dtype], "dw")
 
 
+@pytest.mark.parametrize("tokens,vocab", [(400, 700), (900, 2050), (60, 5000)])
 @pytest.mark.parametrize("k", [0, 8])
-def test_bits_repeat(k):
-    x, w, dloss, ids, teacher = (None if t is None else t.cuda() for t in inputs(400, 700, 192, B, k, 9))
+def test_bits_repeat(k, tokens, vocab):
+    x, w, dloss, ids, teacher = (None if t is None else t.cuda() for t in inputs(tokens, vocab, 192, B, k, 9))
     def call():
         return M.distill_loss_grads(dloss, x, w, teacher, ids) if k else M.classifier_loss_grads(dloss, x, w, ids)
     first = call()
@@ -455,8 +459,12 @@ def step_inputs(seed, dtype=B, n=300, vocab=500, dim=128, k=8):
             w, torch.randn(n, k, generator=g).cuda(), ids, torch.randn(n, generator=g).cuda())
 
 
-def test_a_step_on_a_stream_of_its_own():
-    args = step_inputs(1)
+STEPS = pytest.mark.parametrize("sizes", [(300, 500, 128), (400, 2100, 136), (20, 500, 64), (100, 5000, 72)])
+
+
+@STEPS
+def test_a_step_on_a_stream_of_its_own(sizes):
+    args = step_inputs(1, B, *sizes)
     want = model_step(*args)
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
@@ -470,17 +478,18 @@ def test_a_step_on_a_stream_of_its_own():
     assert torch.equal(loss, want[0])
 
 
+@STEPS
 @pytest.mark.parametrize("dtype", [F, B], ids=str)
-def test_a_step_in_a_graph(dtype):
+def test_a_step_in_a_graph(dtype, sizes):
     """Captured once, replayed on other values with eager work between."""
-    args = step_inputs(2, dtype)
+    args = step_inputs(2, dtype, *sizes)
     model_step(*args)
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         out = model_step(*args)
     for seed in (3, 4, 5):
-        for a, b in zip(args, step_inputs(seed, dtype)):
+        for a, b in zip(args, step_inputs(seed, dtype, *sizes)):
             a.copy_(b)
         want = model_step(*args)
         torch.cuda.synchronize()
@@ -489,9 +498,10 @@ def test_a_step_in_a_graph(dtype):
         assert all(torch.equal(a, b) for a, b in zip(out, want))
 
 
-def test_two_calls_at_once():
+@STEPS
+def test_two_calls_at_once(sizes):
     """Calls on two streams have workspaces of their own."""
-    a, b = step_inputs(6), step_inputs(7)
+    a, b = step_inputs(6, B, *sizes), step_inputs(7, B, *sizes)
     want = model_step(*a), model_step(*b)
     torch.cuda.synchronize()
     streams = torch.cuda.Stream(), torch.cuda.Stream()
@@ -521,7 +531,7 @@ def test_outputs_off_16_bytes():
     """The entry point writes dx and dw at any alignment of their type, and nothing beside them."""
     import ctypes
     from matrix_orthogonalizing_optimizer_muon_amd import _lib as L
-    for tokens, vocab, dim in ((300, 520, 72), (70, 33, 8)):
+    for tokens, vocab, dim in ((300, 520, 72), (70, 33, 8), (600, 1000, 72)):
         x, w, dloss, ids, _ = (None if t is None else t.cuda() for t in inputs(tokens, vocab, dim, B, 0, 31))
         want = M.classifier_loss_grads(dloss, x, w, ids)
         need = ctypes.c_uint64()
@@ -540,14 +550,15 @@ def test_outputs_off_16_bytes():
         assert torch.equal(loss, want[0]) and torch.equal(lse, want[1])
 
 
-def test_given_lse_is_taken_as_it_is():
+@pytest.mark.parametrize("tokens,vocab", [(90, 200), (700, 1000)])
+def test_given_lse_is_taken_as_it_is(tokens, vocab):
     """The backward pass goes by the lse that it is given, a shifted one too."""
-    x, w, dloss, ids, _ = inputs(90, 200, 40, F, 0, 41, absent=0.0)
-    at, q = O.target_weights(ids, 200)
+    x, w, dloss, ids, _ = inputs(tokens, vocab, 40, F, 0, 41, absent=0.0)
+    at, q = O.target_weights(ids, vocab)
     lse = O.loss(x, w, at, q)[1].float() + 0.25
     dx, dw = M.classifier_loss_backward(dloss.cuda(), x.cuda(), w.cuda(), ids.cuda(), lse.cuda())
     want = O.grads(dloss, x, w, at, q, 1.0, lse)
-    b = bounds_of(x, w, dloss, at, q, torch.zeros(90, dtype=torch.float64), 1.0, 1)
+    b = bounds_of(x, w, dloss, at, q, torch.zeros(tokens, dtype=torch.float64), 1.0, HALF[F])
     close(dx, want[0], b[2] + HALF[F] * (want[0].abs() + b[2]), "dx")
     close(dw, want[1], b[3] + HALF[F] * (want[1].abs() + b[3]), "dw")
 
