@@ -50,7 +50,7 @@ struct LossArgs {
   const int32_t* ids;
   float* picked;
   int32_t k, kp;
-  // by slot of the chunk: probabilities are 2^(l to_log2 - base) scale; g is dloss times temperature
+  // by slot of the chunk: probabilities are 2^(l to_log2 - base) scale; g is dloss times temperature, in units
   const float* base;
   const float* scale;
   const float* g;
@@ -75,8 +75,6 @@ struct LossArgs {
 // Rows of dl that are kept twice: a slot's two are in the registers of one lane.
 __host__ __device__ __forceinline__ int64_t twice_row(int64_t slot) { return slot + slot / 32 * 32; }
 __host__ __device__ __forceinline__ int32_t whole_slots(int32_t slots) { return (slots + 31) / 32 * 32; }
-
-__device__ __forceinline__ float in_units(const LossArgs& a, float g) { return a.unit ? g * a.unit[0] : g; }
 
 // log2(e) and ln 2, each in two parts
 constexpr float kLog2e = 1.4426950408889634f, kLog2eLow = (float)(1.4426950408889634 - (double)kLog2e);

@@ -466,7 +466,7 @@ struct LogitsWalk {
         const int32_t r = t.m0 + row0 + 32 * i + (lane & 31);
         const bool exists = i < mt && r < live;
         bases[i] = exists ? a.base[r] : 0.f;
-        scales[i] = exists ? a.scale[r] * in_units(a, a.g[r]) : 0.f;
+        scales[i] = exists ? a.scale[r] * a.g[r] : 0.f;
       }
     }
 #pragma unroll
