@@ -553,19 +553,24 @@ struct GradWalk {
   __device__ __forceinline__ int32_t rows() const { return kX ? live : a.vocab; }
   __device__ __forceinline__ int64_t m_left(const OutTile& t) const { return rows() - t.m0; }
   __device__ __forceinline__ int64_t n_left(const OutTile& t) const { return a.dim - t.n0; }
+  // k of the tile's part: a part of one k-tile runs two, the second of which reads zeros and not the next part's first
+  __device__ __forceinline__ int32_t part_k(const OutTile& t, int64_t left) const {
+    const int64_t part = (int64_t)t.nk * kBK;
+    return (int32_t)(left < part ? left : part);
+  }
   __device__ __forceinline__ Panel p(const OutTile& t) const {
     const char* dl = static_cast<const char*>(a.dl);
     const int64_t k = (int64_t)t.k0 * kBK;
     if (kX)
-      return Panel{dl + (t.m0 * a.dl_ld + k) * 2, (uint32_t)a.dl_ld * 2u, live - t.m0, (int32_t)(a.dl_ld - k)};
-    return Panel{dl + (k * a.dl_ld + t.m0) * 2, (uint32_t)a.dl_ld * 2u, (int32_t)a.dl_ld - t.m0, (int32_t)(live - k)};
+      return Panel{dl + (t.m0 * a.dl_ld + k) * 2, (uint32_t)a.dl_ld * 2u, live - t.m0, part_k(t, a.dl_ld - k)};
+    return Panel{dl + (k * a.dl_ld + t.m0) * 2, (uint32_t)a.dl_ld * 2u, (int32_t)a.dl_ld - t.m0, part_k(t, live - k)};
   }
   __device__ __forceinline__ Panel q(const OutTile& t) const {
     const int64_t k = (int64_t)t.k0 * kBK;
     const char* from = kX ? static_cast<const char*>(a.w) + k * a.ld * 2
                           : a.twice ? static_cast<const char*>(a.xd) + k * a.ld * 2
                                     : static_cast<const char*>(a.xs) + (a.ch.slot0 + k) * a.ld * 2;
-    return Panel{from + t.n0 * 2ll, (uint32_t)a.ld * 2u, a.ld - t.n0, (int32_t)((kX ? a.vocab : live) - k)};
+    return Panel{from + t.n0 * 2ll, (uint32_t)a.ld * 2u, a.ld - t.n0, part_k(t, (kX ? a.vocab : live) - k)};
   }
   __device__ __forceinline__ int store(Acc& acc, const OutTile& t, int mt, int row0, int col0, MUON_LDS char* buf,
                                        int lane) const {

@@ -1,0 +1,93 @@
+"""The vocabulary operators at the borders of what they take, on inputs that are
+valid but seldom: few rows that count in a long call, logits far from zero, w at any
+address.  Bounds as in test_vocabulary_gpu.py."""
+import math
+
+import pytest
+import torch
+
+import matrix_orthogonalizing_optimizer_muon_amd as M
+import test_vocabulary_gpu as base
+from oracle import vocabulary_oracle as O
+
+pytestmark = pytest.mark.gpu
+
+F, B = torch.float32, torch.bfloat16
+HALF, TINY, ULP = base.HALF, base.TINY, base.ULP
+inf = math.inf
+
+
+def on_gpu(values):
+    return [None if t is None else t.cuda() for t in values]
+
+
+def gradients(dloss, x, w, ids, teacher, tau, lse=None):
+    """(dx, dw) of a loss call with gradients, or of one from lse."""
+    if teacher is None:
+        return M.classifier_loss_grads(dloss, x, w, ids)[2:] if lse is None else \
+            M.classifier_loss_backward(dloss, x, w, ids, lse)
+    kw = {"temperature": tau}
+    return M.distill_loss_grads(dloss, x, w, teacher, ids, **kw)[2:] if lse is None else \
+        M.distill_loss_backward(dloss, x, w, teacher, ids, lse, **kw)
+
+
+def check_gradients(x, w, dloss, ids, teacher, tau, what, twice):
+    """Both forms on these inputs (on the GPU) against the oracle there.  twice: dl is kept to twice its digits."""
+    if teacher is None:
+        at, q = O.target_weights(ids, w.shape[0])
+        arg = torch.zeros(x.shape[0], dtype=torch.float64, device="cuda")
+    else:
+        at, q = O.teacher_weights(teacher, ids, w.shape[0], tau)
+        t = torch.where(at >= 0, teacher.double(), math.nan)
+        arg = torch.nan_to_num((t.nan_to_num(-inf).max(1).values - t.nan_to_num(inf).min(1).values) / tau, posinf=0,
+                               neginf=0)
+    half = HALF[x.dtype]
+    lse = O.loss(x, w, at, q, tau)[1].float()
+    for form in ("both", "backward"):
+        # two roundings to the type where exponentials come first; twice: the rest's, and nine bits of a fraction
+        rounding = half * half + 2.0 ** -10 if twice else half * (1 + half) * (2 if form == "both" else 1)
+        bounds = base.bounds_of(x, w, dloss, at, q, arg, tau, rounding)[2:]
+        given = lse if form == "backward" else None
+        base.poison(tuple(x.shape), tuple(w.shape))
+        got, want = gradients(dloss, x, w, ids, teacher, tau, given), O.grads(dloss, x, w, at, q, tau, given)
+        for name, g, v, b in zip(("dx", "dw"), got, want, bounds):
+            base.close(g, v, b + half * (v.abs() + b) + TINY[x.dtype], f"{what}: {form} {name}")
+
+
+# ------------------------------------------------ few rows count in a long call
+
+def few_live(tokens, vocab, dim, live, where, dtype, k, seed):
+    """Inputs of which `live` rows count: spread over the call, or its last ones."""
+    x, w, dloss, ids, teacher = base.inputs(tokens, vocab, dim, dtype, k, seed, absent=0.0)
+    keep = torch.randperm(tokens, generator=base.gen(seed))[:live] if where == "spread" else \
+        torch.arange(tokens - live, tokens)
+    dead = torch.ones(tokens, dtype=torch.bool)
+    dead[keep] = False
+    ids[dead] = -1
+    return on_gpu((x, w, dloss, ids, teacher))
+
+
+@pytest.mark.parametrize("where", ["spread", "last"])
+@pytest.mark.parametrize("k,tau", [(0, 1.0), (3, 2.0)])
+@pytest.mark.parametrize("dtype", [B, F], ids=str)
+@pytest.mark.parametrize("tokens,vocab,dim,live", [
+    (8192, 1000, 256, 820), (2048, 4000, 256, 200), (1024, 1000, 256, 65), (1024, 1000, 256, 100),
+    (1024, 1000, 256, 128), (1024, 1000, 256, 129), (8192, 2048, 1024, 500), (20000, 300, 96, 1), (20000, 300, 96, 64),
+    (20000, 300, 96, 65), (20000, 300, 96, 128), (20000, 300, 96, 200), (20000, 300, 96, 513), (20000, 300, 96, 2240),
+    (20000, 300, 96, 2241), (8193, 40, 8, 900)])
+def test_few_rows_of_many_count(tokens, vocab, dim, live, dtype, k, tau, where):
+    """dw's sum is cut into parts by the rows of the call, of which those that count may leave a part one k-tile
+    or none."""
+    x, w, dloss, ids, teacher = few_live(tokens, vocab, dim, live, where, dtype, k, tokens + live)
+    check_gradients(x, w, dloss, ids, teacher, tau, where, twice=False)
+
+
+def test_a_short_last_chunk():
+    """32768 rows of this vocabulary are a chunk, and a chunk's dw two parts; the last chunk has two k-tiles."""
+    x, w, dloss, ids, _ = on_gpu(base.inputs(32768 + 100, 32768, 64, B, 0, 5, absent=0.0))
+    at, q = O.target_weights(ids, 32768)
+    _, _, dx, dw = M.classifier_loss_grads(dloss, x, w, ids)
+    arg = torch.zeros(x.shape[0], dtype=torch.float64, device="cuda")
+    bound = base.bounds_of(x, w, dloss, at, q, arg, 1.0, HALF[B] * (1 + HALF[B]) * 2)[2:]
+    for name, g, v, b in zip(("dx", "dw"), (dx, dw), O.grads(dloss, x, w, at, q), bound):
+        base.close(g, v, b + HALF[B] * (v.abs() + b) + TINY[B], name)
