@@ -396,10 +396,11 @@ __global__ __launch_bounds__(256) void k_rescale(LossArgs a, JoinArgs j, const T
         v[u][i] = i < cnt ? __builtin_amdgcn_exp2f(exponent(a, v[u][i], base, T())) * scale * g : 0.f;
     } else {
       load_exps(exps + s * a.dl_ld + c, cnt, v[u]);
-      const float n = cnt ? a.stats[2 * ((int64_t)(c / Slab<T>::kCols) * a.ch.size + s)] : 0.f;
+      // past the vocabulary: zeros by a finite factor, whatever the row's base (NaN where the row's scale is)
+      const float n = cnt ? a.stats[2 * ((int64_t)(c / Slab<T>::kCols) * a.ch.size + s)] : base;
       const float by = __builtin_amdgcn_exp2f(n - base) * (scale * g);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[u][i] *= by;   // past the vocabulary: 0, or NaN where the row's are
+      for (int i = 0; i < 8; ++i) v[u][i] *= by;
     }
   }
   for (int32_t j0 = 0; j0 < a.kp; j0 += 64) {

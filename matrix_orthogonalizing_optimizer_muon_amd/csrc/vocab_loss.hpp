@@ -91,9 +91,10 @@ __device__ __forceinline__ float exponent(const LossArgs& a, float l, float n, f
   return fmaf(l, a.to_log2_low, fmaf(l, a.to_log2, -n));
 }
 __device__ __forceinline__ float exponent(const LossArgs& a, float l, float n, bf16_t) { return fmaf(l, a.to_log2, -n); }
-// n of a largest logit (0 for one of -inf).
+// n of a largest logit.  Where all are -inf, and exponentials 0, one below any other, so that 2^(n - a row's) is 0 too
+// and not infinite in a row far below zero.
 __device__ __forceinline__ float whole_exponent(const LossArgs& a, float top) {
-  return top == -INFINITY ? 0.f : ceilf(top * a.to_log2);
+  return top == -INFINITY ? -0x1p100f : ceilf(top * a.to_log2);
 }
 
 // Joins two sums of 2^(exponent - n) with their n; a sum of zero (exponents of -inf

@@ -91,3 +91,37 @@ def test_a_short_last_chunk():
     bound = base.bounds_of(x, w, dloss, at, q, arg, 1.0, HALF[B] * (1 + HALF[B]) * 2)[2:]
     for name, g, v, b in zip(("dx", "dw"), (dx, dw), O.grads(dloss, x, w, at, q), bound):
         base.close(g, v, b + HALF[B] * (v.abs() + b) + TINY[B], name)
+
+
+# ------------------------------------------------------------ logits far from zero
+
+@pytest.mark.parametrize("k,tau", [(0, 1.0), (5, 2.0)])
+@pytest.mark.parametrize("dtype", [B, F], ids=str)
+@pytest.mark.parametrize("tokens,vocab", [(20, 5001), (100, 6001), (300, 1000), (300, 2050), (700, 129)])
+@pytest.mark.parametrize("shift", [-700.0, 700.0])
+def test_all_logits_far_from_zero(tokens, vocab, dtype, shift, k, tau):
+    """exp of a whole row's logits under- or overflows; a vocabulary that ends inside a slab."""
+    dim = 64
+    x, w, dloss, ids, teacher = base.inputs(tokens, vocab, dim, dtype, k, tokens + vocab)
+    x = (1 + 0.1 * x.float()).to(dtype)
+    w = (w.float() + shift / dim).to(dtype)
+    check_gradients(*on_gpu((x, w, dloss, ids, teacher)), tau, f"shift {shift}", twice=dtype == B and tokens <= 128)
+
+
+@pytest.mark.parametrize("dtype", [B, F], ids=str)
+@pytest.mark.parametrize("tokens,vocab", [(20, 5001), (100, 6001), (300, 2050)])
+def test_a_slab_of_logits_of_minus_infinity(tokens, vocab, dtype):
+    """Columns whose logits overflow to -inf are those of probability zero, as where they are merely large."""
+    dim = 64
+    x, w, dloss, ids, _ = base.inputs(tokens, vocab, dim, dtype, 0, tokens)
+    w = (w.float() - 700.0 / dim).to(dtype)
+    x = (1 + 0.1 * x.float()).to(dtype)
+    w[:, 0] = 0
+    x[:, 0] = 2.0 ** 66
+    ids[(ids >= 64) & (ids < 192)] = 3
+    got = []
+    for size in (2.0 ** 40, 2.0 ** 66):     # logits of -2^106, and -2^132
+        w[64:192, 0] = -size
+        got.append(M.classifier_loss_grads(*on_gpu((dloss, x, w, ids))))
+    assert all(bool(t.isfinite().all()) for t in got[0])
+    assert all(torch.equal(a, b) for a, b in zip(*got))
