@@ -92,9 +92,13 @@ __device__ __forceinline__ float exponent(const LossArgs& a, float l, float n, f
 }
 __device__ __forceinline__ float exponent(const LossArgs& a, float l, float n, bf16_t) { return fmaf(l, a.to_log2, -n); }
 // n of a largest logit.  Where all are -inf, and exponentials 0, one below any other, so that 2^(n - a row's) is 0 too
-// and not infinite in a row far below zero.
+// and not infinite in a row far below zero.  From 2^23 on the product is rounded to a whole number, which can lie below
+// the exponent, by one and more from 2^24 on: then the fp32 above it, since pack_exps has room for less than 2.
 __device__ __forceinline__ float whole_exponent(const LossArgs& a, float top) {
-  return top == -INFINITY ? -0x1p100f : ceilf(top * a.to_log2);
+  if (top == -INFINITY) return -0x1p100f;
+  const float n = ceilf(top * a.to_log2);
+  if (fabsf(n) < 0x1p23f || !(fmaf(top, a.to_log2, -n) > 0.f)) return n;
+  return __int_as_float(__float_as_int(n) + (n > 0.f ? 1 : -1));
 }
 
 // Joins two sums of 2^(exponent - n) with their n; a sum of zero (exponents of -inf
@@ -161,7 +165,7 @@ struct TeacherRow {
 };
 
 // 2^(exponent - n) of a slab's n, between the first product and k_rescale.
-// In 16 bits: no sign and seven bits of the exponent, which values up to 1 do
+// In 16 bits: no sign and seven bits of the exponent, which values below 2 do
 // without the rest of, leave nine of the fraction, so that this rounding (2^-10 at
 // the most) hardly adds to that of the gradient in bf16 (2^-8): a row's sum of dw
 // off by 1.03 of what one rounding gives, where two to bf16 give 1.4.  A NaN comes

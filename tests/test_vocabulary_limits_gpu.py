@@ -125,3 +125,34 @@ def test_a_slab_of_logits_of_minus_infinity(tokens, vocab, dtype):
         got.append(M.classifier_loss_grads(*on_gpu((dloss, x, w, ids))))
     assert all(bool(t.isfinite().all()) for t in got[0])
     assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+@pytest.mark.parametrize("tau", [1.0, 2.0 ** -20])
+@pytest.mark.parametrize("dtype", [B, F], ids=str)
+@pytest.mark.parametrize("tokens,vocab", [(20, 5001), (100, 6001), (300, 2050)])
+def test_exponents_of_more_than_24_bits(tokens, vocab, dtype, tau):
+    """Logits over the temperature of 2^25, where whole numbers of fp32 lie 4 apart: one entry has all of its row's
+    probability.  It and the target's entry of dl are dloss, rounded twice to bf16 at the most."""
+    g = base.gen(tokens)
+    x, w = torch.zeros(tokens, 8), torch.randn(vocab, 8, generator=g)
+    x[:, 0] = (4096 + 32 * torch.randint(0, 128, (tokens,), generator=g)) * tau
+    w[:, 0] = 4096.0 + 32 * torch.randint(0, 31, (vocab,), generator=g)
+    w[vocab // 3, 0] = 4096.0 + 32 * 32
+    x, w = x.to(dtype), w.to(dtype)
+    ids = torch.randint(0, vocab, (tokens, 1), generator=g)
+    dloss, teacher = torch.randn(tokens, generator=g), torch.zeros(tokens, 1)
+    x, w, ids, dloss, teacher = on_gpu((x, w, ids, dloss, teacher))
+    loss, lse, dx, dw = M.distill_loss_grads(dloss, x, w, teacher, ids, temperature=tau)
+    at, q = O.target_weights(ids[:, 0], vocab)
+    z = x.double() @ w.double().t() / tau
+    want_loss, want_lse = O.loss(x, w, at, q, tau)
+    size = z.abs().max(1).values * 16 * ULP
+    base.close(lse, want_lse, size, "lse")
+    base.close(loss, want_loss, size * tau * tau + want_loss * 16 * ULP, "loss")
+    want = O.grads(dloss, x, w, at, q, tau)
+    # entries of dl, and what a probability and a weight of one are off by where they cancel
+    soft = torch.zeros_like(z).scatter_add_(1, at.clamp_min(0), q)
+    dl = O.logits_grad(dloss, x, w, at, q, tau).abs() * (2 * HALF[dtype] + 2.0 ** -10 if dtype == B else 32 * ULP)
+    dl += 16 * ULP * tau * dloss.double().abs()[:, None] * (torch.exp(z - want_lse[:, None]) + soft)
+    for got, v, s in ((dx, want[0], dl @ w.double().abs()), (dw, want[1], dl.t() @ x.double().abs())):
+        base.close(got, v, s + (HALF[dtype] + 8 * ULP) * (v.abs() + s) + TINY[dtype], "gradient")
