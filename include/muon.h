@@ -592,7 +592,7 @@ int muon_gated_backward(const void* dh, const void* gu, const void* q, const uin
  * targets, a teacher's ids) are signed whole numbers of index_bytes, 4 or 8; one
  * outside [0, vocab) names nothing and is never followed.  Two calls that share a
  * workspace must be ordered.  Limits (EUNSUPPORTED): tokens, vocab and
- * tokens k < 2^31, dim < 2^24, k <= 256.
+ * tokens k < 2^31, dim < 2^24, k <= 256, 2^-63 <= temperature <= 2^63.
  */
 
 /*

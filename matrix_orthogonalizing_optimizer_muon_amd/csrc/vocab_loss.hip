@@ -721,6 +721,9 @@ int check_loss(const Call& c) {
     if (c.k > kMaxTeacher) return fail(MUON_EUNSUPPORTED, "more than 256 teacher entries");
     if (c.tokens * c.k > kMaxCount) return fail(MUON_EUNSUPPORTED, "2^31 teacher entries or more");
     if (!(c.tau > 0.f && c.tau < INFINITY)) return fail(MUON_EINVAL, "temperature must be positive and finite");
+    // its square, which scales the loss, and its inverse, which scales logits, are normal fp32 numbers
+    if (!(c.tau >= 0x1p-63f && c.tau <= 0x1p63f))
+      return fail(MUON_EUNSUPPORTED, "temperature must be in [2^-63, 2^63]");
   }
   return MUON_OK;
 }

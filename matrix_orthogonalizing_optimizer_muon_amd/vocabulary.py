@@ -65,6 +65,8 @@ def _teacher(teacher, ids, temperature):
     temperature = float(temperature)
     if not 0 < temperature < float("inf"):
         raise ValueError(f"temperature must be positive and finite, not {temperature}")
+    if not 2.0 ** -63 <= temperature <= 2.0 ** 63:
+        raise ValueError(f"temperature must be in [2^-63, 2^63], not {temperature}")
     return code, temperature
 
 
