@@ -159,8 +159,9 @@ __global__ __launch_bounds__(64 * kRowsWaves) void k_rows(LossArgs a, RowsArgs o
       const float zero[8] = {};
       T* row = xd + twice_row(t < a.tokens ? a.tokens - 1 - (t - before) : t) * a.ld;
       for (int32_t c = lane * 8; c < a.ld; c += 512) {
-        store8(row + c, 8, zero);
-        store8(row + 32 * a.ld + c, 8, zero);
+        const int cnt = a.ld - c < 8 ? a.ld - c : 8;
+        store8(row + c, cnt, zero);
+        store8(row + 32 * (int64_t)a.ld + c, cnt, zero);
       }
     }
     if (t >= a.tokens) return;
@@ -192,12 +193,12 @@ __global__ __launch_bounds__(64 * kRowsWaves) void k_rows(LossArgs a, RowsArgs o
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {   // past dim: zeros
-      const int32_t at = c + 512 * u, left = a.ld - at;
-      if (left > 0) store8(xs + (int64_t)s * a.ld + at, left < 8 ? left : 8, p[u]);
+      const int32_t at = c + 512 * u, left = a.ld - at, cnt = left < 8 ? left : 8;
+      if (left > 0) store8(xs + (int64_t)s * a.ld + at, cnt, p[u]);
       if (left > 0 && COUNT && a.twice) {
         T* row = xd + twice_row(s) * a.ld + at;
-        store8(row, 8, p[u]);
-        store8(row + 32 * a.ld, 8, p[u]);
+        store8(row, cnt, p[u]);
+        store8(row + 32 * (int64_t)a.ld, cnt, p[u]);
       }
     }
   }
@@ -516,7 +517,7 @@ LossSpace loss_space(int dtype, int64_t tokens, int64_t vocab, int64_t dim, int 
   l.slabs = l.few ? few_blocks(dtype, tokens, vocab, dim) : ceil_div(vocab, slab_cols(dtype));
   l.dl_ld = ceil_div(vocab, 64) * 64;
   const bool large = large_sizes(dtype, tokens, vocab, dim);
-  l.twice = grads && large && l.chunk == tokens && tokens <= kTwiceRows;
+  l.twice = grads && dtype == MUON_BF16 && l.chunk == tokens && tokens <= kTwiceRows;
   const int64_t rows = l.twice ? 2 * whole_slots((int32_t)l.chunk) : l.chunk;   // of dl
   l.parts = grads ? product_parts(dtype, rows, vocab, dim, large) : ProductParts{1, 1};
   l.ld = (int32_t)(large ? ceil_div(dim, 8) * 8 : dim);
@@ -625,7 +626,7 @@ int run(const Call& c, const LossSpace& l, char* ws, hipStream_t s) {
   const double to_log2 = 1.4426950408889634 / (double)c.tau;
   a.to_log2 = (float)to_log2;
   a.to_log2_low = (float)(to_log2 - (double)a.to_log2);
-  a.twice = l.twice && large;
+  a.twice = l.twice;
   a.stats = given && (l.few || !a.twice) ? nullptr : reinterpret_cast<float*>(ws + l.stats);
   a.picked = reinterpret_cast<float*>(ws + l.picked);
   a.ld = l.few && !grads ? a.dim : l.ld;
@@ -658,7 +659,7 @@ int run(const Call& c, const LossSpace& l, char* ws, hipStream_t s) {
     a.first = a.last = true;
     return grads ? dw_product(a, c.dtype, s) : MUON_OK;
   }
-  if (grads && large && !a.twice) {
+  if (grads && c.dtype == MUON_BF16 && !a.twice) {
     float* unit = reinterpret_cast<float*>(ws + l.unit);
     hipLaunchKernelGGL(k_unit, dim3(1), dim3(1024), 0, s, a, c.dloss, c.tau, unit,
                        given ? reinterpret_cast<float*>(ws + l.g) : nullptr);

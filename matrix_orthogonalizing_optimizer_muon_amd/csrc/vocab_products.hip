@@ -200,9 +200,11 @@ __global__ __launch_bounds__(256) void k_tile(LossArgs a, int32_t tiles_m, int32
   const int64_t wide = tiles_m - group * 8 < 8 ? tiles_m - group * 8 : 8;
   const int32_t n0 = (int32_t)(off / wide) * G::B;
   const int64_t m0 = (group * 8 + off % wide) * G::B;
-  const int32_t live = live_slots(a.ch);
+  // rows of dl: two a slot where it is kept twice (bf16)
+  const bool twice = sizeof(T) == 2 && PRODUCT != kLogits && a.twice;
+  const int32_t slots = live_slots(a.ch), live = twice ? 2 * whole_slots(slots) : slots;
   const int32_t* rows = a.ch.rows + a.ch.slot0;
-  const T* xs = static_cast<const T*>(a.xs) + a.ch.slot0 * a.ld;
+  const T* xs = twice ? static_cast<const T*>(a.xd) : static_cast<const T*>(a.xs) + a.ch.slot0 * a.ld;
   int64_t m_left;
   int32_t K;
   typename std::conditional<SHORT, Stager32<PT>, Stager<T, PT>>::type sp;
@@ -306,13 +308,29 @@ __global__ __launch_bounds__(256) void k_tile(LossArgs a, int32_t tiles_m, int32
     step(kt, sp, sq, sp1, sq1);
     if (kt + 1 < nk) step(kt + 1, sp1, sq1, sp, sq);
   }
+  if constexpr (sizeof(T) == 2 && PRODUCT != kLogits) {
+    if (a.unit) {
+      const float u = a.unit[1];
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] *= u;
+    }
+    if (PRODUCT == kDx && twice) {   // a slot's two rows are a lane's
+      static_assert(NT == 2, "32 rows, and what rounding left of them");
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[0][j] += acc[1][j];
+    }
+  }
   static_assert(sizeof(lds) >= 4 * 4096, "the waves' rows");
   if (PRODUCT == kLogits && a.kp > 1) __syncthreads();   // other waves' reads of the last k-tile
   // lane l has row l % 32 of a 32 x 32 tile, registers 4 g + 0..3 columns 8 g + 4 (l / 32) + 0..3
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    const int64_t r = m0 + wy * W + 32 * i + (lane & 31);
-    const bool exists = r < m0 + m_left;
+    const bool pair = PRODUCT == kDx && twice;
+    if (pair && i) break;
+    const int64_t r = pair ? (m0 + wy * W) / 2 + (lane & 31) : m0 + wy * W + 32 * i + (lane & 31);
+    const bool exists = r < (pair ? slots : m0 + m_left);
     const int32_t c0 = n0 + wx * W + 4 * (lane >> 5);
     if constexpr (PRODUCT == kLogits) {
       if (n0 + wx * W >= a.vocab) continue;   // uniform over the wave
@@ -758,7 +776,8 @@ int launch_grad(const LossArgs& a, hipStream_t s) {
   if (a.large) {
     hipLaunchKernelGGL((k_grad<PRODUCT>), dim3(kWalkers), dim3(512), 0, s, a);
   } else {
-    const int rc = launch_tile<T, PRODUCT, kStats>(a, m, a.dim, parts, s);
+    const int64_t rows = PRODUCT == kDx && a.twice ? 2 * whole_slots(a.ch.size) : m;
+    const int rc = launch_tile<T, PRODUCT, kStats>(a, rows, a.dim, parts, s);
     if (rc) return rc;
   }
   if (parts >= kManyParts)

@@ -156,3 +156,44 @@ def test_exponents_of_more_than_24_bits(tokens, vocab, dtype, tau):
     dl += 16 * ULP * tau * dloss.double().abs()[:, None] * (torch.exp(z - want_lse[:, None]) + soft)
     for got, v, s in ((dx, want[0], dl @ w.double().abs()), (dw, want[1], dl.t() @ x.double().abs())):
         base.close(got, v, s + (HALF[dtype] + 8 * ULP) * (v.abs() + s) + TINY[dtype], "gradient")
+
+
+# ---------------------------------------------------------------- w at any address
+
+@pytest.mark.parametrize("k,tau", [(0, 1.0), (5, 2.0)])
+@pytest.mark.parametrize("tokens,vocab,dim", [(1, 300, 72), (5, 33, 8), (31, 515, 2104), (64, 777, 1096), (65, 777, 1096),
+                                              (100, 5003, 72), (128, 300, 72), (127, 516, 135)])
+def test_few_rows_keep_their_digits_wherever_w_lies(tokens, vocab, dim, k, tau):
+    x, w, dloss, ids, teacher = on_gpu(base.inputs(tokens, vocab, dim, B, k, tokens + dim))
+    for off in (1, 3, 4):
+        check_gradients(x, base.guarded(w, off), dloss, ids, teacher, tau, f"w {off} elements on", twice=True)
+
+
+@pytest.mark.parametrize("tokens", [1, 50, 100])
+def test_few_rows_keep_their_digits_in_a_vocabulary_of_2_to_the_21(tokens):
+    x, w, dloss, ids, teacher = on_gpu(base.inputs(tokens, (1 << 21) + 5, 9, B, 3, tokens, absent=0.0))
+    check_gradients(x, w, dloss, ids, teacher, 1.5, "vocabulary of 2^21 and more", twice=True)
+
+
+@pytest.mark.parametrize("form", ["both", "backward"])
+@pytest.mark.parametrize("tokens,vocab", [(300, 1024), (500, 1000), (300, (1 << 21) + 64)])
+def test_equal_dloss_is_not_rounded_wherever_w_lies(tokens, vocab, form):
+    """test_equal_dloss_is_not_rounded's w, off its alignment, in a small vocabulary (whose logits are kept), and in one
+    that the large tiles do not address: others' entries of dl are dloss / vocab, rounded as a power of two (none) or
+    as 1 / 1000 is (by 2^-9 at the most)."""
+    d, g = 40, 1.0036 / 256
+    x = torch.randn(tokens, d, generator=base.gen(1)).bfloat16().cuda()
+    w = base.guarded(torch.zeros(vocab, d).bfloat16())
+    targets = torch.randperm(vocab, generator=base.gen(2))[:tokens].cuda()
+    dloss = torch.full((tokens,), g).cuda()
+    lse = torch.full((tokens,), math.log(vocab)).cuda() if form == "backward" else None
+    dw = gradients(dloss, x, w, targets, None, 1.0, lse)[1]
+    at, q = O.target_weights(targets, vocab)
+    want = O.grads(dloss, x, w, at, q, 1.0, lse)[1]
+    rows = x.double().abs()
+    own = torch.zeros(vocab, d, dtype=torch.float64, device="cuda").index_add_(0, targets, rows * g)
+    p = 1 / vocab
+    near = 0.0 if math.log2(vocab).is_integer() else abs(p / float(torch.tensor(p).bfloat16()) - 1) + 2.0 ** -10
+    # a target's entry, 1 - p, may be off by its distance to one or half a step; lse of 14 by half a step, 2^-21
+    slack = max(2.0 ** -10, p) * own + (tokens + 32) * ULP * own + (near + (tokens + 64) * ULP) * rows.sum(0) * g * p
+    base.close(dw, want, slack + HALF[B] * (want.abs() + slack), "dw")
