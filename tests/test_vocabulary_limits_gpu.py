@@ -197,3 +197,58 @@ def test_equal_dloss_is_not_rounded_wherever_w_lies(tokens, vocab, form):
     # a target's entry, 1 - p, may be off by its distance to one or half a step; lse of 14 by half a step, 2^-21
     slack = max(2.0 ** -10, p) * own + (tokens + 32) * ULP * own + (near + (tokens + 64) * ULP) * rows.sum(0) * g * p
     base.close(dw, want, slack + HALF[B] * (want.abs() + slack), "dw")
+
+
+# ----------------------------------------------------- operands that 31 bits do not address
+
+@pytest.mark.parametrize("dtype", [B, F], ids=str)
+@pytest.mark.parametrize("tokens,vocab,dim", [
+    (3, 300, (1 << 21) + 9), (1000, 600, (1 << 21) + 8), (20, (1 << 21) - 8, 1032), (70, (1 << 21) - 8, 1032),
+    (70, (1 << 21) + 3, 1032), ((1 << 20) + 70, 40, 2056)])
+def test_long_operands(tokens, vocab, dim, dtype):
+    """x or w of 2^31 elements and more, and widths and vocabularies past 2^21.  64 columns are not zero, the first and
+    last among them: sums over the others are exact, so that the bounds are those of 64 columns."""
+    x, w, dloss, ids, _ = base.inputs(tokens, vocab, 64, dtype, 0, 7, absent=0.02)
+    x, w, dloss, ids = on_gpu((x, w, dloss, ids))
+    cols = torch.cat([torch.tensor([0, dim - 1]), 1 + torch.randperm(dim - 2, generator=base.gen(8))[:62]]).cuda()
+    at, q = O.target_weights(ids, vocab)
+    arg = torch.zeros(tokens, dtype=torch.float64, device="cuda")
+    half = HALF[dtype]
+    rounding = half * half + 2.0 ** -10 if dtype == B and tokens <= 128 else half * (1 + half) * 2
+    bounds = base.bounds_of(x, w, dloss, at, q, arg, 1.0, rounding)
+    want = (*O.loss(x, w, at, q), *O.grads(dloss, x, w, at, q))
+    wide = [torch.zeros(t.shape[0], dim, dtype=dtype, device="cuda") for t in (x, w)]
+    for t, narrow in zip(wide, (x, w)):
+        t[:, cols] = narrow
+    loss, lse = M.classifier_loss(*wide, ids)
+    got = M.classifier_loss_grads(dloss, *wide, ids)
+    back = M.classifier_loss_backward(dloss, *wide, ids, want[1].float())
+    from_lse = O.grads(dloss, x, w, at, q, 1.0, want[1].float())
+    for values, name in (((loss, lse), "loss"), (got[:2], "loss with gradients")):
+        for g, v, b in zip(values, want, bounds):
+            base.close(g, v, b, name)
+    for pair, wanted in ((got[2:], want[2:]), (back, from_lse)):
+        for g, v, b, name in zip(pair, wanted, bounds[2:], ("dx", "dw")):
+            base.close(g[:, cols], v, b + half * (v.abs() + b) + TINY[dtype], name)
+            assert int(torch.count_nonzero(g)) == int(torch.count_nonzero(g[:, cols])), f"{name}: other columns"
+
+
+@pytest.mark.parametrize("dtype", [B, F], ids=str)
+def test_embedding_of_a_long_table(dtype):
+    """Rows past 2^31 elements of the table, of its gradient and of the outputs; whole numbers, exactly."""
+    vocab, dim, n = (1 << 21) + 3, 1032, 3000
+    t = torch.cat([torch.tensor([vocab - 1, vocab, 0, -1]), torch.randint(vocab - 100, vocab, (n - 4,),
+                                                                        generator=base.gen(1))]).cuda()
+    table = torch.zeros(vocab, dim, dtype=dtype, device="cuda")
+    table[-100:] = torch.randint(-8, 9, (100, dim), generator=base.gen(2)).to(dtype).cuda()
+    out = M.embed(t, table)
+    named = (t >= 0) & (t < vocab)
+    assert torch.equal(out, torch.where(named[:, None], table[torch.where(named, t, 0)], 0.0))
+    dout = torch.randint(-2, 3, (n, dim), generator=base.gen(3)).to(dtype).cuda()
+    dtable = M.embed_backward(dout, t, vocab)
+    low = vocab - 100
+    want = torch.zeros(100, dim, dtype=torch.float64, device="cuda")
+    here = (t >= low) & (t < vocab)
+    want.index_add_(0, t[here] - low, dout[here].double())
+    assert torch.equal(dtable[low:].double(), want)
+    assert torch.equal(dtable[0].double(), dout[2].double()) and not dtable[1:low].any()
