@@ -70,7 +70,7 @@ __device__ __forceinline__ void take_logits(const LossArgs& a, const I* targets,
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (i < left) top = fmaxf(top, acc[b][i]);
-    const float m = whole_exponent(a, top);
+    const float m = whole_exponent<T>(a, top);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (i < left) add += __builtin_amdgcn_exp2f(exponent(a, acc[b][i], m, T()));

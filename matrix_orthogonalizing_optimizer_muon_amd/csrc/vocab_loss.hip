@@ -18,6 +18,8 @@
 // loss's own pass it is rounded before, too, to 16 bits of its own: pack_exps).
 #include <hip/hip_runtime.h>
 
+#include <math.h>
+
 #include "vocab_loss.hpp"
 
 namespace muon {
@@ -625,7 +627,10 @@ int run(const Call& c, const LossSpace& l, char* ws, hipStream_t s) {
   a.dim = (int32_t)c.dim;
   const double to_log2 = 1.4426950408889634 / (double)c.tau;
   a.to_log2 = (float)to_log2;
-  a.to_log2_low = (float)(to_log2 - (double)a.to_log2);
+  if (sizeof(T) == 4) {   // from below, so that the low part is positive: a logit of -inf times it is -inf
+    if ((double)a.to_log2 > to_log2) a.to_log2 = nextafterf(a.to_log2, 0.f);
+    a.to_log2_low = fmaxf((float)(to_log2 - (double)a.to_log2), 0x1p-126f);
+  }
   a.twice = l.twice;
   a.stats = given && (l.few || !a.twice) ? nullptr : reinterpret_cast<float*>(ws + l.stats);
   a.picked = reinterpret_cast<float*>(ws + l.picked);

@@ -36,10 +36,10 @@ struct LossArgs {
   int64_t tokens;
   int32_t vocab, dim;
   int32_t ld;              // dim, or, for the large tiles, dim in whole 16-byte chunks, filled up with zeros
-  bool large;              // the large tiles take the products
+  bool large;              // the large tiles take the products (large_sizes, and w on 16 bytes where it is not copied)
   bool chunked;            // rows of dx and dw are whole chunks on borders of 16 bytes
   int64_t dl_ld;           // elements of a row of dl: vocab in whole slabs of 64
-  // exp(l / temperature) = 2^(l (to_log2 + to_log2_low)): log2(e) / temperature in two parts
+  // exp(l / temperature) = 2^(l (to_log2 + to_log2_low)): log2(e) / temperature in two parts (bf16: the first alone)
   float to_log2, to_log2_low;
   // logits: exponents of two come as a whole number n and a sum of 2^(l to_log2 - n), so that differences of
   // exponents are exact and nothing is rounded at a logit's size
@@ -91,14 +91,23 @@ __device__ __forceinline__ float exponent(const LossArgs& a, float l, float n, f
   return fmaf(l, a.to_log2_low, fmaf(l, a.to_log2, -n));
 }
 __device__ __forceinline__ float exponent(const LossArgs& a, float l, float n, bf16_t) { return fmaf(l, a.to_log2, -n); }
-// n of a largest logit.  Where all are -inf, and exponentials 0, one below any other, so that 2^(n - a row's) is 0 too
+// n of a largest logit.  Where all are -inf, and exponentials 0, the lowest number, so that 2^(n - a row's) is 0 too
 // and not infinite in a row far below zero.  From 2^23 on the product is rounded to a whole number, which can lie below
-// the exponent, by one and more from 2^24 on: then the fp32 above it, since pack_exps has room for less than 2.
+// the exponent by half the distance of fp32 numbers, and in fp32 the factor's low part adds as much: then n is a number
+// that does not, since pack_exps has room for less than 2, and 2^ that distance can be infinite.
+template <class T>
 __device__ __forceinline__ float whole_exponent(const LossArgs& a, float top) {
-  if (top == -INFINITY) return -0x1p100f;
-  const float n = ceilf(top * a.to_log2);
-  if (fabsf(n) < 0x1p23f || !(fmaf(top, a.to_log2, -n) > 0.f)) return n;
-  return __int_as_float(__float_as_int(n) + (n > 0.f ? 1 : -1));
+  constexpr float kLowest = -3.402823466e38f;
+  if (top == -INFINITY) return kLowest;
+  float n = fmaxf(ceilf(top * a.to_log2), kLowest);
+  if (fabsf(n) >= 0x1p23f) {
+    const float over = exponent(a, top, n, T());
+    if (over > 0.f) {
+      n += over;
+      if (exponent(a, top, n, T()) > 0.f) n = __int_as_float(__float_as_int(n) + (n > 0.f ? 1 : -1));
+    }
+  }
+  return n;
 }
 
 // Joins two sums of 2^(exponent - n) with their n; a sum of zero (exponents of -inf
@@ -201,7 +210,7 @@ ProductParts product_parts(int dtype, int64_t tokens, int64_t vocab, int64_t dim
 // Up to so many rows of bf16 dl are kept twice (LossArgs::twice).  The gradients of
 // a few rows are sums of few large entries of dl, whose rounding to bf16 does not
 // average out: off by up to 2^-8, over the 2^-9 or so that rounding the result gives.
-// Both rows fit one tile's 256, so that the products pass over w and dw once either way,
+// Both rows fit one tile's 256 (or two of 128), so that the products pass over w and dw once either way,
 // and dx is added up in the tile.
 constexpr int64_t kTwiceRows = 128;
 

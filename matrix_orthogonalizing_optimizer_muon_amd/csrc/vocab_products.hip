@@ -357,7 +357,7 @@ __global__ __launch_bounds__(256) void k_tile(LossArgs a, int32_t tiles_m, int32
 #pragma unroll
           for (int v = 0; v < 16; ++v)
             if (c0 + 32 * j + 8 * (v / 4) + v % 4 < a.vocab) top = fmaxf(top, e[j][v]);
-        const float n = whole_exponent(a, fmaxf(top, __shfl_xor(top, 32, 64)));
+        const float n = whole_exponent<T>(a, fmaxf(top, __shfl_xor(top, 32, 64)));
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -506,7 +506,7 @@ struct LogitsWalk {
         for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int v = 0; v < 16; ++v) top = fmaxf(top, acc[i][j][v]);
-        n = whole_exponent(a, fmaxf(top, other_half(top)));
+        n = whole_exponent<bf16_t>(a, fmaxf(top, other_half(top)));
       } else {
         n = bases[i];
         by = scales[i];

@@ -84,7 +84,7 @@ struct ColPanel {
   }
   typedef u32x4 At;
   __device__ __forceinline__ At at(int kt) const {
-    // the last row ends with its columns, not with ld: what lies behind it is another's memory
+    // k that does not exist lies past the range; in the last row that does, columns past extent have no address (init)
     const int64_t left = (k - (int64_t)kt * kBK) * (int64_t)ld;
     return copy_rsrc(base + (int64_t)kt * kBK * ld, left <= 0 ? 0u : left < kRange ? (uint32_t)left : kRange);
   }

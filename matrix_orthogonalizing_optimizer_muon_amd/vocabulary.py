@@ -11,7 +11,8 @@ classifier.
 
 Tokens, targets and ids are int32 or int64; one outside [0, vocab) names
 nothing: its embedding is zeros, and a row whose target (or whole teacher)
-names nothing has loss and lse 0, gradient zero, and costs nothing.
+names nothing has loss and lse 0, gradient zero, and costs nothing (but in a
+small call without gradients, where all rows are computed).
 
 Tensors, streams and autograd are treated as the expert-layer operators treat
 them (experts.py): contiguous float32 or bfloat16 tensors on one GPU, outputs

@@ -158,6 +158,27 @@ def test_exponents_of_more_than_24_bits(tokens, vocab, dtype, tau):
         base.close(got, v, s + (HALF[dtype] + 8 * ULP) * (v.abs() + s) + TINY[dtype], "gradient")
 
 
+@pytest.mark.parametrize("tau", [1.0, 0.7, 2.3])
+@pytest.mark.parametrize("dtype", [B, F], ids=str)
+@pytest.mark.parametrize("tokens,vocab", [(20, 5001), (100, 6001), (300, 2050)])
+def test_slabs_of_logits_far_below_the_others(tokens, vocab, dtype, tau):
+    """Columns of probability zero are that at whatever size of their logits, from -2^17 down to fp32's lowest and below
+    it: nothing else moves by a bit."""
+    dim, g = 64, base.gen(tokens)
+    x, w, dloss, ids, teacher = base.inputs(tokens, vocab, dim, dtype, 3, tokens)
+    w[:, 0] = 0
+    x[:, 0] = 2.0 ** 66 * (1 + torch.rand(tokens, generator=g)).to(dtype)
+    ids[(ids >= 64) & (ids < 256)] = 3
+    size = (1 + torch.rand(192, generator=g)).to(dtype)
+    got = []
+    for e in (-49, -40, -31, -20, 0, 30, 60, 61, 62):
+        w[64:256, 0] = -(size.float() * 2.0 ** e).to(dtype)
+        args = on_gpu((dloss, x, w, teacher, ids))
+        got.append((*M.distill_loss_grads(*args, temperature=tau), *M.distill_loss(*args[1:], temperature=tau)))
+        assert all(bool(t.isfinite().all()) for t in got[-1]), f"2^{e}"
+        assert all(torch.equal(a, b) for a, b in zip(got[0], got[-1])), f"2^{e}"
+
+
 # ---------------------------------------------------------------- w at any address
 
 @pytest.mark.parametrize("k,tau", [(0, 1.0), (5, 2.0)])
