@@ -592,7 +592,8 @@ int muon_gated_backward(const void* dh, const void* gu, const void* q, const uin
  * targets, a teacher's ids) are signed whole numbers of index_bytes, 4 or 8; one
  * outside [0, vocab) names nothing and is never followed.  Two calls that share a
  * workspace must be ordered.  Limits (EUNSUPPORTED): tokens, vocab and
- * tokens k < 2^31, dim < 2^24, k <= 256, 2^-63 <= temperature <= 2^63.
+ * tokens k < 2^31, dim < 2^24, k <= 256, 2^-63 <= temperature <= 2^63.  A row whose
+ * largest logit over temperature is 2^29 or more in size has no defined loss.
  */
 
 /*
@@ -611,16 +612,20 @@ int muon_embed_backward(const void* dout, const void* tokens, int index_bytes, i
                         uint64_t workspace_bytes, void* stream);
 
 /*
- * Cross entropy of the logits l = x w^T, which are in memory for up to 128 rows alone:
+ * Cross entropy of the logits l = x w^T, which are in memory for small calls alone (up to
+ * 64 rows, or rows, in whole 16s, times vocab up to 2^19):
  *   lse[t] = log sum_v exp(l_tv),  loss[t] = lse[t] - l_t,targets[t]
  * A target that names nothing takes its row out: loss and lse 0, its gradient
- * zeros, and its x reaches nothing.  Work goes with the rows that are left.
+ * zeros, and its x reaches nothing.  Work goes with the rows that are left (in a small
+ * call without gradients, with all rows).
  *   muon_classifier_loss           loss and lse (fp32, tokens)
  *   muon_classifier_loss_grads     these and, for the loss's gradient dloss (fp32,
  *                                  tokens), dx (tokens x dim) and dw (vocab x dim):
  *                                  dl_tv = dloss[t] (exp(l_tv - lse[t]) - [v = targets[t]]),
- *                                  dx = dl w, dw = dl^T x, with dl rounded to dtype (bf16: up to
- *                                  128 rows to 16 digits, beyond in units of the largest dloss)
+ *                                  dx = dl w, dw = dl^T x, with dl rounded to dtype (bf16: to 16
+ *                                  digits up to 64 rows, or 128 of up to 2^23 entries, beyond in
+ *                                  units of the largest dloss; where lse is not given,
+ *                                  exponentials to 10 digits before that)
  *   muon_classifier_loss_backward  dx and dw from the lse that a loss call gave
  *                                  (computes the logits again)
  * muon_classifier_loss_workspace: bytes that a call needs; gradients 0: the loss
