@@ -220,6 +220,35 @@ def test_equal_dloss_is_not_rounded_wherever_w_lies(tokens, vocab, form):
     base.close(dw, want, slack + HALF[B] * (want.abs() + slack), "dw")
 
 
+@pytest.mark.parametrize("tokens,vocab", [(8192 + 321, 131072), (600, (1 << 21) + 5)])
+def test_chunks_wherever_w_lies(tokens, vocab):
+    """One unit for the dloss of all chunks, whose dw goes on from one to the next."""
+    x, w, dloss, ids, _ = on_gpu(base.inputs(tokens, vocab, 16, B, 0, 23, absent=0.05))
+    dloss[:400] *= 2.0 ** -8
+    check_gradients(x, base.guarded(w), dloss, ids, None, 1.0, "chunks", twice=False)
+
+
+@pytest.mark.parametrize("sizes", [(300, 500, 128), (400, 2100, 136), (20, 500, 64), (100, 5000, 72)])
+def test_a_step_in_a_graph_with_w_off_alignment(sizes):
+    """Captured once, replayed on other values and numbers of rows that count, with eager work between."""
+    args = list(base.step_inputs(2, B, *sizes))
+    args[3] = base.guarded(args[3])
+    base.model_step(*args)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = base.model_step(*args)
+    for seed in (3, 4, 5):
+        for a, b in zip(args, base.step_inputs(seed, B, *sizes)):
+            a.copy_(b)
+        args[1][seed * 3:] = -1          # targets: few are left
+        want = base.model_step(*args)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
 # ----------------------------------------------------- operands that 31 bits do not address
 
 @pytest.mark.parametrize("dtype", [B, F], ids=str)
